@@ -1,7 +1,8 @@
 /*
  * fp4gemm.h -- C ABI of the BF16 / FP16 x FP4 block-scaled GEMM for AMD MI355X (gfx950),
  * with its grouped mixture-of-experts variant, the offline repack and the
- * offline quantizer.
+ * offline quantizer, and of a key/value cache in the same FP4 formats with the
+ * attention that reads it.
  *
  *   Y[m][N] = A[m][K] . dequant(W)[N][K]^T,   dequant(W)[n][k] = e2m1(code[n][k]) * scale[n][k / G]
  *
@@ -36,7 +37,7 @@
  *     leaves every output untouched.
  *   - The caller owns every buffer.  The library never allocates, frees or
  *     synchronizes in any device entry (fp4_gemm*, fp4_moe_gemm,
- *     fp4_quantize, fp4_dequant*): they only queue kernels on `stream`.
+ *     fp4_quantize, fp4_dequant*, fp4_kv_append, fp4_kv_read, fp4_attention): they only queue kernels on `stream`.
  *   - "device" pointers must be HIP device memory on the current device;
  *     "host" pointers must be ordinary host memory.
  *   - Functions are reentrant and thread-safe; the only global state is a
@@ -295,6 +296,117 @@ int fp4_gemm_native(const void* A, const void* wq, const void* sq, void* C, int6
 int fp4_moe_gemm(const void* A, const void* wq, const void* sq, const int32_t* sorted_ids,
                  const int32_t* expert_offsets, const float* topk_weights, void* C, int64_t a_rows, int64_t a_div,
                  int64_t out_rows, int64_t P, int64_t E, int64_t N, int64_t K, int format, void* stream);
+
+/* ---- FP4 key/value cache and attention over it ------------------------------
+ * A paged key/value cache of one attention layer held in FP4: every row of
+ * head_dim elements (one token, one KV head) is quantized by the
+ * fp4_quantize rule in blocks of G elements, with one per-tensor scale for
+ * the keys and one for the values (value = alpha * e2m1(code) * scale).
+ *
+ * A page holds page_size consecutive tokens of one sequence, for all KV
+ * heads; a slot is page * page_size + (position mod page_size).  Cache layout
+ * (every byte belongs to one token and head): tiles of 32 tokens in the order
+ * [page][KV head][page_size / 32], each of 32 D + 64 D / G bytes (D =
+ * head_dim): key codes (16 D bytes), value codes (16 D), key scales
+ * (32 D / G), value scales (32 D / G).  With t = position mod 32, u = t / 16,
+ * r = t mod 16, j = r / 4, i = t mod 4, byte offsets of the code pair of
+ * elements d, d + 1 (d even; element d in bits 3..0) and of the scale of
+ * block g in their sections:
+ *   D = 64       keys   (d/16*16 + r)*16 + u*8 + d%16/2
+ *                values (16 j + d/4)*16 + u*8 + i*2 + d%4/2
+ *                key scales (g*16 + r)*2 + u
+ *   D = 128, 256 keys   (d/128*2 + u)*1024 + (d%128/32*16 + r)*16 + d%32/2
+ *                values (d/128*2 + u)*1024 + (16 j + d%128/8)*16 + i*4 + d%8/2
+ *                key scales, with P = 32 / G, C = D / 128:
+ *                (g%(4P)/P*16 + r)*(2 C P) + g/(4P)*2P + u*P + g%P
+ *   all D        value scales (g*4 + j)*8 + u*4 + i
+ * (the order of the matrix-core fragments: a tile is read with contiguous
+ * 1 KiB wave loads and without moving values between lanes). */
+typedef struct fp4_kv_cache {
+    void* data;        /* device, fp4_kv_cache_size bytes, 16-byte aligned; needs no initialization */
+    int64_t pages;     /* 1 .. 2^30 */
+    int64_t page_size; /* tokens of a page: a multiple of 32, at most 4096 */
+    int64_t kv_heads;  /* 1 .. 256 */
+    int64_t head_dim;  /* 64, 128 or 256 */
+    int32_t format;    /* FP4_NVFP4 or FP4_MXFP4 */
+    float k_alpha;     /* per-tensor scales: > 0, in [2^-100, 2^100] (FP4_ERR_VALUE) */
+    float v_alpha;
+} fp4_kv_cache;
+
+/* Bytes of a cache (FP4_ERR_FORMAT / FP4_ERR_SHAPE outside the ranges above). */
+int fp4_kv_cache_size(int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim, int format,
+                      size_t* bytes);
+
+/* Quantize the keys and values of `tokens` tokens into their slots on `stream`.
+ *   k, v   device, BF16 (act_type 0) or FP16 (act_type 1): element e of head h
+ *          of token t at t * token_stride + h * head_stride + e
+ *   slots  device, int64 [tokens]; a slot outside [0, pages * page_size) is
+ *          skipped (padding); a slot given twice is a write race (that token
+ *          then holds a mixture of the two; every other slot is unaffected)
+ * Codes and scales are those of fp4_quantize with alpha = k_alpha / v_alpha
+ * (FP16 rows by the same rule).  k and v 16-byte aligned, strides >= 0, below
+ * 2^40 and multiples of 8 elements, tokens <= 2^24 (else FP4_ERR_SHAPE);
+ * tokens == 0 is a no-op. */
+int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, const int64_t* slots, int64_t tokens,
+                  int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                  int act_type, void* stream);
+
+/* Read rows back: k and / or v (either may be NULL) at slots[t], as
+ * code * scale (exact in FP32) times alpha in FP32, rounded to nearest even.
+ * Rows whose slot is outside [0, pages * page_size) are written as zeros.
+ * Alignment, strides and limits as fp4_kv_append; output rows must not
+ * overlap (FP4_ERR_SHAPE). */
+int fp4_kv_read(const fp4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                int act_type, void* stream);
+
+/* One attention call.  Sequence b has seq_lens[b] keys: position p is in page
+ * page_table[b][p / page_size].  Its n query tokens are the last n positions:
+ * query token i is at position seq_lens[b] - n + i.  Query head h reads KV
+ * head h / (q_heads / kv_heads). */
+typedef struct fp4_attention_args {
+    const void* q;             /* device [q_rows][q_heads][head_dim], strided, 16-byte aligned rows */
+    void* out;                 /* device, same type and shape, own strides (rows apart), 16-byte aligned rows */
+    float* lse;                /* device [q_rows][q_heads] contiguous, or NULL: natural log of the softmax sum */
+    const int32_t* page_table; /* device [batch][page_columns]; an entry outside [0, pages) holds no keys */
+    const int32_t* seq_lens;   /* device [batch]; clamped to [0, page_columns * page_size] */
+    const int32_t* q_offsets;  /* device [batch + 1]: query rows of sequence b are q_offsets[b] .. q_offsets[b + 1] - 1,
+                                  clamped to [0, q_rows]; NULL: q_rows / batch rows each.  Ranges must not overlap. */
+    const float* sinks;        /* device [q_heads] or NULL: exp(sink) is added to the softmax sum */
+    int64_t batch, q_rows, q_heads;
+    int64_t max_q;             /* about the most query tokens of a sequence (0: unknown).  Only chooses
+                                  the kernel: results do not depend on it beyond rounding */
+    int64_t page_columns, page_stride; /* columns of the page table and elements between its rows */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements, multiples of 8 */
+    int64_t window;            /* > 0: a query sees only the last `window` positions up to its own (causal only) */
+    int32_t causal;            /* 1: keys at positions up to the query's own; 0: all keys of the sequence */
+    int32_t act_type;          /* 0 BF16, 1 FP16 */
+    float scale;               /* score = scale * q . k; scale >= 2^-100, scale * k_alpha in [2^-100, 2^12] */
+    void* workspace;           /* device scratch, 16-byte aligned, fp4_attention_workspace_size bytes */
+    size_t workspace_bytes;
+} fp4_attention_args;
+
+/* Workspace of fp4_attention: a function of the cache's shape and of batch,
+ * q_rows, q_heads, max_q and page_columns only (no device is queried).  Its
+ * contents need no initialization and are not preserved; calls that may run
+ * at the same time need separate workspaces. */
+int fp4_attention_workspace_size(const fp4_kv_cache* cache, const fp4_attention_args* args, size_t* bytes);
+
+/* out = softmax(scale * q . K^T + mask) . V over the cache, on `stream`.
+ * Accumulation, softmax and sums in FP32; the products run on the 16-bit
+ * matrix cores (BF16 activations with MXFP4 caches: BF16, else FP16; scales
+ * of an MXFP4 cache above 2^125, with FP16 activations above 2^13, act as
+ * that).  A query row that sees no key gives out 0 and lse -Inf (or the
+ * sink's logarithm, out 0).  Rows of q that belong to no sequence leave out
+ * and lse as they were.  All sizes that depend on the data (seq_lens,
+ * q_offsets, page_table) stay on the device: a call captured in a HIP graph
+ * follows their contents on replay.  Deterministic.
+ * q_heads a multiple of kv_heads, at most 1024 queries per KV head; batch and
+ * q_rows at most 2^24; q_rows * q_heads and page_columns * page_size below
+ * 2^31; q_rows a multiple of batch without q_offsets; window without causal,
+ * or a scale outside its range, is FP4_ERR_VALUE.  batch == 0 or q_rows == 0
+ * is a no-op. */
+int fp4_attention(const fp4_kv_cache* cache, const fp4_attention_args* args, void* stream);
 
 #ifdef __cplusplus
 }

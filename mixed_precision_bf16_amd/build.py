@@ -21,8 +21,10 @@ LIB_NAME = "libfp4gemm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["repack.cpp", "fp4gemm.hip", "decode_bf16.hip", "decode_f16.hip", "prefill_bf16.hip", "prefill_f16.hip",
-           "moe_bf16.hip"]
-HEADERS = ["layout.h", "kernels.h", "dispatch.h", "decode_inst.inc", "prefill_inst.inc",
+           "moe_bf16.hip", "kv_cache.hip", "attention.hip", "attention_nv_bf16.hip", "attention_nv_f16.hip",
+           "attention_mx_bf16.hip", "attention_mx_f16.hip"]
+HEADERS = ["layout.h", "kernels.h", "dispatch.h", "decode_inst.inc", "prefill_inst.inc", "kv_layout.h",
+           "attention.h", "attention_inst.inc",
            os.path.join("..", "..", "include", "fp4gemm.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,701 @@
+// Attention over the FP4 key/value cache (include/fp4gemm.h, fp4_attention).
+//
+//   s_j = scale * q . k_j over the keys j that the query token sees,
+//   m = max_j s_j,  p_j = exp(s_j - m),  l = sum_j p_j (+ exp(sink - m)),
+//   out = sum_j p_j v_j / l,  lse = m + ln l.
+//
+// Both products run on the 16-bit matrix cores with FP32 accumulation, on
+// keys and values dequantized in registers (every code x scale product is
+// exact in the type used): FP16 for NVFP4 caches and for FP16 activations,
+// BF16 for MXFP4 caches with BF16 activations (E8M0 scales need its range).
+// The softmax runs in FP32 in base 2 with one pass over the keys: a running
+// maximum m and sum l per query row.  Rows of the accumulators are rescaled
+// only when a score exceeds the running maximum by more than kSlack binary
+// orders, which a wave decides together: probabilities stay below
+// 2^(kBias + kSlack), in range for FP16, and kBias moves the point where FP16
+// probabilities vanish to 2^-(24 + kBias) of the largest one.
+#pragma once
+#include "kv_layout.h"
+
+namespace fp4 {
+
+constexpr float kBias = 8.0f, kSlack = 7.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;  // running maximum before the first visible key
+constexpr int kAttnThreads = 256, kAttnWaves = 4;
+constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
+
+// Matrix-core type of a format and activation type (0: BF16, 1: FP16).
+constexpr int attn_type(int fmt, int act) { return fmt == 0 || act == 1 ? 1 : 0; }
+
+struct AttnArgs {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* q_offsets;  // null: every sequence has q_each query tokens
+    const float* sinks;
+    int64_t q_ts, q_hs, o_ts, o_hs, table_stride;
+    int batch, q_rows, q_each, q_heads, group, table_cols;
+    int max_keys;              // table_cols * page_size
+    int window, causal;
+    uint64_t tpp_magic;        // ceil(2^36 / tiles_per_page): the page of tile t < 2^26 is t * magic >> 36
+    float scale;               // scale * k_alpha * log2(e)
+    float v_alpha;
+    int parts;                 // workgroups that the work is dealt to
+    uint32_t tag;
+    float* ws_o;               // [2 * parts][rows][D]
+    float* ws_ml;              // [2 * parts][rows][2]
+    unsigned long long* words; // [parts]
+};
+
+// ------------------------------------------------------------ one key tile
+template <int FMT, int D>
+struct TileRegs {
+    using L = KvTile<FMT, D>;
+    u32x4 k[L::F], v[L::F];
+    uint32_t ks[(L::kKsLane + 3) / 4];
+    u32x2 vs[L::C];
+};
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_tile(TileRegs<FMT, D>& t, const uint8_t* __restrict__ tile, int lane) {
+    using L = KvTile<FMT, D>;
+    const int r = lane & 15, j = lane >> 4;
+#pragma unroll
+    for (int f = 0; f < L::F; ++f) t.k[f] = *reinterpret_cast<const u32x4*>(tile + f * 1024 + lane * 16);
+#pragma unroll
+    for (int f = 0; f < L::F; ++f) t.v[f] = *reinterpret_cast<const u32x4*>(tile + L::kCodes + f * 1024 + lane * 16);
+    const uint8_t* ks = tile + L::kKs + ((j * L::KD / (L::KG * L::G > L::KD ? L::G : L::KD)) * 16 + r) * L::kKsLane;
+    if constexpr (L::kKsLane == 2) t.ks[0] = *reinterpret_cast<const uint16_t*>(ks);
+    else if constexpr (L::kKsLane == 4) t.ks[0] = *reinterpret_cast<const uint32_t*>(ks);
+    else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(ks);
+        t.ks[0] = w.x;
+        t.ks[1] = w.y;
+    }
+#pragma unroll
+    for (int c = 0; c < L::C; ++c) {
+        const int g = c * (L::CH / L::G) + r * L::VD / L::G;
+        t.vs[c] = *reinterpret_cast<const u32x2*>(tile + L::kVs + (g * 4 + j) * 8);
+    }
+}
+
+// E8M0 byte b -> the convert's FP32 scale operand.  The byte saturates at the
+// largest scale whose products stay finite in the matrix-core type (2^125 in
+// BF16, 2^13 in FP16), so that a key that was written as an infinity cannot
+// reach the queries that do not see it as 0 x Inf.
+template <int CT>
+__device__ __forceinline__ float e8m0_scale(uint32_t b) {
+    return __uint_as_float(min(b, CT == 0 ? 252u : 140u) << 23);
+}
+
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+template <int SEL>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, float s) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, SEL));
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, float s) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, SEL));
+}
+template <int CT, int SEL>
+__device__ __forceinline__ uint32_t codes16(uint32_t w, float s) {
+    if constexpr (CT == 1) return codes_f16<SEL>(w, s);
+    else return codes_bf16<SEL>(w, s);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, f16x2 s) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * s);
+}
+
+// Byte B of the lane's key scales as the dequantization takes it.
+template <int FMT, int CT, int B, int N>
+__device__ __forceinline__ u32x4 key_frag(uint32_t w, const uint32_t (&ks)[N]) {
+    u32x4 o;
+    if constexpr (FMT == 0) {
+        // two E4M3 scales -> FP16 (exact), one of them for both halves; code x scale is exact in FP16
+        const f16x2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)ks[B / 4], 1.0f, (B & 2) != 0);
+        const f16x2 s = (B & 1) ? f16x2{p.y, p.y} : f16x2{p.x, p.x};
+        o.x = mul_f16x2(codes_f16<0>(w, 1.0f), s);
+        o.y = mul_f16x2(codes_f16<1>(w, 1.0f), s);
+        o.z = mul_f16x2(codes_f16<2>(w, 1.0f), s);
+        o.w = mul_f16x2(codes_f16<3>(w, 1.0f), s);
+    } else {
+        const float s = e8m0_scale<CT>((ks[B / 4] >> (8 * (B % 4))) & 0xFFu);
+        o.x = codes16<CT, 0>(w, s);
+        o.y = codes16<CT, 1>(w, s);
+        o.z = codes16<CT, 2>(w, s);
+        o.w = codes16<CT, 3>(w, s);
+    }
+    return o;
+}
+
+// Key fragment of tokens 16 U .. , chunk CK, product step S (elements
+// CH CK + KD j + 8 S .. + 7 of lane (r, j)).
+template <int FMT, int CT, int D, int U, int CK, int S>
+__device__ __forceinline__ u32x4 key_step(const TileRegs<FMT, D>& t) {
+    using L = KvTile<FMT, D>;
+    constexpr int byte = CK * 2 * L::KG + U * L::KG + (S * 8 / L::G) % L::KG;
+    if constexpr (D == 64) return key_frag<FMT, CT, byte>(t.k[0][2 * U + S], t.ks);
+    else return key_frag<FMT, CT, byte>(t.k[CK * 2 + U][S], t.ks);
+}
+
+// Two d-fragments (elements VD r + 2 Q, + 1 of chunk CK) of O^T's left operand:
+// lane (r, j) supplies tokens 4 j .. 4 j + 3 and 16 + 4 j .. .
+template <int FMT, int CT, int D, int CK, int Q>
+__device__ __forceinline__ void value_frags(const TileRegs<FMT, D>& t, u32x4& even, u32x4& odd) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        uint32_t a[4];  // elements 2 Q, 2 Q + 1 of the four tokens
+        const uint32_t sb = t.vs[CK][u];
+        if constexpr (FMT == 0) {
+            if constexpr (D == 64) {
+                a[0] = codes_f16<Q>(t.v[0][2 * u], 1.0f);
+                a[1] = codes_f16<Q + 2>(t.v[0][2 * u], 1.0f);
+                a[2] = codes_f16<Q>(t.v[0][2 * u + 1], 1.0f);
+                a[3] = codes_f16<Q + 2>(t.v[0][2 * u + 1], 1.0f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = codes_f16<Q>(t.v[CK * 2 + u][i], 1.0f);
+            }
+            const f16x2 s01 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)sb, 1.0f, false);
+            const f16x2 s23 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)sb, 1.0f, true);
+            even[2 * u] = mul_f16x2(low_halves(a[0], a[1]), s01);
+            even[2 * u + 1] = mul_f16x2(low_halves(a[2], a[3]), s23);
+            odd[2 * u] = mul_f16x2(high_halves(a[0], a[1]), s01);
+            odd[2 * u + 1] = mul_f16x2(high_halves(a[2], a[3]), s23);
+        } else {
+            float s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((sb >> (8 * i)) & 0xFFu);
+            if constexpr (D == 64) {
+                a[0] = codes16<CT, Q>(t.v[0][2 * u], s[0]);
+                a[1] = codes16<CT, Q + 2>(t.v[0][2 * u], s[1]);
+                a[2] = codes16<CT, Q>(t.v[0][2 * u + 1], s[2]);
+                a[3] = codes16<CT, Q + 2>(t.v[0][2 * u + 1], s[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = codes16<CT, Q>(t.v[CK * 2 + u][i], s[i]);
+            }
+            even[2 * u] = low_halves(a[0], a[1]);
+            even[2 * u + 1] = low_halves(a[2], a[3]);
+            odd[2 * u] = high_halves(a[0], a[1]);
+            odd[2 * u + 1] = high_halves(a[2], a[3]);
+        }
+    }
+}
+
+// Zero the scales of the value tokens at or past `end` (a slot that no token
+// was written to holds anything: its probability is 0, and 0 x NaN is NaN).
+template <int FMT, int D>
+__device__ __forceinline__ void clear_values(TileRegs<FMT, D>& t, int tok0, int j, int end) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int left = end - (tok0 + 16 * u + 4 * j);  // tokens of this quad that exist
+        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+        for (int c = 0; c < KvTile<FMT, D>::C; ++c) t.vs[c][u] &= keep;
+    }
+}
+
+// ------------------------------------------------------------ query rows
+// Row of query-row block rb (R rows): token i and head g of the group.
+template <int FMT, int ACT, int D>
+struct QueryRow {
+    using L = KvTile<FMT, D>;
+    static constexpr int kFrags = D / 32;
+    // Fragments of one row's query for lane (r, j); returns the factor that
+    // turns the accumulated products into base-2 scores.
+    __device__ static __forceinline__ float load(u32x4 (&f)[kFrags], const uint16_t* __restrict__ row, bool valid,
+                                                 int j, float scale) {
+        constexpr int S = L::KD / 8;
+#pragma unroll
+        for (int c = 0; c < L::C; ++c)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                f[c * S + s] = u32x4{0u, 0u, 0u, 0u};
+                if (valid) f[c * S + s] = *reinterpret_cast<const u32x4*>(row + c * L::CH + L::KD * j + 8 * s);
+            }
+        if constexpr (attn_type(FMT, ACT) == 1 && ACT == 0) {
+            // BF16 queries on the FP16 matrix cores: a power of two brings the
+            // row's largest element to 2^13 .. 2^14, so that every element
+            // down to 2^-27 of it converts exactly.
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t p = f[i][e];
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(p << 16)), fabsf(__uint_as_float(p & 0xFFFF0000u))));
+                }
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+            const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t p = f[i][x];
+                    f[i][x] = pack_out<1>(__uint_as_float(p << 16) * up, __uint_as_float(p & 0xFFFF0000u) * up);
+                }
+            return scale * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+        }
+        return scale;
+    }
+};
+
+struct RowRange {
+    int lo, hi;  // keys [lo, hi) that the row sees
+};
+// Keys that query token i of n sees in a sequence of `len` keys.
+__device__ __forceinline__ RowRange row_range(int i, int n, int len, int causal, int window) {
+    RowRange x{0, len};
+    if (causal) {
+        x.hi = max(0, len - n + i + 1);
+        if (window > 0) x.lo = max(0, x.hi - window);
+    }
+    return x;
+}
+
+// ------------------------------------------------------------ streaming kernel
+// Few query rows a sequence (decode, drafted tokens), any number of keys.
+// Work unit: 128 keys (one tile a wave) of one item = (sequence, block of
+// 16 MT query rows, KV head).  All units are numbered sequence by sequence
+// and dealt in equal contiguous ranges to `parts` workgroups, so that long
+// and short sequences load the GPU evenly, whatever the lengths on the device
+// are.  An item whose units fall into several workgroups is joined by the one
+// that arrives last, from the FP32 partial sums of all, in their order.
+struct Item {
+    int b, rb, h, n;       // sequence, row block, KV head, query tokens
+    int q0;                // first query row
+    int len;               // keys
+    int t0, t1;            // tiles [t0, t1) that some query of the sequence sees
+    int units, first;      // units of one item; first unit of the sequence
+    int blocks;            // row blocks
+};
+
+template <int R>
+__device__ __forceinline__ void sequence_of(const AttnArgs& a, int kv_heads, int b, Item& x) {
+    int q0, n;
+    if (a.q_offsets) {
+        q0 = min(max(a.q_offsets[b], 0), a.q_rows);
+        n = min(max(a.q_offsets[b + 1], q0), a.q_rows) - q0;
+    } else {
+        q0 = b * a.q_each;
+        n = a.q_each;
+    }
+    x.b = b;
+    x.q0 = q0;
+    x.n = n;
+    x.len = min(max(a.seq_lens[b], 0), a.max_keys);
+    const RowRange f = row_range(0, n, x.len, a.causal, a.window);
+    x.t0 = f.lo / kKvTile;
+    x.t1 = max((x.len + kKvTile - 1) / kKvTile, x.t0);
+    x.units = max(1, (x.t1 - x.t0 + kUnitTiles - 1) / kUnitTiles);
+    x.blocks = (n * a.group + R - 1) / R;  // 0 for a sequence without queries
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Final value factor and log-sum-exp of a row from its running maximum m,
+// biased sum l and sink.
+__device__ __forceinline__ float finish_row(float m, float l, bool has_sink, float sink, float& lse) {
+    float top = m;
+    if (has_sink) top = fmaxf(m, sink * kLog2e);
+    const float f = exp2_(m - top - kBias);
+    float sum = l * f;
+    if (has_sink) sum += exp2_(sink * kLog2e - top);
+    if (sum == 0.0f) {
+        lse = -__builtin_inff();
+        return 0.0f;
+    }
+    lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    return f / sum;
+}
+
+template <int FMT, int ACT, int D, int MT>
+__global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention_stream(AttnArgs a, KvArgs cache) {
+    using L = KvTile<FMT, D>;
+    constexpr int CT = attn_type(FMT, ACT);
+    constexpr int R = 16 * MT, F = D / 32, S = L::KD / 8, OT = D / 16;
+    constexpr int kPad = D + 4;  // floats of a row in LDS
+    __shared__ float lds_o[kAttnWaves][16][kPad];
+    __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
+    __shared__ float lds_w[64][16];
+    __shared__ int lds_scan[kAttnWaves];
+    __shared__ int lds_found[2];
+    __shared__ int lds_last;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, j = lane >> 4;
+    const int kv_heads = cache.kv_heads;
+
+    // ---- the workgroup's range of units
+    int total = 0;
+    for (int base = 0; base < a.batch; base += kAttnThreads) {
+        const int b = base + threadIdx.x;
+        int u = 0;
+        if (b < a.batch) {
+            Item x;
+            sequence_of<R>(a, kv_heads, b, x);
+            u = x.units * x.blocks * kv_heads;
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) u += __shfl_xor(u, d, 64);
+        __syncthreads();
+        if (lane == 0) lds_scan[wave] = u;
+        __syncthreads();
+        total += lds_scan[0] + lds_scan[1] + lds_scan[2] + lds_scan[3];
+    }
+    if (total == 0) return;
+    const int per = (total + a.parts - 1) / a.parts;
+    const int begin = blockIdx.x * per;  // parts * per < 2^31 (checked on the host)
+    if (begin >= total) return;
+    const int end = min(begin + per, total);
+
+    // ---- the sequence that unit `begin` lies in
+    {
+        int before = 0;
+        for (int base = 0; base < a.batch; base += kAttnThreads) {
+            const int b = base + threadIdx.x;
+            int u = 0;
+            if (b < a.batch) {
+                Item x;
+                sequence_of<R>(a, kv_heads, b, x);
+                u = x.units * x.blocks * kv_heads;
+            }
+            int inc = u;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int t = __shfl_up(inc, d, 64);
+                if (lane >= d) inc += t;
+            }
+            __syncthreads();
+            if (lane == 63) lds_scan[wave] = inc;
+            __syncthreads();
+            int start = before + inc - u;
+            for (int w = 0; w < kAttnWaves; ++w) {
+                if (w < wave) start += lds_scan[w];
+                before += lds_scan[w];
+            }
+            if (begin >= start && begin < start + u) {
+                lds_found[0] = b;
+                lds_found[1] = start;
+            }
+            if (before > begin) break;  // the same in every thread
+        }
+        __syncthreads();
+    }
+    Item it;
+    sequence_of<R>(a, kv_heads, __builtin_amdgcn_readfirstlane(lds_found[0]), it);
+    it.first = __builtin_amdgcn_readfirstlane(lds_found[1]);
+
+    int unit = begin;
+    while (unit < end) {
+        const int seq_units = it.units * it.blocks * kv_heads;
+        if (unit >= it.first + seq_units) {  // the next sequence that has work
+            const int first = it.first + seq_units;
+            sequence_of<R>(a, kv_heads, it.b + 1, it);  // units remain, so there is one
+            it.first = first;
+            continue;
+        }
+        const int in_seq = unit - it.first;
+        const int item = in_seq / it.units;           // (row block, head): heads of a block are neighbours
+        const int skip = in_seq - item * it.units;    // units of the item that earlier workgroups take
+        it.rb = item / kv_heads;
+        it.h = item - it.rb * kv_heads;
+        const int take = min(it.units - skip, end - unit);
+        const int item_first = unit - skip, item_last = item_first + it.units - 1;
+        const int wg0 = item_first / per, wg1 = item_last / per;  // workgroups that share the item
+
+        // ---- query rows
+        const int rows = min(R, it.n * a.group - it.rb * R);
+        u32x4 qf[MT][F];
+        float fac[MT], m[MT], l[MT];
+        RowRange range[MT];
+        f32x4 o[MT][OT];
+        int lo_all = 0, hi_all = it.len;  // keys that every valid row sees
+        {
+            const int i0 = it.rb * R / a.group, i1 = (it.rb * R + rows - 1) / a.group;
+            hi_all = row_range(i0, it.n, it.len, a.causal, a.window).hi;
+            lo_all = row_range(i1, it.n, it.len, a.causal, a.window).lo;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int row = it.rb * R + 16 * mt + r;
+            const bool valid = 16 * mt + r < rows;
+            const int i = row / a.group, g = row - i * a.group;
+            const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(it.h * a.group + g) * a.q_hs;
+            // kept normal: a factor of 0 would turn a hidden key's -Inf into NaN
+            fac[mt] = fmaxf(QueryRow<FMT, ACT, D>::load(qf[mt], src, valid, j, a.scale), 0x1p-126f);
+            range[mt] = row_range(i, it.n, it.len, a.causal, a.window);
+            m[mt] = kNoMax;
+            l[mt] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < OT; ++x) o[mt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        // ---- this wave's tiles
+        const int32_t* pages = a.page_table + (int64_t)it.b * a.table_stride;
+        const int ta = it.t0 + skip * kUnitTiles + wave;
+        const int tb = min(it.t0 + (skip + take) * kUnitTiles, it.t1);
+        for (int t = ta; t < tb; t += kAttnWaves) {
+            const int pi = (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36);
+            int page = __builtin_amdgcn_readfirstlane(pages[pi]);
+            const bool bad = (uint32_t)page >= (uint32_t)cache.pages;  // no keys there
+            page = bad ? 0 : page;
+            const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + it.h) * cache.tiles_per_page +
+                                                (t - pi * cache.tiles_per_page)) * (int64_t)L::kBytes;
+            TileRegs<FMT, D> x;
+            load_tile<FMT, D>(x, tile, lane);
+            const int tok0 = t * kKvTile;
+            const int live = bad ? 0 : it.len;
+            const bool edge = bad || tok0 + kKvTile > hi_all || tok0 < lo_all;
+            if (edge) clear_values<FMT, D>(x, tok0, j, live);
+
+            f32x4 sc[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) sc[mt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            auto keys = [&](auto uc, auto cc, auto stc) {
+                const u32x4 kf = key_step<FMT, CT, D, decltype(uc)::value, decltype(cc)::value, decltype(stc)::value>(x);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    sc[mt][decltype(uc)::value] =
+                        mfma<CT>(kf, qf[mt][decltype(cc)::value * S + decltype(stc)::value], sc[mt][decltype(uc)::value]);
+            };
+            auto keys_u = [&](auto uc) {
+                auto keys_c = [&](auto cc) {
+                    keys(uc, cc, std::integral_constant<int, 0>{});
+                    keys(uc, cc, std::integral_constant<int, 1>{});
+                    if constexpr (S == 4) {
+                        keys(uc, cc, std::integral_constant<int, 2>{});
+                        keys(uc, cc, std::integral_constant<int, 3>{});
+                    }
+                };
+                keys_c(std::integral_constant<int, 0>{});
+                if constexpr (L::C == 2) keys_c(std::integral_constant<int, 1>{});
+            };
+            keys_u(std::integral_constant<int, 0>{});
+            keys_u(std::integral_constant<int, 1>{});
+
+            u32x4 pf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float s[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = sc[mt][e >> 2][e & 3];
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int tok = tok0 + 16 * (e >> 2) + 4 * j + (e & 3);
+                        if (!(tok >= range[mt].lo && tok < range[mt].hi && tok < live)) s[e] = -__builtin_inff();
+                    }
+                }
+                float top = s[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+                top *= fac[mt];
+                if (__any(top > m[mt] + kSlack)) {
+                    top = fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = fmaxf(top, __shfl_xor(top, 32, 64));
+                    const float mn = fmaxf(m[mt], top);
+                    const float down = exp2_(m[mt] - mn);
+                    m[mt] = mn;
+                    l[mt] *= down;
+#pragma unroll
+                    for (int y = 0; y < OT; ++y) o[mt][y] *= down;
+                }
+                const float off = kBias - m[mt];
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = exp2_(fmaf(s[e], fac[mt], off));
+                    l[mt] += p[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pf[mt][e] = pack_out<CT>(p[2 * e], p[2 * e + 1]);
+            }
+
+            auto values = [&](auto cc, auto qc) {
+                constexpr int ck = decltype(cc)::value, q = decltype(qc)::value;
+                u32x4 even, odd;
+                value_frags<FMT, CT, D, ck, q>(x, even, odd);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][ck * L::VD + 2 * q] = mfma<CT>(even, pf[mt], o[mt][ck * L::VD + 2 * q]);
+                    o[mt][ck * L::VD + 2 * q + 1] = mfma<CT>(odd, pf[mt], o[mt][ck * L::VD + 2 * q + 1]);
+                }
+            };
+            auto values_c = [&](auto cc) {
+                values(cc, std::integral_constant<int, 0>{});
+                values(cc, std::integral_constant<int, 1>{});
+                if constexpr (L::VD == 8) {
+                    values(cc, std::integral_constant<int, 2>{});
+                    values(cc, std::integral_constant<int, 3>{});
+                }
+            };
+            values_c(std::integral_constant<int, 0>{});
+            if constexpr (L::C == 2) values_c(std::integral_constant<int, 1>{});
+        }
+
+        // ---- join the four waves, 16 rows at a time
+        const bool whole = wg0 == wg1;
+        const int slot = 2 * (int)blockIdx.x + (unit == begin ? 0 : 1);
+        constexpr int E = D / 16;                       // outputs of a thread: 16 threads a row
+        const int orow = threadIdx.x >> 4, od = (threadIdx.x & 15) * E;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (16 * mt >= rows) break;
+            l[mt] += __shfl_xor(l[mt], 16, 64);
+            l[mt] += __shfl_xor(l[mt], 32, 64);
+            __syncthreads();  // the LDS of the previous 16 rows is free
+            if (j == 0) {
+                lds_m[wave][r] = m[mt];
+                lds_l[wave][r] = l[mt];
+            }
+#pragma unroll
+            for (int c = 0; c < L::C; ++c)
+#pragma unroll
+                for (int reg = 0; reg < 4; ++reg)
+#pragma unroll
+                    for (int k = 0; k < L::VD; k += 4) {
+                        f32x4 w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = o[mt][c * L::VD + k + e][reg];
+                        *reinterpret_cast<f32x4*>(&lds_o[wave][r][c * L::CH + L::VD * (4 * j + reg) + k]) = w;
+                    }
+            __syncthreads();
+            float mx = lds_m[0][orow];
+#pragma unroll
+            for (int w = 1; w < kAttnWaves; ++w) mx = fmaxf(mx, lds_m[w][orow]);
+            float lx = 0.0f, ox[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) ox[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) {
+                const float f = exp2_(lds_m[w][orow] - mx);
+                lx += lds_l[w][orow] * f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) ox[e] += lds_o[w][orow][od + e] * f;
+            }
+            if (16 * mt + orow < rows) {
+                if (whole) {
+                    const int row = it.rb * R + 16 * mt + orow;
+                    const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
+                    float lse;
+                    const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) *
+                                    a.v_alpha;
+                    uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
+#pragma unroll
+                    for (int e = 0; e < E; e += 4)
+                        *reinterpret_cast<u32x2*>(dst + e) =
+                            u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f), pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
+                    if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+                } else {
+                    const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o + (size_t)slot * R * D, R * D * 4);
+                    const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml + (size_t)slot * R * 2, R * 8);
+#pragma unroll
+                    for (int e = 0; e < E; e += 4) {
+                        const f32x4 w = {ox[e], ox[e + 1], ox[e + 2], ox[e + 3]};
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
+                                                               ((16 * mt + orow) * D + od + e) * 4, 0, kDeviceCoherent);
+                    }
+                    if (od == 0)
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(mx), __float_as_uint(lx)}, rm,
+                                                              (16 * mt + orow) * 8, 0, kDeviceCoherent);
+                }
+            }
+        }
+        if (!whole) {
+            // As split_finish: this thread's stores are complete, then one arrival.
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (threadIdx.x == 0) lds_last = split_arrive(a.words + wg0, a.tag, wg1 - wg0 + 1);
+            __syncthreads();
+            if (lds_last) {
+                asm volatile("" ::: "memory");
+                const int parts = wg1 - wg0 + 1;
+                // slot of the item's part in workgroup wg0 + s: the first range
+                // it fills from its start, unless the item begins inside it
+                auto slot_of = [&](int s) { return 2 * (wg0 + s) + (s == 0 && item_first != wg0 * per ? 1 : 0); };
+#pragma unroll 1
+                for (int mt = 0; mt < MT; ++mt) {
+                    if (16 * mt >= rows) break;
+                    float mx = kNoMax, lx = 0.0f, ox[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) ox[e] = 0.0f;
+                    for (int s0 = 0; s0 < parts; s0 += 64) {
+                        const int n = min(64, parts - s0);
+                        float top = mx;
+                        __syncthreads();
+                        for (int s = threadIdx.x & 15; s < n; s += 16) {
+                            const __amdgpu_buffer_rsrc_t rm =
+                                make_rsrc(a.ws_ml + (size_t)slot_of(s0 + s) * R * 2, R * 8);
+                            lds_w[s][orow] = __uint_as_float(
+                                __builtin_amdgcn_raw_buffer_load_b32(rm, (16 * mt + orow) * 8, 0, kDeviceCoherent));
+                        }
+                        __syncthreads();
+                        for (int s = 0; s < n; ++s) top = fmaxf(top, lds_w[s][orow]);
+                        const float down = exp2_(mx - top);
+                        mx = top;
+                        lx *= down;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) ox[e] *= down;
+                        for (int s = 0; s < n; ++s) {
+                            const int sl = slot_of(s0 + s);
+                            const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o + (size_t)sl * R * D, R * D * 4);
+                            const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml + (size_t)sl * R * 2, R * 8);
+                            const float f = exp2_(lds_w[s][orow] - mx);
+                            lx += f * __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                                          rm, (16 * mt + orow) * 8 + 4, 0, kDeviceCoherent));
+#pragma unroll
+                            for (int e = 0; e < E; e += 4) {
+                                const f32x4 w = __builtin_bit_cast(
+                                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               ro, ((16 * mt + orow) * D + od + e) * 4, 0, kDeviceCoherent));
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) ox[e + y] += f * w[y];
+                            }
+                        }
+                    }
+                    if (16 * mt + orow < rows) {
+                        const int row = it.rb * R + 16 * mt + orow;
+                        const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
+                        float lse;
+                        const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) *
+                                        a.v_alpha;
+                        uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
+#pragma unroll
+                        for (int e = 0; e < E; e += 4)
+                            *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f),
+                                                                       pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
+                        if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+                    }
+                }
+            }
+        }
+        unit += take;
+    }
+}
+
+// Compiled shapes of the streaming kernel: X(D, MT), blocks of 16 MT query rows.
+#define FP4_ATTN_SHAPES(X) X(64, 1) X(64, 2) X(64, 4) X(128, 1) X(128, 2) X(128, 4) X(256, 1) X(256, 2)
+
+// Launches of one (format, activation type), in a translation unit each.
+// False when the shape is not compiled.
+bool launch_attention_nv_bf16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_nv_f16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_mx_bf16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_mx_f16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+
+}  // namespace fp4

@@ -8,6 +8,12 @@
 
 namespace fp4 {
 
+// Shared by the C entries of every translation unit (fp4gemm.hip).
+int check_device();         // FP4_OK when the current device is a gfx950
+int launch_status();        // FP4_OK / FP4_ERR_HIP from the launches since the last hipGetLastError
+uint32_t next_split_tag();  // launch tag of split-K arrival words: unique per launch, never 0
+bool alpha_ok(float alpha);
+
 // Decode kernel: TN n-tiles per wave, NWN waves per K group, NWK K groups per
 // workgroup, K split over S workgroups.
 struct DecodeShape {

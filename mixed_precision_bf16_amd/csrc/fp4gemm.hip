@@ -16,7 +16,7 @@ namespace fp4 {
 
 std::atomic<int> g_device_state[64];  // 0 unknown, 1 gfx950, 2 other
 
-static int check_device() {
+int check_device() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return FP4_ERR_DEVICE;
     int st = g_device_state[dev].load(std::memory_order_relaxed);
@@ -29,7 +29,7 @@ static int check_device() {
     return st == 1 ? FP4_OK : FP4_ERR_DEVICE;
 }
 
-static int launch_status() {
+int launch_status() {
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
@@ -130,7 +130,7 @@ static size_t decode_workspace_bytes(const DecodeShape& d, int64_t M, int64_t N,
 
 // Launch tags of the split-K arrival words: unique per launch (never 0).
 static std::atomic<uint32_t> g_split_tag{0};
-static uint32_t next_split_tag() {
+uint32_t next_split_tag() {
     uint32_t t;
     do t = g_split_tag.fetch_add(1, std::memory_order_relaxed) + 1;
     while (t == 0);
@@ -363,7 +363,7 @@ static size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt) {
 }
 
 // alpha: finite, |alpha| in [2^-100, 2^100] or exactly 1 (checked by the entries).
-static bool alpha_ok(float alpha) {
+bool alpha_ok(float alpha) {
     const float a = fabsf(alpha);
     return a == 1.0f || (a >= 0x1p-100f && a <= 0x1p100f);
 }

@@ -1285,34 +1285,12 @@ __device__ __forceinline__ float e4m3_decode(uint32_t byte) {
     return e == 0 ? (float)m * 0x1p-9f : __uint_as_float(((e + 120u) << 23) | (m << 20));
 }
 
+// One block of G elements x: its codes (element i in nibble i) and, returned,
+// its scale byte.  x: BF16 or FP16 values (at most 11 significant bits).
 template <int FMT>
-// Output rows hold gpr_out >= gpr_in blocks: blocks past the input row's
-// gpr_in are written as zero blocks (codes 0, scale byte 0), which pads K for
-// the native FP4 path; gpr_out == gpr_in is the canonical layout.
-__global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restrict__ W, uint8_t* __restrict__ codes,
-                                                       uint8_t* __restrict__ scales, int64_t groups, float alpha,
-                                                       int64_t gpr_in, int64_t gpr_out) {
+__device__ __forceinline__ uint32_t quantize_block(const float (&x)[FMT == 0 ? 16 : 32], float alpha,
+                                                   uint32_t (&out)[FMT == 0 ? 2 : 4]) {
     constexpr int G = FMT == 0 ? 16 : 32;
-    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (g >= groups) return;
-    const int64_t row = g / gpr_out, blk = g - row * gpr_out;
-    if (blk >= gpr_in) {
-        if constexpr (FMT == 0) *reinterpret_cast<u32x2*>(codes + g * (G / 2)) = u32x2{0u, 0u};
-        else *reinterpret_cast<u32x4*>(codes + g * (G / 2)) = u32x4{0u, 0u, 0u, 0u};
-        scales[g] = 0;
-        return;
-    }
-    u32x4 v[G / 8];
-    const u32x4* src = reinterpret_cast<const u32x4*>(W + (row * gpr_in + blk) * G);
-#pragma unroll
-    for (int i = 0; i < G / 8; ++i) v[i] = src[i];
-    float x[G];
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-        const uint32_t d = v[i / 4][i % 4];
-        x[2 * i] = __uint_as_float(d << 16);
-        x[2 * i + 1] = __uint_as_float(d & 0xFFFF0000u);
-    }
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < G; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf drops NaN operands
@@ -1330,7 +1308,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
         sval = __uint_as_float(sb != 0 ? sb << 23 : 0x00400000u);
     }
     const float S = __fmul_rn(alpha, sval);
-    uint32_t out[G / 8];
 #pragma unroll
     for (int w = 0; w < G / 8; ++w) out[w] = 0;
     if constexpr (FMT == 0) {
@@ -1372,9 +1349,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
                 for (int i = 0; i < G; ++i)
                     if (__builtin_isnan(x[i])) out[i / 8] &= ~(0xFu << (4 * (i % 8)));
             }
-            *reinterpret_cast<u32x2*>(codes + g * (G / 2)) = u32x2{out[0], out[1]};
-            scales[g] = (uint8_t)sb;
-            return;
+            return sb;
         }
     }
     if constexpr (FMT == 1) {
@@ -1411,9 +1386,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
                 for (int i = 0; i < G; ++i)
                     if (__builtin_isnan(x[i])) out[i / 8] &= ~(0xFu << (4 * (i % 8)));
             }
-            *reinterpret_cast<u32x4*>(codes + g * (G / 2)) = u32x4{out[0], out[1], out[2], out[3]};
-            scales[g] = (uint8_t)sb;
-            return;
+            return sb;
         }
     }
     // With alpha a power of two, S has at most 4 significant bits and x at
@@ -1445,6 +1418,39 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
         if (c != 0 && x[i] < 0.0f) c |= 8u;
         out[i / 8] |= c << (4 * (i % 8));
     }
+    return sb;
+}
+
+template <int FMT>
+// Output rows hold gpr_out >= gpr_in blocks: blocks past the input row's
+// gpr_in are written as zero blocks (codes 0, scale byte 0), which pads K for
+// the native FP4 path; gpr_out == gpr_in is the canonical layout.
+__global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restrict__ W, uint8_t* __restrict__ codes,
+                                                       uint8_t* __restrict__ scales, int64_t groups, float alpha,
+                                                       int64_t gpr_in, int64_t gpr_out) {
+    constexpr int G = FMT == 0 ? 16 : 32;
+    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (g >= groups) return;
+    const int64_t row = g / gpr_out, blk = g - row * gpr_out;
+    if (blk >= gpr_in) {
+        if constexpr (FMT == 0) *reinterpret_cast<u32x2*>(codes + g * (G / 2)) = u32x2{0u, 0u};
+        else *reinterpret_cast<u32x4*>(codes + g * (G / 2)) = u32x4{0u, 0u, 0u, 0u};
+        scales[g] = 0;
+        return;
+    }
+    u32x4 v[G / 8];
+    const u32x4* src = reinterpret_cast<const u32x4*>(W + (row * gpr_in + blk) * G);
+#pragma unroll
+    for (int i = 0; i < G / 8; ++i) v[i] = src[i];
+    float x[G];
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) {
+        const uint32_t d = v[i / 4][i % 4];
+        x[2 * i] = __uint_as_float(d << 16);
+        x[2 * i + 1] = __uint_as_float(d & 0xFFFF0000u);
+    }
+    uint32_t out[G / 8];
+    const uint32_t sb = quantize_block<FMT>(x, alpha, out);
     if constexpr (FMT == 0) {
         *reinterpret_cast<u32x2*>(codes + g * (G / 2)) = u32x2{out[0], out[1]};
     } else {

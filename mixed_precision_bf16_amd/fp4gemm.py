@@ -24,6 +24,24 @@ _c_i64 = ctypes.c_int64
 _c_vp = ctypes.c_void_p
 _c_sz = ctypes.c_size_t
 
+
+class _KVCacheDesc(ctypes.Structure):
+    """fp4_kv_cache of include/fp4gemm.h."""
+    _fields_ = [("data", _c_vp), ("pages", _c_i64), ("page_size", _c_i64), ("kv_heads", _c_i64),
+                ("head_dim", _c_i64), ("format", ctypes.c_int32), ("k_alpha", ctypes.c_float),
+                ("v_alpha", ctypes.c_float)]
+
+
+class _AttentionArgs(ctypes.Structure):
+    """fp4_attention_args of include/fp4gemm.h."""
+    _fields_ = [("q", _c_vp), ("out", _c_vp), ("lse", _c_vp), ("page_table", _c_vp), ("seq_lens", _c_vp),
+                ("q_offsets", _c_vp), ("sinks", _c_vp), ("batch", _c_i64), ("q_rows", _c_i64), ("q_heads", _c_i64),
+                ("max_q", _c_i64), ("page_columns", _c_i64), ("page_stride", _c_i64), ("q_token_stride", _c_i64),
+                ("q_head_stride", _c_i64), ("out_token_stride", _c_i64), ("out_head_stride", _c_i64),
+                ("window", _c_i64), ("causal", ctypes.c_int32), ("act_type", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("workspace", _c_vp), ("workspace_bytes", _c_sz)]
+
+
 # name -> (restype, argtypes); mirrors include/fp4gemm.h
 _SIGNATURES = {
     "fp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -50,6 +68,14 @@ _SIGNATURES = {
                                        _c_sz, _c_vp]),
     "fp4_moe_gemm": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64,
                                     _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_vp]),
+    "fp4_kv_cache_size": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.POINTER(_c_sz)]),
+    "fp4_kv_append": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64,
+                                     _c_i64, _c_i64, ctypes.c_int, _c_vp]),
+    "fp4_kv_read": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
+                                   _c_i64, _c_i64, ctypes.c_int, _c_vp]),
+    "fp4_attention_workspace_size": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), ctypes.POINTER(_AttentionArgs),
+                                                    ctypes.POINTER(_c_sz)]),
+    "fp4_attention": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), ctypes.POINTER(_AttentionArgs), _c_vp]),
 }
 
 STATUS = {0: "FP4_OK", 1: "FP4_ERR_NULL", 2: "FP4_ERR_SHAPE", 3: "FP4_ERR_FORMAT", 4: "FP4_ERR_VALUE",
@@ -375,3 +401,237 @@ def gemm_native(A, wq, sq, N: int, K: int, out=None, workspace=None, stream=None
     _check(lib().fp4_gemm_native(_dev_ptr(A), _dev_ptr(wq), _dev_ptr(sq), _dev_ptr(out), m, N, K, alpha,
                                  _dev_ptr(workspace), ws_bytes, _stream_handle(stream)), "fp4_gemm_native")
     return out
+
+
+# ------------------------------------------------- FP4 key/value cache, attention
+def kv_cache_size(pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int) -> int:
+    """Bytes of a cache of this shape (fp4_kv_cache_size)."""
+    b = _c_sz()
+    _check(lib().fp4_kv_cache_size(pages, page_size, kv_heads, head_dim, fmt, ctypes.byref(b)), "fp4_kv_cache_size")
+    return b.value
+
+
+class KVCache:
+    """A paged FP4 key/value cache of one attention layer: `data` (a contiguous
+    uint8 CUDA tensor of kv_cache_size bytes, in the layout that
+    include/fp4gemm.h documents) and its shape.  k_alpha / v_alpha are the
+    per-tensor scales of keys and values."""
+
+    __slots__ = ("data", "pages", "page_size", "kv_heads", "head_dim", "fmt", "k_alpha", "v_alpha", "_desc", "_ref")
+
+    def __init__(self, data, pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int, k_alpha: float = 1.0,
+                 v_alpha: float = 1.0):
+        import torch
+        if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous():
+            raise ValueError("data must be a contiguous uint8 CUDA tensor")
+        if data.numel() != kv_cache_size(pages, page_size, kv_heads, head_dim, fmt):
+            raise ValueError("data does not have the cache's size")
+        self.data, self.pages, self.page_size, self.kv_heads = data, pages, page_size, kv_heads
+        self.head_dim, self.fmt, self.k_alpha, self.v_alpha = head_dim, fmt, k_alpha, v_alpha
+        self._desc = _KVCacheDesc(data.data_ptr(), pages, page_size, kv_heads, head_dim, fmt, k_alpha, v_alpha)
+        self._ref = ctypes.byref(self._desc)
+
+
+def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int, k_alpha: float = 1.0,
+                 v_alpha: float = 1.0, device="cuda") -> KVCache:
+    """An uninitialized cache (slots may hold anything until they are appended to)."""
+    import torch
+    data = torch.empty(kv_cache_size(pages, page_size, kv_heads, head_dim, fmt), dtype=torch.uint8, device=device)
+    return KVCache(data, pages, page_size, kv_heads, head_dim, fmt, k_alpha, v_alpha)
+
+
+class _OnStream:
+    """Device and stream of a call: the tensors' device is made current for the
+    library call, and what the wrapper allocates belongs to the stream that the
+    kernels run on."""
+
+    __slots__ = ("handle", "_guards")
+
+    def __init__(self, device, stream):
+        import torch
+        self._guards = []
+        if torch.cuda.current_device() != device.index:
+            self._guards.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream must be a stream of {device}")
+            self.handle = stream.cuda_stream
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _act_type(dtype, what: str) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float16:
+        return 1
+    raise ValueError(f"{what} must be bfloat16 or float16")
+
+
+def _rows(t, what: str, tokens: int, heads: int, head_dim: int, device):
+    """(token stride, head stride) of a [tokens][heads][head_dim] tensor."""
+    if t.shape != (tokens, heads, head_dim) or t.device != device:
+        raise ValueError(f"{what} must be a tensor [{tokens}][{heads}][{head_dim}] on {device}")
+    a, b, c = t.stride()
+    a, b = a if tokens > 1 else 0, b if heads > 1 else 0  # the stride of a single row means nothing
+    if c != 1 or a % 8 or b % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{what} must have contiguous, 16-byte aligned rows")
+    return a, b
+
+
+def _vector(t, what: str, n: int, dtype, device):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
+    """fp4_kv_append: quantize k, v (bfloat16 or float16 CUDA [tokens][kv_heads][head_dim],
+    any token and head strides that are multiples of 8) into the cache at
+    slots (int64 CUDA [tokens]; page * page_size + position in the page, a slot
+    outside the cache is skipped, no slot twice)."""
+    import torch
+    act = _act_type(k.dtype, "k")
+    dev = cache.data.device
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have the same type")
+    n = k.shape[0]
+    kt, kh = _rows(k, "k", n, cache.kv_heads, cache.head_dim, dev)
+    vt, vh = _rows(v, "v", n, cache.kv_heads, cache.head_dim, dev)
+    sp = _vector(slots, "slots", n, torch.int64, dev)
+    with _OnStream(dev, stream) as s:
+        st = lib().fp4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), sp, n, kt, kh, vt, vh, act, s)
+    if st:
+        _check(st, "fp4_kv_append")
+
+
+def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=None):
+    """fp4_kv_read: the cache's rows at slots (int64 CUDA [tokens]) as
+    (k, v), each [tokens][kv_heads][head_dim] of `dtype` (bfloat16 by default);
+    zeros for a slot outside the cache.  k_out / v_out are filled if given."""
+    import torch
+    dev = cache.data.device
+    given = [t.dtype for t in (k_out, v_out) if t is not None]
+    if dtype is None:
+        dtype = given[0] if given else torch.bfloat16
+    act = _act_type(dtype, "dtype")
+    if any(g != dtype for g in given):
+        raise ValueError("k_out and v_out must have the requested type")
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    sp = _vector(slots, "slots", n, torch.int64, dev)
+    with _OnStream(dev, stream) as s:
+        shape = (n, cache.kv_heads, cache.head_dim)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        kt, kh = _rows(k_out, "k_out", *shape, dev)
+        vt, vh = _rows(v_out, "v_out", *shape, dev)
+        st = lib().fp4_kv_read(cache._ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), kt, kh, vt, vh, act, s)
+    if st:
+        _check(st, "fp4_kv_read")
+    return k_out, v_out
+
+
+def _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks):
+    import torch
+    dev = cache.data.device
+    if q.dim() != 3:
+        raise ValueError("q must be a tensor [q_rows][q_heads][head_dim]")
+    act = _act_type(q.dtype, "q")
+    rows, heads, _ = q.shape
+    qt, qh = _rows(q, "q", rows, heads, cache.head_dim, dev)
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"page_table must be an int32 matrix [batch][columns] on {dev} with contiguous rows")
+    batch, columns = page_table.shape
+    a = _AttentionArgs()
+    a.q, a.q_token_stride, a.q_head_stride = q.data_ptr(), qt, qh
+    a.page_table, a.page_columns = page_table.data_ptr(), columns
+    a.page_stride = page_table.stride(0) if batch > 1 else columns
+    a.seq_lens = _vector(seq_lens, "seq_lens", batch, torch.int32, dev)
+    if q_offsets is not None:
+        a.q_offsets = _vector(q_offsets, "q_offsets", batch + 1, torch.int32, dev)
+        a.max_q = max_q if max_q is not None else rows
+    else:
+        if batch and rows % batch:
+            raise ValueError("q_rows must be a multiple of the batch without q_offsets")
+        a.max_q = rows // batch if batch else 0
+    if sinks is not None:
+        a.sinks = _vector(sinks, "sinks", heads, torch.float32, dev)
+    a.batch, a.q_rows, a.q_heads, a.window, a.causal, a.act_type = batch, rows, heads, window, int(causal), act
+    a.scale = cache.head_dim ** -0.5 if scale is None else scale
+    return a
+
+
+def attention_workspace_size(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None) -> int:
+    """Bytes of workspace that attention() needs for these shapes."""
+    a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, True, 0, None, None)
+    b = _c_sz()
+    _check(lib().fp4_attention_workspace_size(cache._ref, ctypes.byref(a), ctypes.byref(b)),
+           "fp4_attention_workspace_size")
+    return b.value
+
+
+def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None, causal: bool = True,
+              window: int = 0, scale=None, sinks=None, out=None, lse=None, return_lse: bool = False, workspace=None,
+              stream=None):
+    """fp4_attention: softmax(scale * q . K^T) . V over the cache.
+
+    q: bfloat16 or float16 CUDA [q_rows][q_heads][head_dim]; page_table: int32
+    [batch][columns]; seq_lens: int32 [batch], keys of each sequence, the query
+    tokens' own among them.  The query rows of sequence b are
+    q_offsets[b] .. q_offsets[b + 1] - 1 (int32 [batch + 1]) or, without
+    q_offsets, q_rows / batch each; they are its last positions.  max_q: about
+    the most query tokens of a sequence (default: q_rows), for the choice of
+    kernel.  window > 0: only the last `window` positions up to the query's
+    own.  scale: head_dim ** -0.5 by default.  sinks: float32 [q_heads].
+    Returns out ([q_rows][q_heads][head_dim] of q's type) or (out, lse) with
+    lse float32 [q_rows][q_heads].  What the wrapper allocates is zero-filled
+    (lse: -inf) when q_offsets may leave rows out."""
+    import torch
+    a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks)
+    dev = cache.data.device
+    rows, heads, dim = q.shape
+    with _OnStream(dev, stream) as s:
+        if out is None:
+            out = (torch.empty if q_offsets is None else torch.zeros)((rows, heads, dim), dtype=q.dtype, device=dev)
+        elif out.dtype != q.dtype:
+            raise ValueError("out must have q's type")
+        a.out = out.data_ptr()
+        a.out_token_stride, a.out_head_stride = _rows(out, "out", rows, heads, dim, dev)
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
+                raise ValueError(f"lse must be a contiguous float32 tensor [{rows}][{heads}] on {dev}")
+        elif return_lse:
+            if q_offsets is None:
+                lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+            else:
+                lse = torch.full((rows, heads), float("-inf"), dtype=torch.float32, device=dev)
+        if lse is not None:
+            a.lse = lse.data_ptr()
+        ref = ctypes.byref(a)
+        if workspace is None:
+            b = _c_sz()
+            _check(lib().fp4_attention_workspace_size(cache._ref, ref, ctypes.byref(b)),
+                   "fp4_attention_workspace_size")
+            workspace = torch.empty(b.value, dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+        st = lib().fp4_attention(cache._ref, ref, s)
+    if st:
+        _check(st, "fp4_attention")
+    return (out, lse) if return_lse else out

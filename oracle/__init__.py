@@ -30,4 +30,5 @@ from .fp4_oracle import (  # noqa: F401
     unpack_codes,
 )
 from .moe_oracle import moe_reference  # noqa: F401,E402
-from .quant_oracle import native_reference, quantize_reference, scaled_gemm_reference  # noqa: F401,E402
+from .quant_oracle import native_reference, quantize_reference, quantize_values, scaled_gemm_reference  # noqa: F401,E402
+from .kv_oracle import attention_reference, kv_offsets, kv_read_reference, kv_write_reference  # noqa: F401,E402

@@ -75,8 +75,12 @@ def nearest_e2m1(q: np.ndarray) -> np.ndarray:
 def quantize_reference(w_bits: np.ndarray, fmt: int, alpha: float = 1.0):
     """BF16 weights [N][K] (bit patterns) -> (codes u8 [N][K/2], scales u8
     [N][K/G]) by the rules in the module docstring."""
+    return quantize_values(bf16_bits_to_f64(w_bits).astype(np.float32), fmt, alpha)   # exact
+
+
+def quantize_values(w: np.ndarray, fmt: int, alpha: float = 1.0):
+    """quantize_reference of FP32 values [N][K]."""
     G = group_size(fmt)
-    w = bf16_bits_to_f64(w_bits).astype(np.float32)            # exact
     N, K = w.shape
     if K % G:
         raise ValueError("K must be a multiple of the group size")

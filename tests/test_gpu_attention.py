@@ -1,0 +1,431 @@
+"""GPU parity of fp4_attention against the float64 oracle.
+
+Inputs are written into the cache by the oracle, so the reference knows the
+rows exactly.  Tolerance of one output, from the roundings of the kernel: half
+a step u_o of the output type on the result, and on every probability half a
+step u_p of the matrix-core type (BF16 for MXFP4 caches with BF16 activations,
+else FP16) plus the error e_s of its score in FP32:
+
+    |out - ref| <= u_o |ref| + (u_p + 2 e_s) sum_j p_j |v_j| / l + tiny
+
+with e_s = (D + 4) 2^-24 scale max_j sum_d |q_d k_jd| + 2^-20 (the FP32 sums of
+the products, and the exponential) plus (keys) 2^-24 for the FP32 sum over
+the keys; tiny covers FP16 subnormals of the output (2^-25).  The numerator and
+the denominator both carry e_s, hence the 2.  lse: e_s + 2^-22 |lse| +
+(keys) 2^-24."""
+
+import numpy as np
+import pytest
+
+import oracle
+from mixed_precision_bf16_amd import fp4gemm as F
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gfx950():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    name = torch.cuda.get_device_properties(0).gcnArchName
+    if not name.startswith("gfx950"):
+        pytest.skip(f"needs gfx950, found {name}")
+    F.lib()
+    yield
+
+
+class Problem:
+    """Sequences of `lens` keys with `news` query tokens each, pages in random
+    order, everything that no token was written to filled with 0xFF (NaN
+    scales)."""
+
+    def __init__(self, lens, news, fmt=0, dtype=BF16, D=128, H=2, group=4, page=64, seed=0, strength=1.5, ka=1.0,
+                 va=1.0, extra_columns=0):
+        rng = np.random.Generator(np.random.PCG64(seed))
+        self.lens, self.fmt, self.dtype, self.D, self.H, self.page = list(lens), fmt, dtype, D, H, page
+        self.ka, self.va, self.heads = ka, va, H * group
+        per = [-(-x // page) for x in lens]
+        self.pages = sum(per) + 2
+        order = rng.permutation(self.pages)
+        cols = max(per + [1]) + extra_columns
+        self.table = np.full((len(lens), cols), -1, np.int32)
+        at = 0
+        for b, n in enumerate(per):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.data = np.full(F.kv_cache_size(self.pages, page, H, D, fmt), 0xFF, np.uint8)
+        slots = np.concatenate([self.slots(b, np.arange(x)) for b, x in enumerate(lens)]).astype(np.int64)
+        x = rng.standard_normal((2, len(slots), H, D)).astype(np.float32)
+        x[0, :, :, :3] *= 4.0
+        x[0] *= ka
+        x[1] *= va
+        oracle.kv_write_reference(self.data, slots, x[0], x[1], page, fmt, ka, va)
+        self.k = np.zeros((self.pages * page, H, D))
+        self.v = np.zeros_like(self.k)
+        if len(slots):
+            self.k[slots], self.v[slots] = oracle.kv_read_reference(self.data, slots, H, D, page, fmt, ka, va)
+        self.offsets = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        q = rng.standard_normal((int(self.offsets[-1]), self.heads, D)) * strength / ka
+        self.q = torch.from_numpy(q).to(dtype)
+        self.uniform = len(set(news)) == 1
+        self.scale = D ** -0.5
+
+    def slots(self, b, pos):
+        return self.table[b, pos // self.page].astype(np.int64) * self.page + pos % self.page
+
+    def cache(self):
+        return F.KVCache(torch.from_numpy(self.data).cuda(), self.pages, self.page, self.H, self.D, self.fmt, self.ka,
+                         self.va)
+
+    def run(self, q=None, **kw):
+        off = kw.pop("offsets", None)
+        if off is None and not self.uniform:
+            off = torch.from_numpy(self.offsets).cuda()
+        kw.setdefault("scale", self.scale)
+        return F.attention(self.q.cuda() if q is None else q, self.cache(), torch.from_numpy(self.table).cuda(),
+                           torch.tensor(self.lens, dtype=torch.int32, device="cuda"), q_offsets=off, return_lse=True,
+                           **kw)
+
+    def check(self, got, causal=True, window=0, sinks=None, scale=None):
+        scale = float(np.float32(self.scale if scale is None else scale))
+        q = self.q.double().numpy()
+        ref, lse, weight = oracle.attention_reference(q, self.k, self.v, self.table, self.lens, self.offsets, self.page,
+                                                      causal, window, scale, sinks)
+        out = got[0].double().cpu().numpy()
+        got_lse = got[1].double().cpu().numpy()
+        group = self.heads // self.H
+        u_o = torch.finfo(self.dtype).eps / 2
+        u_p = 2.0 ** -8 if self.fmt == 1 and self.dtype == BF16 else 2.0 ** -11
+        e_s = np.zeros(lse.shape)
+        for b, n in enumerate(np.diff(self.offsets)):
+            s = self.slots(b, np.arange(self.lens[b])) if self.lens[b] else np.zeros(0, np.int64)
+            s = s[(s >= 0) & (s < len(self.k))]
+            for h in range(self.heads):
+                qa = np.abs(q[self.offsets[b]:self.offsets[b] + n, h])
+                mag = (qa @ np.abs(self.k[s, h // group]).T).max(-1, initial=0.0) if n else 0.0
+                e_s[self.offsets[b]:self.offsets[b] + n, h] = (self.D + 4) * 2.0 ** -24 * scale * mag + 2.0 ** -20
+        keys = max(self.lens + [1]) * 2.0 ** -24
+        bound = u_o * np.abs(ref) + (u_p + 2 * e_s[..., None] + keys) * weight + 2.0 ** -25
+        assert np.all(np.isfinite(out))
+        off = np.abs(out - ref)
+        assert np.all(off <= bound), (float((off / bound).max()), np.argwhere(off > bound)[:4])
+        empty = np.isneginf(lse)
+        assert np.array_equal(np.isneginf(got_lse), empty)
+        d = np.abs(got_lse[~empty] - lse[~empty])
+        assert np.all(d <= (e_s + keys)[~empty] + 2.0 ** -22 * np.abs(lse[~empty])), float(d.max(initial=0))
+
+
+def _go(p, **kw):
+    sinks = kw.get("sinks")
+    dev = dict(kw)
+    if sinks is not None:
+        dev["sinks"] = torch.from_numpy(sinks).cuda()
+    got = p.run(**dev)
+    torch.cuda.synchronize()
+    kw.pop("max_q", None)
+    p.check(got, **kw)
+    return got
+
+
+def _sinks(heads, seed):
+    s = np.random.Generator(np.random.PCG64(seed)).standard_normal(heads).astype(np.float32)
+    s[0] = -np.inf
+    return s
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("D,H,group,page", [(64, 1, 1, 32), (64, 8, 8, 64), (128, 2, 4, 96), (128, 8, 8, 64),
+                                            (128, 1, 16, 128), (256, 2, 5, 32), (256, 1, 1, 256)])
+def test_decode(D, H, group, page, fmt, dtype):
+    """One query token a sequence, lengths from one key on."""
+    print("[case] decode", D, H, group, page, fmt, dtype, flush=True)
+    p = Problem([1, 31, 32, 33, 127, 129, 300, 64], [1] * 8, fmt, dtype, D, H, group, page, seed=D + group)
+    _go(p)
+
+
+@pytest.mark.parametrize("fmt,dtype,ka,va", [(0, BF16, 0.02, 0.7), (0, FP16, 1.3, 0.01), (1, BF16, 0.3, 1.9),
+                                             (1, FP16, 2.0, 0.5)])
+def test_alphas(fmt, dtype, ka, va):
+    _go(Problem([70, 200], [1, 1], fmt, dtype, ka=ka, va=va, seed=3))
+
+
+@pytest.mark.parametrize("fmt,dtype", [(0, BF16), (1, BF16), (1, FP16)])
+@pytest.mark.parametrize("news,lens,D,group", [
+    ([4, 4, 4], [4, 100, 257], 128, 8), ([2, 2], [2, 65], 64, 20), ([1, 5, 3, 0, 2], [9, 200, 3, 50, 64], 128, 4),
+    ([17, 1, 40], [17, 500, 130], 128, 5), ([33, 70], [33, 200], 256, 3), ([7, 130], [64, 130], 64, 8)])
+def test_several_query_tokens(news, lens, D, group, fmt, dtype):
+    """Drafted tokens, ragged chunks and prompts; a sequence without queries."""
+    print("[case] several", news, lens, D, group, fmt, dtype, flush=True)
+    p = Problem(lens, news, fmt, dtype, D, 2, group, seed=len(lens) + D)
+    _go(p)
+    _go(p, max_q=max(news))
+
+
+@pytest.mark.parametrize("max_q", [1, None])
+@pytest.mark.parametrize("window", [1, 31, 33, 128, 5000])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_window_and_sinks(window, sinks, max_q):
+    p = Problem([1, 40, 333, 700], [1, 3, 2, 40], 1, BF16, 64, 2, 8, 32, seed=window)
+    _go(p, window=window, sinks=_sinks(16, 5) if sinks else None, max_q=max_q)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 20, 1]])
+def test_all_keys_without_causal_order(news):
+    _go(Problem([5, 90, 260], news, 0, FP16, seed=8), causal=False)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_rows_that_see_nothing(sinks, max_q):
+    """Empty sequences, and query tokens that lie before the first key."""
+    p = Problem([0, 2, 0, 70, 10], [1, 5, 3, 2, 33], 0, BF16, seed=9)
+    got = _go(p, sinks=_sinks(8, 6) if sinks else None, max_q=max_q)
+    assert torch.all(got[0][0] == 0) and torch.all(got[0][1:4] == 0)
+
+
+@pytest.mark.parametrize("max_q", [2, 60])
+def test_pages_that_are_not_there(max_q):
+    """Entries outside [0, pages) hold no keys, wherever they are."""
+    p = Problem([200, 300, 64], [2, 60, 1], 0, BF16, page=32, seed=10)
+    p.table[0, 2], p.table[1, 0], p.table[1, 9], p.table[2, :] = -1, p.pages, np.iinfo(np.int32).min, -7
+    _go(p, max_q=max_q)
+
+
+def test_infinite_keys_stay_with_the_queries_that_see_them():
+    """A token written with infinities does not reach earlier queries (NVFP4
+    saturates them, an MXFP4 scale saturates in the value product)."""
+    for fmt, dtype in ((0, BF16), (1, BF16), (1, FP16)):
+        p = Problem([40], [3], fmt, dtype, 128, 1, 4, 64, seed=11)
+        clean = p.run()
+        bad = np.full((1, 1, 128), np.inf, np.float32)
+        oracle.kv_write_reference(p.data, p.slots(0, np.array([39])), bad, bad, 64, fmt)
+        got = p.run()
+        assert torch.equal(got[0][:2], clean[0][:2]) and torch.equal(got[1][:2], clean[1][:2])
+
+
+@pytest.mark.parametrize("fmt,dtype,strength", [(0, BF16, 200.0), (0, BF16, 1e-20), (1, BF16, 200.0), (0, FP16, 100.0),
+                                                (1, FP16, 1e-3)])
+def test_strong_and_weak_queries(fmt, dtype, strength):
+    """Peaked and flat softmax; BF16 queries far from FP16's range."""
+    _go(Problem([130, 513], [1, 4], fmt, dtype, strength=strength, seed=12))
+
+
+def test_growing_scores_rescale():
+    """Scores that grow along the sequence: the running maximum moves in every
+    tile, and early keys vanish."""
+    p = Problem([600], [1], 0, BF16, 128, 1, 4, 64, seed=13)
+    slots = p.slots(0, np.arange(600))
+    k = np.random.Generator(np.random.PCG64(1)).standard_normal((600, 1, 128)).astype(np.float32) * 0.05
+    k[:, 0, 0] = np.arange(600) * 0.2
+    v = np.random.Generator(np.random.PCG64(2)).standard_normal((600, 1, 128)).astype(np.float32)
+    oracle.kv_write_reference(p.data, slots, k, v, 64, 0)
+    p.k[slots], p.v[slots] = oracle.kv_read_reference(p.data, slots, 1, 128, 64, 0)
+    p.q[..., 0] = 6.0
+    _go(p)
+    p.q[..., 0] = -6.0
+    _go(p)
+
+
+@pytest.mark.parametrize("lens,H", [([9000], 1), ([4000, 1, 70, 2500], 2), ([700] * 40, 4)])
+def test_items_split_over_workgroups(lens, H):
+    """Long sequences are joined from partial sums; repeated calls with a used
+    workspace give the same bits."""
+    p = Problem(lens, [1] * len(lens), 0, BF16, 128, H, 8, 64, seed=H)
+    size = F.attention_workspace_size(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+                                      torch.tensor(p.lens, dtype=torch.int32, device="cuda"))
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    first = _go(p)
+    for _ in range(3):
+        again = p.run(workspace=ws)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+@pytest.mark.parametrize("B", [300, 1000])
+def test_large_batches(B):
+    """More sequences than one pass of the work scan covers, most of them short."""
+    rng = np.random.Generator(np.random.PCG64(B))
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    lens[B // 2] = 2000
+    _go(Problem(lens, [1] * B, 1, BF16, 64, 1, 2, 32, seed=B))
+
+
+def test_strides_rows_of_no_sequence_and_longer_tables():
+    p = Problem([100, 80], [2, 3], 0, BF16, 128, 2, 4, 64, seed=14, extra_columns=3)
+    want = p.run()
+    q = torch.randn((8, 3 * 8, 128), device="cuda").to(BF16)
+    q[1:6, 8:16] = p.q.cuda()
+    out = torch.full((8, 8 * 2, 128), 5.0, dtype=BF16, device="cuda")
+    lse = torch.full((8, 8), 5.0, device="cuda")
+    wide = torch.full((2, 2 * p.table.shape[1]), 1 << 20, dtype=torch.int32, device="cuda")
+    wide[:, :p.table.shape[1]] = torch.from_numpy(p.table).cuda()
+    off = torch.tensor([1, 3, 6], dtype=torch.int32, device="cuda")
+    F.attention(q[:, 8:16], p.cache(), wide[:, :p.table.shape[1]],
+                torch.tensor(p.lens, dtype=torch.int32, device="cuda"), q_offsets=off, out=out[:, ::2], lse=lse,
+                scale=p.scale)
+    assert torch.equal(out[1:6, ::2], want[0]) and torch.equal(lse[1:6], want[1])
+    assert torch.all(out[:, 1::2] == 5) and torch.all(out[[0, 6, 7]] == 5) and torch.all(lse[[0, 6, 7]] == 5)
+
+
+def test_lengths_past_the_table_are_clamped():
+    p = Problem([64, 128], [1, 1], 0, BF16, page=64, seed=15)
+    p.table = np.where(p.table < 0, -1, p.table)
+    got = F.attention(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+                      torch.tensor([64, 1 << 30], dtype=torch.int32, device="cuda"), return_lse=True)
+    p.check(got)
+    got = F.attention(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+                      torch.tensor([-5, 128], dtype=torch.int32, device="cuda"), return_lse=True)
+    assert torch.all(got[0][0] == 0) and torch.all(torch.isneginf(got[1][0]))
+
+
+def test_offsets_out_of_range_are_clamped():
+    p = Problem([50, 60], [1, 2], 0, BF16, seed=16)
+    off = torch.tensor([-4, 1, 1 << 30], dtype=torch.int32, device="cuda")
+    p.check(p.run(offsets=off))
+
+
+def test_graph_replay_follows_the_data():
+    """A captured step (append, attention) replayed with other lengths, tokens
+    and queries, the program's own work between the replays; a second graph
+    shares the workspace."""
+    H, D, group, page, B = 2, 128, 4, 64, 3
+    cache = F.new_kv_cache(40, page, H, D, 0)
+    gen = torch.Generator("cuda").manual_seed(3)
+    fill = torch.randn((40 * page, 2 * H, D), device="cuda", generator=gen).to(BF16)
+    F.kv_append(cache, fill[:, :H], fill[:, H:], torch.arange(40 * page, device="cuda"))
+    table = torch.randperm(36, device="cuda", generator=gen).to(torch.int32).reshape(3, 12)
+    q = torch.empty((B, H * group, D), dtype=BF16, device="cuda")
+    kv = torch.empty((B, 2 * H, D), dtype=BF16, device="cuda")
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+    ws = torch.empty(F.attention_workspace_size(q, cache, table, lens), dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty_like(q), torch.empty((B, H * group), device="cuda")) for _ in range(2)]
+
+    def step(i):
+        F.kv_append(cache, kv[:, :H], kv[:, H:], slots)
+        F.attention(q, cache, table, lens, out=outs[i][0], lse=outs[i][1], workspace=ws)
+
+    def load(seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        q.copy_(torch.randn(q.shape, device="cuda", generator=g))
+        kv.copy_(torch.randn(kv.shape, device="cuda", generator=g))
+        n = torch.randint(1, 12 * page, (B,), device="cuda", generator=g)
+        lens.copy_(n)
+        slots.copy_(table.gather(1, ((n - 1) // page)[:, None])[:, 0].long() * page + (n - 1) % page)
+
+    load(0)
+    step(0)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(i)
+        graphs.append(g)
+    for seed in range(1, 7):
+        load(seed)
+        want = F.attention(q, _appended(cache, kv, H, slots), table, lens, return_lse=True)
+        torch.cuda.synchronize()
+        i = seed % 2
+        outs[i][0].fill_(9.0)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
+
+
+def _appended(cache, kv, H, slots):
+    c = F.KVCache(cache.data.clone(), cache.pages, cache.page_size, cache.kv_heads, cache.head_dim, cache.fmt)
+    F.kv_append(c, kv[:, :H], kv[:, H:], slots)
+    return c
+
+
+def test_another_stream():
+    p = Problem([500, 3000], [1, 1], 0, BF16, seed=17)
+    want = p.run()
+    q, cache, table = p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [F.attention(q, cache, table, lens, scale=p.scale, stream=side, return_lse=True) for _ in range(4)]
+    k, v = F.kv_read(cache, torch.from_numpy(p.slots(1, np.arange(100))).cuda(), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+    assert np.array_equal(k.double().cpu().numpy(), p.k[p.slots(1, np.arange(100))])
+
+
+def test_no_queries_is_a_no_op():
+    p = Problem([5], [1], seed=18)
+    e = torch.empty((0, 8, 128), dtype=BF16, device="cuda")
+    out = F.attention(e, p.cache(), torch.from_numpy(p.table).cuda(),
+                      torch.tensor([5], dtype=torch.int32, device="cuda"))
+    assert out.shape == (0, 8, 128)
+
+
+def test_binding_refusals():
+    p = Problem([50, 60], [1, 1], seed=19)
+    q, c, t = p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda()
+    n = torch.tensor([50, 60], dtype=torch.int32, device="cuda")
+    for bad in (lambda: F.attention(q.float(), c, t, n), lambda: F.attention(q[:, :, :64], c, t, n),
+                lambda: F.attention(q, c, t.long(), n), lambda: F.attention(q, c, t, n.long()),
+                lambda: F.attention(q, c, t, n[:1]), lambda: F.attention(q, c, t.cpu(), n),
+                lambda: F.attention(q.cpu(), c, t, n), lambda: F.attention(q[0], c, t, n),
+                lambda: F.attention(q[:1], c, t, n), lambda: F.attention(q, c, t, n, q_offsets=n),
+                lambda: F.attention(q, c, t, n, sinks=torch.zeros(7, device="cuda")),
+                lambda: F.attention(q, c, t, n, out=torch.empty_like(q, dtype=FP16)),
+                lambda: F.attention(q, c, t, n, lse=torch.empty((2, 7), device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (dict(window=3, causal=False), dict(scale=0.0), dict(scale=float("nan")), dict(window=-1),
+                dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(F.Fp4Error):
+            F.attention(q, c, t, n, **bad)
+    with pytest.raises(F.Fp4Error):
+        F.attention(torch.cat([q, q], 1)[:, :9], c, t, n)
+
+
+@pytest.mark.parametrize("fmt,dtype", [(0, BF16), (1, FP16)])
+def test_projection_cache_attention_projection(fmt, dtype):
+    """The operators as a decode step uses them: an FP4 projection makes q, k
+    and v, the new tokens go into the cache, attention reads it, and an FP4
+    projection follows; each stage against its oracle on the stage's inputs."""
+    B, H, group, D, page, width = 3, 2, 4, 64, 32, 256
+    heads = H * group
+    rng = np.random.Generator(np.random.PCG64(21))
+    p = Problem([33, 70, 5], [1, 1, 1], fmt, dtype, D, H, group, page, seed=20)
+
+    def weight(N, K):
+        w = torch.from_numpy(rng.standard_normal((N, K)).astype(np.float32) * K ** -0.5).to(BF16)
+        codes, scales = oracle.quantize_reference(w.view(torch.int16).numpy().view(np.uint16), fmt)
+        return codes, scales, F.upload(*F.repack(codes, scales, N, K, fmt))
+
+    c1, s1, (w1, z1) = weight((heads + 2 * H) * D, width)
+    c2, s2, (w2, z2) = weight(width, heads * D)
+    x = torch.from_numpy(rng.standard_normal((B, width)).astype(np.float32)).to(dtype).cuda()
+    qkv = F.gemm(x, w1, z1, (heads + 2 * H) * D, width, fmt).reshape(B, heads + 2 * H, D)
+    cache = p.cache()
+    table = torch.from_numpy(p.table).cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32, device="cuda")
+    at = np.array([p.slots(b, np.array([n - 1]))[0] for b, n in enumerate(p.lens)])
+    F.kv_append(cache, qkv[:, heads:heads + H], qkv[:, heads + H:], torch.from_numpy(at).cuda())
+    out, lse = F.attention(qkv[:, :heads], cache, table, lens, scale=p.scale, return_lse=True)
+    y = F.gemm(out.reshape(B, heads * D), w2, z2, width, heads * D, fmt)
+    torch.cuda.synchronize()
+
+    new = qkv[:, heads:].float().cpu().numpy()
+    oracle.kv_write_reference(p.data, at, new[:, :H], new[:, H:], page, fmt)
+    assert np.array_equal(cache.data.cpu().numpy(), p.data)
+    p.k[at], p.v[at] = oracle.kv_read_reference(p.data, at, H, D, page, fmt)
+    p.q = qkv[:, :heads].cpu()
+    p.check((out, lse))
+    bits = lambda t: t.cpu().contiguous().view(torch.int16).numpy().view(np.uint16)  # noqa: E731
+    act = "bf16" if dtype == BF16 else "f16"
+    for a, c, s, K, got in ((x, c1, s1, width, qkv.reshape(B, -1)), (out.reshape(B, -1), c2, s2, heads * D, y)):
+        ref = oracle.act_bits_to_f64(bits(a), act) @ oracle.dequant_weights(c, s, K, fmt).T
+        mag = np.abs(oracle.act_bits_to_f64(bits(a), act)) @ np.abs(oracle.dequant_weights(c, s, K, fmt)).T
+        assert np.all(np.abs(got.double().cpu().numpy() - ref) <= 8e-3 * np.abs(ref) + 2e-3 * mag)
