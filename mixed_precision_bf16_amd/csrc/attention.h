@@ -23,6 +23,9 @@ constexpr float kBias = 8.0f, kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;  // running maximum before the first visible key
 constexpr int kAttnThreads = 256, kAttnWaves = 4;
+// Waves per SIMD that the streaming kernel's registers allow; the GPU then holds
+// 256 times as many of its workgroups (a workgroup has a wave on each SIMD).
+constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1; }
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
 
 // Matrix-core type of a format and activation type (0: BF16, 1: FP16).
@@ -211,10 +214,9 @@ template <int FMT, int ACT, int D>
 struct QueryRow {
     using L = KvTile<FMT, D>;
     static constexpr int kFrags = D / 32;
-    // Fragments of one row's query for lane (r, j); returns the factor that
-    // turns the accumulated products into base-2 scores.
-    __device__ static __forceinline__ float load(u32x4 (&f)[kFrags], const uint16_t* __restrict__ row, bool valid,
-                                                 int j, float scale) {
+    // Raw fragments of one row's query for lane (r, j).
+    __device__ static __forceinline__ void load(u32x4 (&f)[kFrags], const uint16_t* __restrict__ row, bool valid,
+                                                int j) {
         constexpr int S = L::KD / 8;
 #pragma unroll
         for (int c = 0; c < L::C; ++c)
@@ -223,6 +225,11 @@ struct QueryRow {
                 f[c * S + s] = u32x4{0u, 0u, 0u, 0u};
                 if (valid) f[c * S + s] = *reinterpret_cast<const u32x4*>(row + c * L::CH + L::KD * j + 8 * s);
             }
+    }
+    // Converts them to the matrix-core type; returns the factor that turns the
+    // accumulated products into base-2 scores (kept normal: a factor of 0
+    // would turn a hidden key's -Inf into NaN).
+    __device__ static __forceinline__ float convert(u32x4 (&f)[kFrags], float scale) {
         if constexpr (attn_type(FMT, ACT) == 1 && ACT == 0) {
             // BF16 queries on the FP16 matrix cores: a power of two brings the
             // row's largest element to 2^13 .. 2^14, so that every element
@@ -246,9 +253,9 @@ struct QueryRow {
                     const uint32_t p = f[i][x];
                     f[i][x] = pack_out<1>(__uint_as_float(p << 16) * up, __uint_as_float(p & 0xFFFF0000u) * up);
                 }
-            return scale * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+            scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
         }
-        return scale;
+        return fmaxf(scale, 0x1p-126f);
     }
 };
 
@@ -322,14 +329,13 @@ __device__ __forceinline__ float finish_row(float m, float l, bool has_sink, flo
 }
 
 template <int FMT, int ACT, int D, int MT>
-__global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention_stream(AttnArgs a, KvArgs cache) {
+__global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_stream(AttnArgs a, KvArgs cache) {
     using L = KvTile<FMT, D>;
     constexpr int CT = attn_type(FMT, ACT);
     constexpr int R = 16 * MT, F = D / 32, S = L::KD / 8, OT = D / 16;
     constexpr int kPad = D + 4;  // floats of a row in LDS
     __shared__ float lds_o[kAttnWaves][16][kPad];
     __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
-    __shared__ float lds_w[64][16];
     __shared__ int lds_scan[kAttnWaves];
     __shared__ int lds_found[2];
     __shared__ int lds_last;
@@ -338,62 +344,64 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
     const int r = lane & 15, j = lane >> 4;
     const int kv_heads = cache.kv_heads;
 
-    // ---- the workgroup's range of units
-    int total = 0;
-    for (int base = 0; base < a.batch; base += kAttnThreads) {
-        const int b = base + threadIdx.x;
-        int u = 0;
-        if (b < a.batch) {
-            Item x;
-            sequence_of<R>(a, kv_heads, b, x);
-            u = x.units * x.blocks * kv_heads;
-        }
+    // ---- the workgroup's range of units, and the sequence where it begins.
+    // One pass over the sequences for the total, one to find the owner of unit
+    // `begin`; up to kAttnThreads sequences the first pass's counts serve both.
+    auto count = [&](int b) {
+        if (b >= a.batch) return 0;
+        Item x;
+        sequence_of<R>(a, kv_heads, b, x);
+        return x.units * x.blocks * kv_heads;
+    };
+    auto scan = [&](int u, int& sum) {  // exclusive prefix of u over the workgroup, and its sum
+        int inc = u;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) u += __shfl_xor(u, d, 64);
+        for (int d = 1; d < 64; d <<= 1) {
+            const int t = __shfl_up(inc, d, 64);
+            if (lane >= d) inc += t;
+        }
         __syncthreads();
-        if (lane == 0) lds_scan[wave] = u;
+        if (lane == 63) lds_scan[wave] = inc;
         __syncthreads();
-        total += lds_scan[0] + lds_scan[1] + lds_scan[2] + lds_scan[3];
+        int start = inc - u;
+        sum = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) {
+            if (w < wave) start += lds_scan[w];
+            sum += lds_scan[w];
+        }
+        return start;
+    };
+    int total;
+    const int mine = count(threadIdx.x);
+    const int start = scan(mine, total);
+    for (int base = kAttnThreads; base < a.batch; base += kAttnThreads) {
+        int sum;
+        scan(count(base + threadIdx.x), sum);
+        total += sum;
     }
-    if (total == 0) return;
     const int per = (total + a.parts - 1) / a.parts;
     const int begin = blockIdx.x * per;  // parts * per < 2^31 (checked on the host)
     if (begin >= total) return;
     const int end = min(begin + per, total);
-
-    // ---- the sequence that unit `begin` lies in
-    {
-        int before = 0;
-        for (int base = 0; base < a.batch; base += kAttnThreads) {
-            const int b = base + threadIdx.x;
-            int u = 0;
-            if (b < a.batch) {
-                Item x;
-                sequence_of<R>(a, kv_heads, b, x);
-                u = x.units * x.blocks * kv_heads;
-            }
-            int inc = u;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int t = __shfl_up(inc, d, 64);
-                if (lane >= d) inc += t;
-            }
-            __syncthreads();
-            if (lane == 63) lds_scan[wave] = inc;
-            __syncthreads();
-            int start = before + inc - u;
-            for (int w = 0; w < kAttnWaves; ++w) {
-                if (w < wave) start += lds_scan[w];
-                before += lds_scan[w];
-            }
-            if (begin >= start && begin < start + u) {
-                lds_found[0] = b;
-                lds_found[1] = start;
-            }
-            if (before > begin) break;  // the same in every thread
+    if (a.batch <= kAttnThreads) {
+        if (begin >= start && begin < start + mine) {
+            lds_found[0] = threadIdx.x;
+            lds_found[1] = start;
         }
-        __syncthreads();
+    } else {
+        for (int base = 0, before = 0; before <= begin; base += kAttnThreads) {  // ends: begin < total
+            const int n = count(base + threadIdx.x);
+            int sum;
+            const int first = before + scan(n, sum);
+            if (begin >= first && begin < first + n) {
+                lds_found[0] = base + threadIdx.x;
+                lds_found[1] = first;
+            }
+            before += sum;
+        }
     }
+    __syncthreads();
     Item it;
     sequence_of<R>(a, kv_heads, __builtin_amdgcn_readfirstlane(lds_found[0]), it);
     it.first = __builtin_amdgcn_readfirstlane(lds_found[1]);
@@ -416,9 +424,40 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
         const int item_first = unit - skip, item_last = item_first + it.units - 1;
         const int wg0 = item_first / per, wg1 = item_last / per;  // workgroups that share the item
 
-        // ---- query rows
+        // ---- query rows and this wave's tiles.  The page numbers of the next
+        // 64 tiles are one load (lane x: tile x), and the loads of a tile are
+        // under way while the tile before it is computed.
         const int rows = min(R, it.n * a.group - it.rb * R);
+        const int32_t* pages = a.page_table + (int64_t)it.b * a.table_stride;
+        const int ta = it.t0 + skip * kUnitTiles + wave;
+        const int tb = min(it.t0 + (skip + take) * kUnitTiles, it.t1);
+        auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36); };
+        auto load_pages = [&](int t) { return pages[page_of(max(0, min(t + kAttnWaves * lane, tb - 1)))]; };
+        int window_pages = ta < tb ? load_pages(ta) : 0, window_first = ta;
         u32x4 qf[MT][F];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int row = it.rb * R + 16 * mt + r;
+            const bool valid = 16 * mt + r < rows;
+            const int i = row / a.group, g = row - i * a.group;
+            const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(it.h * a.group + g) * a.q_hs;
+            QueryRow<FMT, ACT, D>::load(qf[mt], src, valid, j);
+        }
+        TileRegs<FMT, D> next;
+        bool next_bad = false;
+        auto fetch = [&](int t) {
+            if (t - window_first >= 64 * kAttnWaves) {
+                window_pages = load_pages(t);
+                window_first = t;
+            }
+            int page = __builtin_amdgcn_readlane(window_pages, (t - window_first) / kAttnWaves);
+            next_bad = (uint32_t)page >= (uint32_t)cache.pages;  // no keys there
+            page = next_bad ? 0 : page;
+            const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + it.h) * cache.tiles_per_page +
+                                                (t - page_of(t) * cache.tiles_per_page)) * (int64_t)L::kBytes;
+            load_tile<FMT, D>(next, tile, lane);
+        };
+        if (ta < tb) fetch(ta);
         float fac[MT], m[MT], l[MT];
         RowRange range[MT];
         f32x4 o[MT][OT];
@@ -430,32 +469,18 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int row = it.rb * R + 16 * mt + r;
-            const bool valid = 16 * mt + r < rows;
-            const int i = row / a.group, g = row - i * a.group;
-            const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(it.h * a.group + g) * a.q_hs;
-            // kept normal: a factor of 0 would turn a hidden key's -Inf into NaN
-            fac[mt] = fmaxf(QueryRow<FMT, ACT, D>::load(qf[mt], src, valid, j, a.scale), 0x1p-126f);
-            range[mt] = row_range(i, it.n, it.len, a.causal, a.window);
+            fac[mt] = QueryRow<FMT, ACT, D>::convert(qf[mt], a.scale);
+            range[mt] = row_range((it.rb * R + 16 * mt + r) / a.group, it.n, it.len, a.causal, a.window);
             m[mt] = kNoMax;
             l[mt] = 0.0f;
 #pragma unroll
             for (int x = 0; x < OT; ++x) o[mt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        // ---- this wave's tiles
-        const int32_t* pages = a.page_table + (int64_t)it.b * a.table_stride;
-        const int ta = it.t0 + skip * kUnitTiles + wave;
-        const int tb = min(it.t0 + (skip + take) * kUnitTiles, it.t1);
         for (int t = ta; t < tb; t += kAttnWaves) {
-            const int pi = (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36);
-            int page = __builtin_amdgcn_readfirstlane(pages[pi]);
-            const bool bad = (uint32_t)page >= (uint32_t)cache.pages;  // no keys there
-            page = bad ? 0 : page;
-            const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + it.h) * cache.tiles_per_page +
-                                                (t - pi * cache.tiles_per_page)) * (int64_t)L::kBytes;
-            TileRegs<FMT, D> x;
-            load_tile<FMT, D>(x, tile, lane);
+            TileRegs<FMT, D> x = next;
+            const bool bad = next_bad;
+            if (t + kAttnWaves < tb) fetch(t + kAttnWaves);
             const int tok0 = t * kKvTile;
             const int live = bad ? 0 : it.len;
             const bool edge = bad || tok0 + kKvTile > hi_all || tok0 < lo_all;
@@ -550,9 +575,24 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
 
         // ---- join the four waves, 16 rows at a time
         const bool whole = wg0 == wg1;
+        // partial sums of all workgroups (below 2^28 bytes)
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o, 2 * a.parts * R * D * 4);
+        const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml, 2 * a.parts * R * 8);
         const int slot = 2 * (int)blockIdx.x + (unit == begin ? 0 : 1);
         constexpr int E = D / 16;                       // outputs of a thread: 16 threads a row
         const int orow = threadIdx.x >> 4, od = (threadIdx.x & 15) * E;
+        auto store_row = [&](int mt, int srow, float mx, float lx, const float (&ox)[E]) {
+            const int row = it.rb * R + 16 * mt + srow;
+            const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
+            float lse;
+            const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
+            uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
+#pragma unroll
+            for (int e = 0; e < E; e += 4)
+                *reinterpret_cast<u32x2*>(dst + e) =
+                    u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f), pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
+            if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+        };
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (16 * mt >= rows) break;
@@ -590,29 +630,18 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
             }
             if (16 * mt + orow < rows) {
                 if (whole) {
-                    const int row = it.rb * R + 16 * mt + orow;
-                    const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
-                    float lse;
-                    const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) *
-                                    a.v_alpha;
-                    uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
-#pragma unroll
-                    for (int e = 0; e < E; e += 4)
-                        *reinterpret_cast<u32x2*>(dst + e) =
-                            u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f), pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
-                    if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+                    store_row(mt, orow, mx, lx, ox);
                 } else {
-                    const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o + (size_t)slot * R * D, R * D * 4);
-                    const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml + (size_t)slot * R * 2, R * 8);
+                    const uint32_t row = slot * R + 16 * mt + orow;
 #pragma unroll
                     for (int e = 0; e < E; e += 4) {
                         const f32x4 w = {ox[e], ox[e + 1], ox[e + 2], ox[e + 3]};
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
-                                                               ((16 * mt + orow) * D + od + e) * 4, 0, kDeviceCoherent);
+                                                               (row * D + od + e) * 4, 0, kDeviceCoherent);
                     }
                     if (od == 0)
                         __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(mx), __float_as_uint(lx)}, rm,
-                                                              (16 * mt + orow) * 8, 0, kDeviceCoherent);
+                                                              row * 8, 0, kDeviceCoherent);
                 }
             }
         }
@@ -624,63 +653,76 @@ __global__ __launch_bounds__(kAttnThreads, MT * D >= 512 ? 1 : 2) void attention
             __syncthreads();
             if (lds_last) {
                 asm volatile("" ::: "memory");
-                const int parts = wg1 - wg0 + 1;
                 // slot of the item's part in workgroup wg0 + s: the first range
                 // it fills from its start, unless the item begins inside it
-                auto slot_of = [&](int s) { return 2 * (wg0 + s) + (s == 0 && item_first != wg0 * per ? 1 : 0); };
+                const int parts = wg1 - wg0 + 1, first_slot = 2 * wg0 + (item_first != wg0 * per ? 1 : 0);
 #pragma unroll 1
                 for (int mt = 0; mt < MT; ++mt) {
-                    if (16 * mt >= rows) break;
+                    const int left = rows - 16 * mt;
+                    if (left <= 0) break;
+                    // 16 threads a row; with at most 8 rows the two halves of
+                    // the workgroup take every second batch of parts
+                    const int halves = left <= 8 ? 2 : 1;
+                    const int crow = halves == 2 ? orow & 7 : orow, half = halves == 2 ? orow >> 3 : 0;
+                    constexpr int kBatch = 8;
                     float mx = kNoMax, lx = 0.0f, ox[E];
 #pragma unroll
                     for (int e = 0; e < E; ++e) ox[e] = 0.0f;
-                    for (int s0 = 0; s0 < parts; s0 += 64) {
-                        const int n = min(64, parts - s0);
-                        float top = mx;
-                        __syncthreads();
-                        for (int s = threadIdx.x & 15; s < n; s += 16) {
-                            const __amdgpu_buffer_rsrc_t rm =
-                                make_rsrc(a.ws_ml + (size_t)slot_of(s0 + s) * R * 2, R * 8);
-                            lds_w[s][orow] = __uint_as_float(
-                                __builtin_amdgcn_raw_buffer_load_b32(rm, (16 * mt + orow) * 8, 0, kDeviceCoherent));
-                        }
-                        __syncthreads();
-                        for (int s = 0; s < n; ++s) top = fmaxf(top, lds_w[s][orow]);
-                        const float down = exp2_(mx - top);
-                        mx = top;
-                        lx *= down;
+                    if (crow < left) {
+                        for (int s0 = half * kBatch; s0 < parts; s0 += halves * kBatch) {
+                            u32x2 ml[kBatch];
+                            u32x4 po[kBatch][E / 4];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) ox[e] *= down;
-                        for (int s = 0; s < n; ++s) {
-                            const int sl = slot_of(s0 + s);
-                            const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o + (size_t)sl * R * D, R * D * 4);
-                            const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml + (size_t)sl * R * 2, R * 8);
-                            const float f = exp2_(lds_w[s][orow] - mx);
-                            lx += f * __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                                          rm, (16 * mt + orow) * 8 + 4, 0, kDeviceCoherent));
+                            for (int s = 0; s < kBatch; ++s) {
+                                // past the last part: an offset past the buffer, which reads zeros
+                                const int at = s0 + s;
+                                const uint32_t row = (at == 0 ? first_slot : 2 * (wg0 + at)) * R + 16 * mt + crow;
+                                ml[s] = __builtin_amdgcn_raw_buffer_load_b64(rm, at < parts ? row * 8 : kOutOfRange, 0,
+                                                                             kDeviceCoherent);
 #pragma unroll
-                            for (int e = 0; e < E; e += 4) {
-                                const f32x4 w = __builtin_bit_cast(
-                                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               ro, ((16 * mt + orow) * D + od + e) * 4, 0, kDeviceCoherent));
+                                for (int e = 0; e < E / 4; ++e)
+                                    po[s][e] = __builtin_amdgcn_raw_buffer_load_b128(
+                                        ro, at < parts ? (row * D + od + 4 * e) * 4 : kOutOfRange, 0, kDeviceCoherent);
+                            }
+                            float top = mx;
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) ox[e + y] += f * w[y];
+                            for (int s = 0; s < kBatch; ++s)
+                                if (s0 + s < parts) top = fmaxf(top, __uint_as_float(ml[s].x));
+                            const float down = exp2_(mx - top);
+                            mx = top;
+                            lx *= down;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) ox[e] *= down;
+#pragma unroll
+                            for (int s = 0; s < kBatch; ++s) {
+                                const float f = s0 + s < parts ? exp2_(__uint_as_float(ml[s].x) - mx) : 0.0f;
+                                lx += f * __uint_as_float(ml[s].y);
+#pragma unroll
+                                for (int e = 0; e < E; ++e) ox[e] += f * __uint_as_float(po[s][e / 4][e % 4]);
                             }
                         }
                     }
-                    if (16 * mt + orow < rows) {
-                        const int row = it.rb * R + 16 * mt + orow;
-                        const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
-                        float lse;
-                        const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) *
-                                        a.v_alpha;
-                        uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
+                    __syncthreads();
+                    if (halves == 2) {
+                        if (half == 1) {
 #pragma unroll
-                        for (int e = 0; e < E; e += 4)
-                            *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f),
-                                                                       pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
-                        if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+                            for (int e = 0; e < E; ++e) lds_o[0][crow][od + e] = ox[e];
+                            if (od == 0) {
+                                lds_m[0][crow] = mx;
+                                lds_l[0][crow] = lx;
+                            }
+                        }
+                        __syncthreads();
+                        if (half == 0) {
+                            const float m1 = lds_m[0][crow], top = fmaxf(mx, m1);
+                            const float f0 = exp2_(mx - top), f1 = exp2_(m1 - top);
+                            mx = top;
+                            lx = lx * f0 + lds_l[0][crow] * f1;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) ox[e] = ox[e] * f0 + lds_o[0][crow][od + e] * f1;
+                        }
                     }
+                    if (half == 0 && crow < left) store_row(mt, crow, mx, lx, ox);
                 }
             }
         }

@@ -7,8 +7,6 @@ namespace fp4 {
 int kv_check(const fp4_kv_cache* c, KvArgs* a);  // kv_cache.hip
 bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs);
 
-// Workgroups that the streaming kernel deals its units to: two per CU.
-constexpr int64_t kAttnParts = 512;
 
 struct AttnPlan {
     int MT, parts;
@@ -31,8 +29,10 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t items = (x.q_rows * group / R + x.batch) * c.kv_heads;
     const int64_t unit_keys = kUnitTiles * kKvTile;
     const int64_t units = (x.page_columns * c.page_size + unit_keys - 1) / unit_keys + 1;
-    if (items > (int64_t(1) << 31) || items * units >= (int64_t(1) << 31) - kAttnParts) return FP4_ERR_SHAPE;
-    p->parts = (int)std::max<int64_t>(1, std::min(kAttnParts, items * units));
+    // as many workgroups as the GPU holds at a time
+    const int64_t most = 256 * attn_waves((int)D, p->MT);
+    if (items > (int64_t(1) << 31) || items * units >= (int64_t(1) << 31) - most) return FP4_ERR_SHAPE;
+    p->parts = (int)std::max<int64_t>(1, std::min(most, items * units));
     const size_t slots = 2 * (size_t)p->parts;
     p->ml_off = slots * R * D * 4;
     p->word_off = p->ml_off + slots * R * 8;
