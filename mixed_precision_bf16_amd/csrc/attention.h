@@ -26,6 +26,11 @@ constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // Waves per SIMD that the streaming kernel's registers allow; the GPU then holds
 // 256 times as many of its workgroups (a workgroup has a wave on each SIMD).
 constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1; }
+#ifndef FP4_ITEM_COST
+#define FP4_ITEM_COST 3
+#endif
+constexpr int kItemCost = FP4_ITEM_COST;
+constexpr int kTeam = 16;              // shares of an item that are joined at a time
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
 
 // Matrix-core type of a format and activation type (0: BF16, 1: FP16).
@@ -46,11 +51,12 @@ struct AttnArgs {
     uint64_t tpp_magic;        // ceil(2^36 / tiles_per_page): the page of tile t < 2^26 is t * magic >> 36
     float scale;               // scale * k_alpha * log2(e)
     float v_alpha;
-    int parts;                 // workgroups that the work is dealt to
+    float inv_group;           // 1 / group
+    int grid;                  // workgroups: as many as the GPU holds
     uint32_t tag;
-    float* ws_o;               // [2 * parts][rows][D]
-    float* ws_ml;              // [2 * parts][rows][2]
-    unsigned long long* words; // [parts]
+    float* ws_o;               // [2 * grid][rows][D]
+    float* ws_ml;              // [2 * grid][rows][2]
+    unsigned long long* words; // [2 * grid]
 };
 
 // ------------------------------------------------------------ one key tile
@@ -274,40 +280,56 @@ __device__ __forceinline__ RowRange row_range(int i, int n, int len, int causal,
 
 // ------------------------------------------------------------ streaming kernel
 // Few query rows a sequence (decode, drafted tokens), any number of keys.
-// Work unit: 128 keys (one tile a wave) of one item = (sequence, block of
-// 16 MT query rows, KV head).  All units are numbered sequence by sequence
-// and dealt in equal contiguous ranges to `parts` workgroups, so that long
-// and short sequences load the GPU evenly, whatever the lengths on the device
-// are.  An item whose units fall into several workgroups is joined by the one
-// that arrives last, from the FP32 partial sums of all, in their order.
-struct Item {
-    int b, rb, h, n;       // sequence, row block, KV head, query tokens
-    int q0;                // first query row
-    int len;               // keys
-    int t0, t1;            // tiles [t0, t1) that some query of the sequence sees
-    int units, first;      // units of one item; first unit of the sequence
-    int blocks;            // row blocks
+// An item is a (sequence, block of 16 MT query rows, KV head); its keys are cut
+// into units of 128 (one tile a wave).  All units, with kItemCost places for
+// the fixed cost of each item, are numbered item by item and dealt in equal
+// contiguous ranges to the workgroups that the GPU holds, so that long and
+// short sequences load it evenly, whatever the lengths on the device are.  An
+// item that falls into several workgroups is joined by the one that arrives
+// last, from the FP32 partial sums of all, in their order.
+struct Seq {
+    int q0, n;       // first query row, query tokens
+    int len;         // keys
+    int t0, t1;      // tiles [t0, t1) that some query sees
+    int units;       // of one item
+    int blocks;      // row blocks; 0 for a sequence without queries
 };
 
 template <int R>
-__device__ __forceinline__ void sequence_of(const AttnArgs& a, int kv_heads, int b, Item& x) {
-    int q0, n;
+__device__ __forceinline__ Seq sequence_from(const AttnArgs& a, int q0, int n, int len) {
+    Seq x;
+    x.q0 = q0;
+    x.n = n;
+    x.len = len;
+    const RowRange f = row_range(0, n, len, a.causal, a.window);
+    x.t0 = f.lo / kKvTile;
+    x.t1 = max((len + kKvTile - 1) / kKvTile, x.t0);
+    x.units = max(1, (x.t1 - x.t0 + kUnitTiles - 1) / kUnitTiles);
+    x.blocks = (n * a.group + R - 1) / R;
+    return x;
+}
+
+// Sequence b; one without queries for b past the batch.
+template <int R>
+__device__ __forceinline__ Seq sequence_of(const AttnArgs& a, int b) {
+    if (b >= a.batch) return Seq{};
+    int q0 = b * a.q_each, n = a.q_each;
     if (a.q_offsets) {
         q0 = min(max(a.q_offsets[b], 0), a.q_rows);
         n = min(max(a.q_offsets[b + 1], q0), a.q_rows) - q0;
-    } else {
-        q0 = b * a.q_each;
-        n = a.q_each;
     }
-    x.b = b;
-    x.q0 = q0;
-    x.n = n;
-    x.len = min(max(a.seq_lens[b], 0), a.max_keys);
-    const RowRange f = row_range(0, n, x.len, a.causal, a.window);
-    x.t0 = f.lo / kKvTile;
-    x.t1 = max((x.len + kKvTile - 1) / kKvTile, x.t0);
-    x.units = max(1, (x.t1 - x.t0 + kUnitTiles - 1) / kUnitTiles);
-    x.blocks = (n * a.group + R - 1) / R;  // 0 for a sequence without queries
+    return sequence_from<R>(a, q0, n, min(max(a.seq_lens[b], 0), a.max_keys));
+}
+
+// Sum over lanes 0 .. lane.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2, 3
+    return v;
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -337,110 +359,105 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
     __shared__ float lds_o[kAttnWaves][16][kPad];
     __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
     __shared__ int lds_scan[kAttnWaves];
-    __shared__ int lds_found[2];
+    __shared__ int lds_found[5];
     __shared__ int lds_last;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, j = lane >> 4;
     const int kv_heads = cache.kv_heads;
 
-    // ---- the workgroup's range of units, and the sequence where it begins.
-    // One pass over the sequences for the total, one to find the owner of unit
-    // `begin`; up to kAttnThreads sequences the first pass's counts serve both.
-    auto count = [&](int b) {
-        if (b >= a.batch) return 0;
-        Item x;
-        sequence_of<R>(a, kv_heads, b, x);
-        return x.units * x.blocks * kv_heads;
-    };
+    // ---- units of all sequences, and the shares of each
     auto scan = [&](int u, int& sum) {  // exclusive prefix of u over the workgroup, and its sum
-        int inc = u;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int t = __shfl_up(inc, d, 64);
-            if (lane >= d) inc += t;
-        }
+        int p = wave_scan(u);
         __syncthreads();
-        if (lane == 63) lds_scan[wave] = inc;
+        if (lane == 63) lds_scan[wave] = p;
         __syncthreads();
-        int start = inc - u;
+        p -= u;
         sum = 0;
 #pragma unroll
         for (int w = 0; w < kAttnWaves; ++w) {
-            if (w < wave) start += lds_scan[w];
+            p += w < wave ? lds_scan[w] : 0;
             sum += lds_scan[w];
         }
-        return start;
+        return p;
     };
+    // A position is a unit or one of the kItemCost places before an item's units.
+    auto cost = [&](const Seq& x) { return (x.units + kItemCost) * x.blocks * kv_heads; };
+    const Seq own = sequence_of<R>(a, threadIdx.x);
+    const int own_cost = cost(own);
     int total;
-    const int mine = count(threadIdx.x);
-    const int start = scan(mine, total);
+    const int own_first = scan(own_cost, total);
     for (int base = kAttnThreads; base < a.batch; base += kAttnThreads) {
         int sum;
-        scan(count(base + threadIdx.x), sum);
+        scan(cost(sequence_of<R>(a, base + threadIdx.x)), sum);
         total += sum;
     }
-    const int per = (total + a.parts - 1) / a.parts;
-    const int begin = blockIdx.x * per;  // parts * per < 2^31 (checked on the host)
+    const int per = (total + a.grid - 1) / a.grid;
+    const int begin = blockIdx.x * per;  // grid * per < 2^31 (checked on the host)
     if (begin >= total) return;
     const int end = min(begin + per, total);
+
+    // ---- the sequence that position `begin` lies in
+    auto found = [&](const Seq& x, int b, int first) {
+        lds_found[0] = b;
+        lds_found[1] = x.q0;
+        lds_found[2] = x.n;
+        lds_found[3] = x.len;
+        lds_found[4] = first;
+    };
     if (a.batch <= kAttnThreads) {
-        if (begin >= start && begin < start + mine) {
-            lds_found[0] = threadIdx.x;
-            lds_found[1] = start;
-        }
+        if (begin >= own_first && begin < own_first + own_cost) found(own, threadIdx.x, own_first);
     } else {
         for (int base = 0, before = 0; before <= begin; base += kAttnThreads) {  // ends: begin < total
-            const int n = count(base + threadIdx.x);
+            const Seq x = sequence_of<R>(a, base + threadIdx.x);
+            const int n = cost(x);
             int sum;
             const int first = before + scan(n, sum);
-            if (begin >= first && begin < first + n) {
-                lds_found[0] = base + threadIdx.x;
-                lds_found[1] = first;
-            }
+            if (begin >= first && begin < first + n) found(x, base + threadIdx.x, first);
             before += sum;
         }
     }
     __syncthreads();
-    Item it;
-    sequence_of<R>(a, kv_heads, __builtin_amdgcn_readfirstlane(lds_found[0]), it);
-    it.first = __builtin_amdgcn_readfirstlane(lds_found[1]);
+    int b = __builtin_amdgcn_readfirstlane(lds_found[0]);
+    int seq_first = __builtin_amdgcn_readfirstlane(lds_found[4]);
+    Seq it = sequence_from<R>(a, __builtin_amdgcn_readfirstlane(lds_found[1]),
+                              __builtin_amdgcn_readfirstlane(lds_found[2]),
+                              __builtin_amdgcn_readfirstlane(lds_found[3]));
+    int item = (begin - seq_first) / (it.units + kItemCost);
 
-    int unit = begin;
-    while (unit < end) {
-        const int seq_units = it.units * it.blocks * kv_heads;
-        if (unit >= it.first + seq_units) {  // the next sequence that has work
-            const int first = it.first + seq_units;
-            sequence_of<R>(a, kv_heads, it.b + 1, it);  // units remain, so there is one
-            it.first = first;
-            continue;
+    for (;; ++item) {
+        while (item >= it.blocks * kv_heads) {  // the next sequence that has work
+            seq_first += cost(it);
+            if (seq_first >= end) return;
+            it = sequence_of<R>(a, ++b);  // positions remain, so there is one
+            item = 0;
         }
-        const int in_seq = unit - it.first;
-        const int item = in_seq / it.units;           // (row block, head): heads of a block are neighbours
-        const int skip = in_seq - item * it.units;    // units of the item that earlier workgroups take
-        it.rb = item / kv_heads;
-        it.h = item - it.rb * kv_heads;
-        const int take = min(it.units - skip, end - unit);
-        const int item_first = unit - skip, item_last = item_first + it.units - 1;
-        const int wg0 = item_first / per, wg1 = item_last / per;  // workgroups that share the item
+        const int unit0 = seq_first + item * (it.units + kItemCost) + kItemCost;  // position of the item's first unit
+        const int u0 = max(begin - unit0, 0), u1 = min(end - unit0, it.units);
+        if (unit0 >= end) return;
+        if (u0 >= u1) continue;
+        const int rb = item / kv_heads, h = item - rb * kv_heads;  // heads of a row block are neighbours
+        const int wg0 = unit0 / per, parts = (unit0 + it.units - 1) / per - wg0 + 1, part = (int)blockIdx.x - wg0;
 
         // ---- query rows and this wave's tiles.  The page numbers of the next
         // 64 tiles are one load (lane x: tile x), and the loads of a tile are
         // under way while the tile before it is computed.
-        const int rows = min(R, it.n * a.group - it.rb * R);
-        const int32_t* pages = a.page_table + (int64_t)it.b * a.table_stride;
-        const int ta = it.t0 + skip * kUnitTiles + wave;
-        const int tb = min(it.t0 + (skip + take) * kUnitTiles, it.t1);
+        const int rows = min(R, it.n * a.group - rb * R);
+        const int32_t* pages = a.page_table + (int64_t)b * a.table_stride;
+        const int ta = it.t0 + u0 * kUnitTiles + wave;
+        const int tb = min(it.t0 + u1 * kUnitTiles, it.t1);
         auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36); };
         auto load_pages = [&](int t) { return pages[page_of(max(0, min(t + kAttnWaves * lane, tb - 1)))]; };
         int window_pages = ta < tb ? load_pages(ta) : 0, window_first = ta;
+        // row x of the block: token i0 + (x + g0) / group (below 2^11: exact in FP32)
+        const int i0 = rb * R / a.group, g0 = rb * R - i0 * a.group;
+        auto token_of = [&](int x) { return (int)(((float)(x + g0) + 0.5f) * a.inv_group); };
         u32x4 qf[MT][F];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int row = it.rb * R + 16 * mt + r;
             const bool valid = 16 * mt + r < rows;
-            const int i = row / a.group, g = row - i * a.group;
-            const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(it.h * a.group + g) * a.q_hs;
+            const int di = token_of(16 * mt + r), i = i0 + di, g = 16 * mt + r + g0 - di * a.group;
+            const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs;
             QueryRow<FMT, ACT, D>::load(qf[mt], src, valid, j);
         }
         TileRegs<FMT, D> next;
@@ -453,7 +470,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             int page = __builtin_amdgcn_readlane(window_pages, (t - window_first) / kAttnWaves);
             next_bad = (uint32_t)page >= (uint32_t)cache.pages;  // no keys there
             page = next_bad ? 0 : page;
-            const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + it.h) * cache.tiles_per_page +
+            const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + h) * cache.tiles_per_page +
                                                 (t - page_of(t) * cache.tiles_per_page)) * (int64_t)L::kBytes;
             load_tile<FMT, D>(next, tile, lane);
         };
@@ -463,14 +480,14 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         f32x4 o[MT][OT];
         int lo_all = 0, hi_all = it.len;  // keys that every valid row sees
         {
-            const int i0 = it.rb * R / a.group, i1 = (it.rb * R + rows - 1) / a.group;
+            const int i1 = i0 + __builtin_amdgcn_readfirstlane(token_of(rows - 1));
             hi_all = row_range(i0, it.n, it.len, a.causal, a.window).hi;
             lo_all = row_range(i1, it.n, it.len, a.causal, a.window).lo;
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             fac[mt] = QueryRow<FMT, ACT, D>::convert(qf[mt], a.scale);
-            range[mt] = row_range((it.rb * R + 16 * mt + r) / a.group, it.n, it.len, a.causal, a.window);
+            range[mt] = row_range(i0 + token_of(16 * mt + r), it.n, it.len, a.causal, a.window);
             m[mt] = kNoMax;
             l[mt] = 0.0f;
 #pragma unroll
@@ -574,16 +591,15 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         }
 
         // ---- join the four waves, 16 rows at a time
-        const bool whole = wg0 == wg1;
+        const bool whole = parts == 1;
         // partial sums of all workgroups (below 2^28 bytes)
-        const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o, 2 * a.parts * R * D * 4);
-        const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml, 2 * a.parts * R * 8);
-        const int slot = 2 * (int)blockIdx.x + (unit == begin ? 0 : 1);
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o, 2 * a.grid * R * D * 4);
+        const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml, 2 * a.grid * R * 8);
         constexpr int E = D / 16;                       // outputs of a thread: 16 threads a row
         const int orow = threadIdx.x >> 4, od = (threadIdx.x & 15) * E;
         auto store_row = [&](int mt, int srow, float mx, float lx, const float (&ox)[E]) {
-            const int row = it.rb * R + 16 * mt + srow;
-            const int i = row / a.group, head = it.h * a.group + (row - i * a.group);
+            const int di = token_of(16 * mt + srow), i = i0 + di;
+            const int head = h * a.group + 16 * mt + srow + g0 - di * a.group;
             float lse;
             const float f = finish_row(mx, lx, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
             uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs + od;
@@ -592,6 +608,21 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                 *reinterpret_cast<u32x2*>(dst + e) =
                     u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f), pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
             if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+        };
+        // Partial sums: an item that goes on in the next workgroup is the last of
+        // its first one (slot 2 wg0 + 1) and the first of the others.
+        auto slot_of = [&](int p) { return 2 * (wg0 + p) + (p == 0 ? 1 : 0); };
+        auto keep_row = [&](int slot, int row, float mx, float lx, const float (&ox)[E]) {
+            const uint32_t at = slot * R + row;
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const f32x4 w = {ox[e], ox[e + 1], ox[e + 2], ox[e + 3]};
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro, (at * D + od + e) * 4, 0,
+                                                       kDeviceCoherent);
+            }
+            if (od == 0)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(mx), __float_as_uint(lx)}, rm, at * 8, 0,
+                                                      kDeviceCoherent);
         };
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -632,62 +663,56 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                 if (whole) {
                     store_row(mt, orow, mx, lx, ox);
                 } else {
-                    const uint32_t row = slot * R + 16 * mt + orow;
-#pragma unroll
-                    for (int e = 0; e < E; e += 4) {
-                        const f32x4 w = {ox[e], ox[e + 1], ox[e + 2], ox[e + 3]};
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
-                                                               (row * D + od + e) * 4, 0, kDeviceCoherent);
-                    }
-                    if (od == 0)
-                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(mx), __float_as_uint(lx)}, rm,
-                                                              row * 8, 0, kDeviceCoherent);
+                    keep_row(slot_of(part), 16 * mt + orow, mx, lx, ox);
                 }
             }
         }
         if (!whole) {
-            // As split_finish: this thread's stores are complete, then one arrival.
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            if (threadIdx.x == 0) lds_last = split_arrive(a.words + wg0, a.tag, wg1 - wg0 + 1);
-            __syncthreads();
-            if (lds_last) {
+            // ---- join the shares of the item: sixteen by their last workgroup, and
+            // where there are more than sixteen, those sums by the last of all
+            // as split_finish: this thread's stores are complete, then one arrival
+            auto arrive = [&](int word, int count) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+                if (threadIdx.x == 0) lds_last = split_arrive(a.words + word, a.tag, count);
+                __syncthreads();
                 asm volatile("" ::: "memory");
-                // slot of the item's part in workgroup wg0 + s: the first range
-                // it fills from its start, unless the item begins inside it
-                const int parts = wg1 - wg0 + 1, first_slot = 2 * wg0 + (item_first != wg0 * per ? 1 : 0);
+                return lds_last != 0;
+            };
+            // sum of `count` parts from p0 on, `step` apart, in their order
+            auto join = [&](int p0, int step, int count, bool last) {
 #pragma unroll 1
                 for (int mt = 0; mt < MT; ++mt) {
                     const int left = rows - 16 * mt;
                     if (left <= 0) break;
-                    // 16 threads a row; with at most 8 rows the two halves of
-                    // the workgroup take every second batch of parts
+                    // 16 threads a row; with at most 8 rows the two halves of the
+                    // workgroup take every second batch of slots
                     const int halves = left <= 8 ? 2 : 1;
                     const int crow = halves == 2 ? orow & 7 : orow, half = halves == 2 ? orow >> 3 : 0;
-                    constexpr int kBatch = 8;
+                    constexpr int kBatch = D == 256 ? 4 : 8;
                     float mx = kNoMax, lx = 0.0f, ox[E];
 #pragma unroll
                     for (int e = 0; e < E; ++e) ox[e] = 0.0f;
                     if (crow < left) {
-                        for (int s0 = half * kBatch; s0 < parts; s0 += halves * kBatch) {
+                        for (int s0 = half * kBatch; s0 < count; s0 += halves * kBatch) {
                             u32x2 ml[kBatch];
                             u32x4 po[kBatch][E / 4];
 #pragma unroll
                             for (int s = 0; s < kBatch; ++s) {
-                                // past the last part: an offset past the buffer, which reads zeros
-                                const int at = s0 + s;
-                                const uint32_t row = (at == 0 ? first_slot : 2 * (wg0 + at)) * R + 16 * mt + crow;
-                                ml[s] = __builtin_amdgcn_raw_buffer_load_b64(rm, at < parts ? row * 8 : kOutOfRange, 0,
+                                // past the last slot: an offset past the buffer, which reads zeros
+                                const bool there = s0 + s < count;
+                                const uint32_t at = slot_of(p0 + (s0 + s) * step) * R + 16 * mt + crow;
+                                ml[s] = __builtin_amdgcn_raw_buffer_load_b64(rm, there ? at * 8 : kOutOfRange, 0,
                                                                              kDeviceCoherent);
 #pragma unroll
                                 for (int e = 0; e < E / 4; ++e)
                                     po[s][e] = __builtin_amdgcn_raw_buffer_load_b128(
-                                        ro, at < parts ? (row * D + od + 4 * e) * 4 : kOutOfRange, 0, kDeviceCoherent);
+                                        ro, there ? (at * D + od + 4 * e) * 4 : kOutOfRange, 0, kDeviceCoherent);
                             }
                             float top = mx;
 #pragma unroll
                             for (int s = 0; s < kBatch; ++s)
-                                if (s0 + s < parts) top = fmaxf(top, __uint_as_float(ml[s].x));
+                                if (s0 + s < count) top = fmaxf(top, __uint_as_float(ml[s].x));
                             const float down = exp2_(mx - top);
                             mx = top;
                             lx *= down;
@@ -695,10 +720,10 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                             for (int e = 0; e < E; ++e) ox[e] *= down;
 #pragma unroll
                             for (int s = 0; s < kBatch; ++s) {
-                                const float f = s0 + s < parts ? exp2_(__uint_as_float(ml[s].x) - mx) : 0.0f;
-                                lx += f * __uint_as_float(ml[s].y);
+                                const float w = s0 + s < count ? exp2_(__uint_as_float(ml[s].x) - mx) : 0.0f;
+                                lx += w * __uint_as_float(ml[s].y);
 #pragma unroll
-                                for (int e = 0; e < E; ++e) ox[e] += f * __uint_as_float(po[s][e / 4][e % 4]);
+                                for (int e = 0; e < E; ++e) ox[e] += w * __uint_as_float(po[s][e / 4][e % 4]);
                             }
                         }
                     }
@@ -722,11 +747,19 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                             for (int e = 0; e < E; ++e) ox[e] = ox[e] * f0 + lds_o[0][crow][od + e] * f1;
                         }
                     }
-                    if (half == 0 && crow < left) store_row(mt, crow, mx, lx, ox);
+                    if (half == 0 && crow < left) {
+                        if (last) store_row(mt, crow, mx, lx, ox);
+                        else keep_row(slot_of(p0), 16 * mt + crow, mx, lx, ox);  // its own reads of the slot are done
+                    }
                 }
+            };
+            const int p0 = part / kTeam * kTeam, teams = (parts + kTeam - 1) / kTeam, size = min(kTeam, parts - p0);
+            // words: the slot of the team's first part; for the teams, that of part 1
+            if (arrive(slot_of(p0), size)) {
+                join(p0, 1, size, teams == 1);
+                if (teams > 1 && arrive(slot_of(1), teams)) join(0, kTeam, teams, true);
             }
         }
-        unit += take;
     }
 }
 

@@ -9,7 +9,7 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs
 
 
 struct AttnPlan {
-    int MT, parts;
+    int MT, grid;
     size_t ml_off, word_off, ws_bytes;
 };
 
@@ -31,12 +31,12 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t units = (x.page_columns * c.page_size + unit_keys - 1) / unit_keys + 1;
     // as many workgroups as the GPU holds at a time
     const int64_t most = 256 * attn_waves((int)D, p->MT);
-    if (items > (int64_t(1) << 31) || items * units >= (int64_t(1) << 31) - most) return FP4_ERR_SHAPE;
-    p->parts = (int)std::max<int64_t>(1, std::min(most, items * units));
-    const size_t slots = 2 * (size_t)p->parts;
+    if (items > (int64_t(1) << 30) || items * (units + kItemCost) >= (int64_t(1) << 31) - most) return FP4_ERR_SHAPE;
+    p->grid = (int)std::max<int64_t>(1, std::min(most, items * units));
+    const size_t slots = 2 * (size_t)p->grid;
     p->ml_off = slots * R * D * 4;
     p->word_off = p->ml_off + slots * R * 8;
-    p->ws_bytes = p->word_off + (size_t)p->parts * 8;
+    p->ws_bytes = p->word_off + slots * 8;
     return FP4_OK;
 }
 
@@ -102,7 +102,8 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.tpp_magic = ((uint64_t(1) << 36) + c.tiles_per_page - 1) / c.tiles_per_page;
     a.scale = x->scale * c.k_alpha * kLog2e;
     a.v_alpha = c.v_alpha;
-    a.parts = p.parts;
+    a.inv_group = 1.0f / a.group;
+    a.grid = p.grid;
     a.tag = next_split_tag();
     char* ws = static_cast<char*>(x->workspace);
     a.ws_o = reinterpret_cast<float*>(ws);
