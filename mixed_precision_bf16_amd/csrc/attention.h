@@ -30,6 +30,7 @@ constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 12
 #define FP4_ITEM_COST 3
 #endif
 constexpr int kItemCost = FP4_ITEM_COST;
+constexpr int kTiledRows = 128;        // query rows of a workgroup of the tiled kernel
 constexpr int kTeam = 16;              // shares of an item that are joined at a time
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
 
@@ -68,6 +69,14 @@ struct TileRegs {
     u32x2 vs[L::C];
 };
 
+// Offset of lane (r, j)'s key scales in their section: lanes j of one scale
+// block (two, where a block is longer than a lane's elements) share them.
+template <int FMT, int D>
+__device__ __forceinline__ int key_scale_lane(int r, int j) {
+    using L = KvTile<FMT, D>;
+    return (j * L::KD / (L::G > L::KD ? L::G : L::KD) * 16 + r) * L::kKsLane;
+}
+
 template <int FMT, int D>
 __device__ __forceinline__ void load_tile(TileRegs<FMT, D>& t, const uint8_t* __restrict__ tile, int lane) {
     using L = KvTile<FMT, D>;
@@ -76,7 +85,7 @@ __device__ __forceinline__ void load_tile(TileRegs<FMT, D>& t, const uint8_t* __
     for (int f = 0; f < L::F; ++f) t.k[f] = *reinterpret_cast<const u32x4*>(tile + f * 1024 + lane * 16);
 #pragma unroll
     for (int f = 0; f < L::F; ++f) t.v[f] = *reinterpret_cast<const u32x4*>(tile + L::kCodes + f * 1024 + lane * 16);
-    const uint8_t* ks = tile + L::kKs + ((j * L::KD / (L::KG * L::G > L::KD ? L::G : L::KD)) * 16 + r) * L::kKsLane;
+    const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j);
     if constexpr (L::kKsLane == 2) t.ks[0] = *reinterpret_cast<const uint16_t*>(ks);
     else if constexpr (L::kKsLane == 4) t.ks[0] = *reinterpret_cast<const uint32_t*>(ks);
     else {
@@ -763,14 +772,341 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
     }
 }
 
+// ------------------------------------------------------------ tiled kernel
+// Many query rows a sequence (prompts, chunks).  A workgroup takes 16 MT rows
+// a wave of one (sequence, row block, KV head) and walks over the keys in
+// steps of TT tiles.  Each key and value is dequantized once per workgroup:
+// the waves share a step's fragments through LDS, where a fragment is the
+// 1 KiB that a wave reads with one 16-byte load a lane, without bank
+// conflicts.  Two LDS buffers and one barrier a step: while step i is
+// multiplied, step i + 1 is dequantized into the other buffer and the codes of
+// step i + 2 are loaded.  Scores, softmax and probabilities stay in registers,
+// as in the streaming kernel.
+template <int FMT, int D, int WPT>
+struct TilePart {  // what one of the WPT waves of a tile dequantizes
+    using L = KvTile<FMT, D>;
+    static constexpr int KF = D == 64 ? 1 : (WPT == 4 ? 1 : L::C);  // key fragments of 1 KiB that it loads
+    static constexpr int VF = D == 64 ? 1 : (WPT == 4 ? 2 : L::F);
+    static constexpr int VC = WPT == 4 ? 1 : L::C;
+    u32x4 k[KF], v[VF];
+    uint32_t ks[(L::kKsLane + 3) / 4];
+    u32x2 vs[VC];
+};
+
+template <int FMT, int ACT, int D, int MT, int NW, int TT>
+__global__ __launch_bounds__(64 * NW) void attention_tiled(AttnArgs a, KvArgs cache) {
+    using L = KvTile<FMT, D>;
+    constexpr int CT = attn_type(FMT, ACT);
+    constexpr int R = 16 * MT * NW, F = D / 32, S = L::KD / 8, OT = D / 16, WPT = NW / TT;
+    static_assert(WPT == 2 || (WPT == 4 && L::C == 2), "a tile is dequantized by two waves, or by two for each chunk");
+    constexpr int kTileFrags = 2 * F + OT;  // 1 KiB fragments of a tile
+    __shared__ u32x4 lds[2][TT][kTileFrags][64];
+    __shared__ int lds_scan[NW], lds_found[5];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, j = lane >> 4;
+    const int kv_heads = cache.kv_heads;
+
+    // ---- the item: sequences in order, their last row blocks (the longest
+    // ones) first, the KV heads of a block next to each other
+    {
+        int before = 0;
+        bool there = false;
+        for (int base = 0; base < a.batch && !there; base += 64 * NW) {
+            const int b = base + threadIdx.x;
+            Seq x = sequence_of<R>(a, b);
+            const int n = x.blocks * kv_heads;
+            int p = wave_scan(n);
+            __syncthreads();
+            if (lane == 63) lds_scan[wave] = p;
+            __syncthreads();
+            p += before - n;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                p += w < wave ? lds_scan[w] : 0;
+                before += lds_scan[w];
+            }
+            if ((int)blockIdx.x >= p && (int)blockIdx.x < p + n) {
+                lds_found[0] = b;
+                lds_found[1] = x.q0;
+                lds_found[2] = x.n;
+                lds_found[3] = x.len;
+                lds_found[4] = p;
+            }
+            there = (int)blockIdx.x < before;  // the same in every thread
+        }
+        if (!there) return;
+        __syncthreads();
+    }
+    const int b = __builtin_amdgcn_readfirstlane(lds_found[0]);
+    const Seq it = sequence_from<R>(a, __builtin_amdgcn_readfirstlane(lds_found[1]),
+                                    __builtin_amdgcn_readfirstlane(lds_found[2]),
+                                    __builtin_amdgcn_readfirstlane(lds_found[3]));
+    const int item = (int)blockIdx.x - __builtin_amdgcn_readfirstlane(lds_found[4]);
+    const int rb = it.blocks - 1 - item / kv_heads, h = item % kv_heads;
+    const int rows = min(R, it.n * a.group - rb * R);
+    const int i0 = rb * R / a.group, g0 = rb * R - i0 * a.group;
+    auto token_of = [&](int x) { return (int)(((float)(x + g0) + 0.5f) * a.inv_group); };
+    auto range_of = [&](int x) { return row_range(i0 + token_of(x), it.n, it.len, a.causal, a.window); };
+    const int last_hi = __builtin_amdgcn_readfirstlane(range_of(rows - 1).hi);
+    const int first_lo = __builtin_amdgcn_readfirstlane(range_of(0).lo);
+    const int t0 = first_lo / kKvTile, t1 = (min(last_hi, it.len) + kKvTile - 1) / kKvTile;
+    const int steps = max(0, (t1 - t0 + TT - 1) / TT);
+
+    // ---- query rows of this wave
+    const int my0 = wave * 16 * MT;
+    u32x4 qf[MT][F];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int x = my0 + 16 * mt + r, di = token_of(x), i = i0 + di, g = x + g0 - di * a.group;
+        const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs;
+        QueryRow<FMT, ACT, D>::load(qf[mt], src, x < rows, j);
+    }
+
+    // ---- loads of this wave's part of a step
+    const int32_t* pages = a.page_table + (int64_t)b * a.table_stride;
+    const int my_tile = wave / WPT, sub = wave % WPT;
+    auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36); };
+    auto load_pages = [&](int t) { return pages[page_of(max(0, min(t + lane, t1 - 1)))]; };
+    int window_pages = steps > 0 ? load_pages(t0) : 0, window_first = t0;
+    TilePart<FMT, D, WPT> raw;
+    int raw_bad = 0, raw_clear = 0;  // tiles of the step without keys; whether this wave's tile runs past them
+    auto fetch = [&](int step) {
+        const int ts = t0 + step * TT;
+        if (ts + TT - window_first > 64) {
+            window_pages = load_pages(ts);
+            window_first = ts;
+        }
+        raw_bad = 0;
+        int page = 0;
+#pragma unroll
+        for (int x = 0; x < TT; ++x) {
+            const int p = __builtin_amdgcn_readlane(window_pages, ts + x - window_first);
+            const bool bad = ts + x >= t1 || (uint32_t)p >= (uint32_t)cache.pages;
+            raw_bad |= bad ? 1 << x : 0;
+            if (x == my_tile) page = bad ? 0 : p;
+        }
+        const int t = min(ts + my_tile, t1 - 1);
+        raw_clear = (raw_bad >> my_tile & 1) || (t + 1) * kKvTile > it.len;
+        const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + h) * cache.tiles_per_page +
+                                            (t - page_of(t) * cache.tiles_per_page)) * (int64_t)L::kBytes;
+        using P = TilePart<FMT, D, WPT>;
+        const int u = sub & 1, c = sub >> 1;
+#pragma unroll
+        for (int f = 0; f < P::KF; ++f)
+            raw.k[f] = *reinterpret_cast<const u32x4*>(tile + (D == 64 ? 0 : (WPT == 4 ? c : f) * 2 + u) * 1024 +
+                                                       lane * 16);
+#pragma unroll
+        for (int f = 0; f < P::VF; ++f)
+            raw.v[f] = *reinterpret_cast<const u32x4*>(tile + L::kCodes + (WPT == 4 ? c * 2 + f : f) * 1024 + lane * 16);
+        const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j);
+        if constexpr (L::kKsLane == 2) raw.ks[0] = *reinterpret_cast<const uint16_t*>(ks);
+        else if constexpr (L::kKsLane == 4) raw.ks[0] = *reinterpret_cast<const uint32_t*>(ks);
+        else {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(ks);
+            raw.ks[0] = w.x;
+            raw.ks[1] = w.y;
+        }
+#pragma unroll
+        for (int x = 0; x < P::VC; ++x) {
+            const int g = (WPT == 4 ? c : x) * (L::CH / L::G) + r * L::VD / L::G;
+            raw.vs[x] = *reinterpret_cast<const u32x2*>(tile + L::kVs + (g * 4 + j) * 8);
+        }
+    };
+    // raw -> fragments in LDS buffer `buf`; `step` is the step that raw holds
+    auto spread = [&](int buf, int step) {
+        using P = TilePart<FMT, D, WPT>;
+        u32x4(*out)[64] = lds[buf][my_tile];
+        TileRegs<FMT, D> x;  // only what this wave loaded is used
+#pragma unroll
+        for (int c = 0; c < L::C; ++c) x.vs[c] = raw.vs[WPT == 4 ? 0 : c];
+#pragma unroll
+        for (int e = 0; e < (L::kKsLane + 3) / 4; ++e) x.ks[e] = raw.ks[e];
+        if (raw_clear) {
+            const int tok0 = (t0 + step * TT + my_tile) * kKvTile;
+            clear_values<FMT, D>(x, tok0, j, (raw_bad >> my_tile & 1) ? 0 : it.len);
+        }
+        auto part = [&](auto uc, auto cc) {  // keys of tokens 16 u ..; half u of the value elements
+            constexpr int u = decltype(uc)::value, c = decltype(cc)::value;
+            constexpr int kf = D == 64 ? 0 : (WPT == 4 ? 0 : c), vf = D == 64 ? 0 : (WPT == 4 ? 0 : c * 2);
+            if constexpr (D == 64) {
+                x.k[0] = raw.k[0];
+                x.v[0] = raw.v[0];
+            } else {
+                x.k[c * 2 + u] = raw.k[kf];
+                x.v[c * 2] = raw.v[vf];
+                x.v[c * 2 + 1] = raw.v[vf + 1];
+            }
+            auto key = [&](auto sc) {
+                constexpr int s = decltype(sc)::value;
+                out[u * F + c * S + s][lane] = key_step<FMT, CT, D, u, c, s>(x);
+            };
+            key(std::integral_constant<int, 0>{});
+            key(std::integral_constant<int, 1>{});
+            if constexpr (S == 4) {
+                key(std::integral_constant<int, 2>{});
+                key(std::integral_constant<int, 3>{});
+            }
+            auto value = [&](auto qc) {
+                constexpr int q = decltype(qc)::value;
+                u32x4 even, odd;
+                value_frags<FMT, CT, D, c, q>(x, even, odd);
+                out[2 * F + c * L::VD + 2 * q][lane] = even;
+                out[2 * F + c * L::VD + 2 * q + 1][lane] = odd;
+            };
+            constexpr int Q = L::VD / 4;  // pairs of value elements of half a chunk
+            value(std::integral_constant<int, u * Q>{});
+            if constexpr (Q == 2) value(std::integral_constant<int, u * Q + 1>{});
+        };
+        auto chunk = [&](auto uc) {
+            if constexpr (WPT == 4) {
+                if (sub >> 1) part(uc, std::integral_constant<int, 1>{});
+                else part(uc, std::integral_constant<int, 0>{});
+            } else {
+                part(uc, std::integral_constant<int, 0>{});
+                if constexpr (L::C == 2) part(uc, std::integral_constant<int, 1>{});
+            }
+        };
+        if (sub & 1) chunk(std::integral_constant<int, 1>{});
+        else chunk(std::integral_constant<int, 0>{});
+    };
+
+    if (steps > 0) fetch(0);
+    float fac[MT], m[MT], l[MT];
+    RowRange range[MT];
+    f32x4 o[MT][OT];
+    const int my_rows = min(16 * MT, rows - my0);  // may be below 1
+    const int hi_all = __builtin_amdgcn_readfirstlane(range_of(min(my0, rows - 1)).hi);
+    const int lo_all = __builtin_amdgcn_readfirstlane(range_of(max(0, my0 + max(my_rows, 1) - 1)).lo);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        fac[mt] = QueryRow<FMT, ACT, D>::convert(qf[mt], a.scale);
+        range[mt] = range_of(my0 + 16 * mt + r);
+        m[mt] = kNoMax;
+        l[mt] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < OT; ++x) o[mt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    int cur_bad = 0;
+    if (steps > 0) {
+        spread(0, 0);
+        cur_bad = raw_bad;
+        if (steps > 1) fetch(1);
+    }
+
+    for (int step = 0; step < steps; ++step) {
+        __syncthreads();  // buffer `step` is written, the other one is read out
+        const int buf = step & 1, tok0 = (t0 + step * TT) * kKvTile;
+        const u32x4(*in)[kTileFrags][64] = lds[buf];
+        f32x4 sc[MT][2 * TT];
+#pragma unroll
+        for (int x = 0; x < TT; ++x)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) sc[mt][2 * x + u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const u32x4 kf = in[x][u * F + f][lane];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) sc[mt][2 * x + u] = mfma<CT>(kf, qf[mt][f], sc[mt][2 * x + u]);
+                }
+            }
+        const bool edge = cur_bad || tok0 + TT * kKvTile > hi_all || tok0 < lo_all;
+        const int bad = cur_bad;
+        if (step + 1 < steps) {
+            spread(buf ^ 1, step + 1);
+            cur_bad = raw_bad;
+            if (step + 2 < steps) fetch(step + 2);
+        }
+
+        u32x4 pf[MT][TT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (edge) {
+#pragma unroll
+                for (int e = 0; e < 8 * TT; ++e) {
+                    const int tok = tok0 + 16 * (e >> 2) + 4 * j + (e & 3);
+                    const bool see = tok >= range[mt].lo && tok < range[mt].hi && tok < it.len && !(bad >> (e >> 3) & 1);
+                    if (!see) sc[mt][e >> 2][e & 3] = -__builtin_inff();
+                }
+            }
+            float top = sc[mt][0][0];
+#pragma unroll
+            for (int e = 1; e < 8 * TT; ++e) top = fmaxf(top, sc[mt][e >> 2][e & 3]);
+            top *= fac[mt];
+            if (__any(top > m[mt] + kSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float mn = fmaxf(m[mt], top);
+                const float down = exp2_(m[mt] - mn);
+                m[mt] = mn;
+                l[mt] *= down;
+#pragma unroll
+                for (int y = 0; y < OT; ++y) o[mt][y] *= down;
+            }
+            const float off = kBias - m[mt];
+#pragma unroll
+            for (int x = 0; x < TT; ++x) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = exp2_(fmaf(sc[mt][2 * x + (e >> 2)][e & 3], fac[mt], off));
+                    l[mt] += p[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pf[mt][x][e] = pack_out<CT>(p[2 * e], p[2 * e + 1]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < TT; ++x)
+#pragma unroll
+            for (int y = 0; y < OT; ++y) {
+                const u32x4 vf = in[x][2 * F + y][lane];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt][y] = mfma<CT>(vf, pf[mt][x], o[mt][y]);
+            }
+    }
+
+    // ---- outputs: lane (r, j) holds 2 VD.. consecutive elements of its row
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, 64);
+        l[mt] += __shfl_xor(l[mt], 32, 64);
+        const int x = my0 + 16 * mt + r;
+        if (x < rows) {
+            const int di = token_of(x), i = i0 + di, head = h * a.group + x + g0 - di * a.group;
+            float lse;
+            const float f = finish_row(m[mt], l[mt], a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
+            uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs;
+#pragma unroll
+            for (int c = 0; c < L::C; ++c)
+#pragma unroll
+                for (int reg = 0; reg < 4; ++reg) {
+                    uint32_t w[L::VD / 2];
+#pragma unroll
+                    for (int k = 0; k < L::VD; k += 2)
+                        w[k / 2] = pack_out<ACT>(o[mt][c * L::VD + k][reg] * f, o[mt][c * L::VD + k + 1][reg] * f);
+                    uint16_t* to = dst + c * L::CH + L::VD * (4 * j + reg);
+                    if constexpr (L::VD == 8) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+                    else *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+                }
+            if (a.lse && j == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+        }
+    }
+}
+
+// Compiled shapes of the tiled kernel: X(D, MT, NW, TT).
+#define FP4_ATTN_TILED(X) X(64, 2, 4, 2) X(128, 2, 4, 2) X(256, 2, 4, 1)
+
 // Compiled shapes of the streaming kernel: X(D, MT), blocks of 16 MT query rows.
 #define FP4_ATTN_SHAPES(X) X(64, 1) X(64, 2) X(64, 4) X(128, 1) X(128, 2) X(128, 4) X(256, 1) X(256, 2)
 
 // Launches of one (format, activation type), in a translation unit each.
 // False when the shape is not compiled.
-bool launch_attention_nv_bf16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
-bool launch_attention_nv_f16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
-bool launch_attention_mx_bf16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
-bool launch_attention_mx_f16(int D, int MT, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_nv_bf16(int D, int MT, bool tiled, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_nv_f16(int D, int MT, bool tiled, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_mx_bf16(int D, int MT, bool tiled, const AttnArgs& a, const KvArgs& c, hipStream_t s);
+bool launch_attention_mx_f16(int D, int MT, bool tiled, const AttnArgs& a, const KvArgs& c, hipStream_t s);
 
 }  // namespace fp4

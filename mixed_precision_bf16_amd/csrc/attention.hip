@@ -9,6 +9,7 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs
 
 
 struct AttnPlan {
+    bool tiled;
     int MT, grid;
     size_t ml_off, word_off, ws_bytes;
 };
@@ -24,6 +25,15 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t each = x.max_q > 0 ? std::min(x.max_q, x.q_rows) : x.q_rows;
     const int64_t rows = each * group;
     p->MT = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
+    // the tiled kernel (128 rows a workgroup) where its items fill the GPU
+    const int64_t tiled_items = (x.q_rows * group / kTiledRows + x.batch) * c.kv_heads;
+    p->tiled = rows > 64 && x.q_rows * group / kTiledRows * c.kv_heads >= 256;
+    if (p->tiled) {
+        if (tiled_items >= (int64_t(1) << 31)) return FP4_ERR_SHAPE;
+        p->grid = (int)tiled_items;
+        p->ml_off = p->word_off = p->ws_bytes = 0;
+        return FP4_OK;
+    }
     const int64_t R = 16 * p->MT;
     // every sequence has at most one partly filled row block
     const int64_t items = (x.q_rows * group / R + x.batch) * c.kv_heads;
@@ -73,7 +83,8 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
           reinterpret_cast<uintptr_t>(x->seq_lens) | reinterpret_cast<uintptr_t>(x->q_offsets) |
           reinterpret_cast<uintptr_t>(x->sinks)) & 3))
         return FP4_ERR_SHAPE;
-    if (!x->workspace || x->workspace_bytes < p.ws_bytes || (reinterpret_cast<uintptr_t>(x->workspace) & 15))
+    if (p.ws_bytes > 0 &&
+        (!x->workspace || x->workspace_bytes < p.ws_bytes || (reinterpret_cast<uintptr_t>(x->workspace) & 15)))
         return FP4_ERR_WORKSPACE;
     st = check_device();
     if (st != FP4_OK) return st;
@@ -114,7 +125,7 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     const bool nv = cache->format == FP4_NVFP4;
     const auto launch = nv ? (x->act_type == 0 ? launch_attention_nv_bf16 : launch_attention_nv_f16)
                            : (x->act_type == 0 ? launch_attention_mx_bf16 : launch_attention_mx_f16);
-    if (!launch((int)D, p.MT, a, c, s)) return FP4_ERR_SHAPE;
+    if (!launch((int)D, p.MT, p.tiled, a, c, s)) return FP4_ERR_SHAPE;
     return launch_status();
 }
 

@@ -429,3 +429,82 @@ def test_projection_cache_attention_projection(fmt, dtype):
         ref = oracle.act_bits_to_f64(bits(a), act) @ oracle.dequant_weights(c, s, K, fmt).T
         mag = np.abs(oracle.act_bits_to_f64(bits(a), act)) @ np.abs(oracle.dequant_weights(c, s, K, fmt)).T
         assert np.all(np.abs(got.double().cpu().numpy() - ref) <= 8e-3 * np.abs(ref) + 2e-3 * mag)
+
+
+@pytest.mark.parametrize("fmt,dtype", [(0, BF16), (1, BF16), (0, FP16), (1, FP16)])
+@pytest.mark.parametrize("D,H,group,lens,news", [
+    (128, 8, 8, [300, 700], [300, 260]), (64, 16, 4, [1, 513, 130, 200], [1, 513, 77, 130]),
+    (256, 4, 4, [900, 64, 33], [900, 64, 20]), (128, 8, 5, [640, 40], [600, 40]), (128, 32, 1, [1100], [1050])])
+def test_prompts_that_fill_the_gpu(D, H, group, lens, news, fmt, dtype):
+    """Enough query rows for the tiled kernel; rows checked against the oracle."""
+    print("[case] prompts", D, H, group, lens, news, fmt, dtype, flush=True)
+    assert sum(news) * group // 128 * H >= 256 or sum(news) * group * H >= 4096
+    p = Problem(lens, news, fmt, dtype, D, H, group, 32 if D == 64 else 96, seed=D + H)
+    got = p.run()
+    torch.cuda.synchronize()
+    _check_sampled(p, got)
+
+
+def _check_sampled(p, got, **kw):
+    """p.check on a few query tokens and heads (the oracle is slow)."""
+    rows = int(p.offsets[-1])
+    rng = np.random.Generator(np.random.PCG64(rows))
+    heads = sorted({0, p.heads - 1, int(rng.integers(p.heads))})
+    group = p.heads // p.H
+    for b, n in enumerate(np.diff(p.offsets)):
+        for i in sorted({0, 1, int(n) - 1, int(n) // 2, *(int(x) for x in rng.integers(0, max(n, 1), 6))} & set(range(n))):
+            for h in heads:
+                one = Problem.__new__(Problem)
+                one.__dict__.update(p.__dict__)
+                row = int(p.offsets[b]) + i
+                one.lens, one.table = [max(0, p.lens[b] - int(n) + i + 1)], p.table[b:b + 1]
+                one.offsets = np.array([0, 1], np.int32)
+                one.q = p.q[row:row + 1, h:h + 1]
+                one.H, one.heads = 1, 1
+                one.k, one.v = p.k[:, h // group:h // group + 1], p.v[:, h // group:h // group + 1]
+                one.check((got[0][row:row + 1, h:h + 1], got[1][row:row + 1, h:h + 1]),
+                          **({**kw, "sinks": kw["sinks"][h:h + 1]} if kw.get("sinks") is not None else kw))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, True), (1, False), (70, True), (300, False)])
+def test_prompts_with_window_and_sinks(window, sinks):
+    p = Problem([700, 90], [650, 90], 1, BF16, 64, 16, 4, 32, seed=window + 2)
+    s = _sinks(64, 4) if sinks else None
+    got = p.run(window=window, sinks=None if s is None else torch.from_numpy(s).cuda())
+    _check_sampled(p, got, window=window, sinks=s)
+
+
+def test_prompts_with_empty_rows_missing_pages_and_strides():
+    """Queries before the first key, pages that are not there and rows of no
+    sequence, in the tiled kernel."""
+    p = Problem([600, 100, 0], [600, 180, 9], 0, BF16, 128, 8, 8, 32, seed=33)
+    p.table[0, 3], p.table[0, 10], p.table[1, 0] = -1, p.pages + 4, -2
+    q = torch.full((800, 2 * 64, 128), float("nan"), dtype=BF16, device="cuda")
+    q[4:793, :64] = p.q.cuda()
+    out = torch.full((800, 64, 256), 5.0, dtype=BF16, device="cuda")[:, :, :128]
+    lse = torch.full((800, 64), 5.0, device="cuda")
+    F.attention(q[:, :64], p.cache(), torch.from_numpy(p.table).cuda(),
+                torch.tensor(p.lens, dtype=torch.int32, device="cuda"),
+                q_offsets=torch.from_numpy(p.offsets + 4).cuda(), out=out, lse=lse, scale=p.scale)
+    assert torch.all(out[:4] == 5) and torch.all(out[793:] == 5) and torch.all(lse[:4] == 5) and torch.all(lse[793:] == 5)
+    _check_sampled(p, (out[4:793], lse[4:793]))
+    assert torch.all(out[604:684] == 0) and torch.all(torch.isneginf(lse[604:684]))
+    assert torch.all(out[784:793] == 0) and torch.all(torch.isneginf(lse[784:793]))
+
+
+def test_prompts_without_causal_order():
+    p = Problem([520], [513], 1, FP16, 128, 8, 8, 64, seed=34)
+    got = p.run(causal=False)
+    q = p.q[:3].double().numpy()
+    ref, lse, w = oracle.attention_reference(q, p.k, p.v, p.table, p.lens, [0, 3], 64, False, 0,
+                                             float(np.float32(p.scale)))
+    off = np.abs(got[0][:3].double().cpu().numpy() - ref)
+    assert np.all(off <= 2.0 ** -11 * np.abs(ref) + 2.0 ** -10 * w + 2.0 ** -25)
+
+
+def test_kernels_agree():
+    """max_q only chooses the kernel: both give the same rows up to rounding."""
+    p = Problem([900, 333], [700, 333], 0, FP16, 128, 8, 8, 64, seed=35)
+    a, b = p.run(max_q=1), p.run()
+    assert torch.all((a[0].float() - b[0].float()).abs() <= 2.0 ** -9 * b[0].float().abs() + 2.0 ** -10)
+    assert torch.all((a[1] - b[1]).abs() <= 2.0 ** -18 * (1 + b[1].abs()))
