@@ -794,7 +794,7 @@ struct TilePart {  // what one of the WPT waves of a tile dequantizes
 };
 
 template <int FMT, int ACT, int D, int MT, int NW, int TT>
-__global__ __launch_bounds__(64 * NW) void attention_tiled(AttnArgs a, KvArgs cache) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_tiled(AttnArgs a, KvArgs cache) {
     using L = KvTile<FMT, D>;
     constexpr int CT = attn_type(FMT, ACT);
     constexpr int R = 16 * MT * NW, F = D / 32, S = L::KD / 8, OT = D / 16, WPT = NW / TT;
