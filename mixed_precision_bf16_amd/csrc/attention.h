@@ -794,7 +794,7 @@ struct TilePart {  // what one of the WPT waves of a tile dequantizes
 };
 
 template <int FMT, int ACT, int D, int MT, int NW, int TT>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_tiled(AttnArgs a, KvArgs cache) {
+__global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs cache) {
     using L = KvTile<FMT, D>;
     constexpr int CT = attn_type(FMT, ACT);
     constexpr int R = 16 * MT * NW, F = D / 32, S = L::KD / 8, OT = D / 16, WPT = NW / TT;
@@ -1097,7 +1097,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_tiled(Att
 }
 
 // Compiled shapes of the tiled kernel: X(D, MT, NW, TT).
-#define FP4_ATTN_TILED(X) X(64, 2, 4, 2) X(128, 2, 4, 2) X(256, 2, 4, 1)
+#define FP4_ATTN_TILED(X) X(64, 2, 4, 2) X(128, 2, 4, 2) X(256, 1, 8, 2)
 
 // Compiled shapes of the streaming kernel: X(D, MT), blocks of 16 MT query rows.
 #define FP4_ATTN_SHAPES(X) X(64, 1) X(64, 2) X(64, 4) X(128, 1) X(128, 2) X(128, 4) X(256, 1) X(256, 2)
