@@ -782,16 +782,55 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
 // multiplied, step i + 1 is dequantized into the other buffer and the codes of
 // step i + 2 are loaded.  Scores, softmax and probabilities stay in registers,
 // as in the streaming kernel.
+//
+// A tile's dequantization is dealt to WPT waves by token half u (tokens 16 u ..
+// 16 u + 15) and, with four waves, by chunk: each loads whole fragments of
+// codes and writes whole key fragments and its half (8 bytes a lane) of the
+// value fragments.
 template <int FMT, int D, int WPT>
-struct TilePart {  // what one of the WPT waves of a tile dequantizes
+struct TilePart {
     using L = KvTile<FMT, D>;
-    static constexpr int KF = D == 64 ? 1 : (WPT == 4 ? 1 : L::C);  // key fragments of 1 KiB that it loads
-    static constexpr int VF = D == 64 ? 1 : (WPT == 4 ? 2 : L::F);
-    static constexpr int VC = WPT == 4 ? 1 : L::C;
-    u32x4 k[KF], v[VF];
-    uint32_t ks[(L::kKsLane + 3) / 4];
-    u32x2 vs[VC];
+    static constexpr int N = WPT == 4 ? 1 : L::C;  // chunks
+    static constexpr int W = D == 64 ? 2 : 4;      // dwords of a lane's codes of one chunk and half
+    uint32_t k[N][W], v[N][W];
+    uint32_t ks[N];  // the KG key scales of each chunk in the low bytes
+    uint32_t vs[N];  // the scales of the four value tokens
 };
+
+// Fragments of a part, chunk n: key steps, and the halves of the value
+// fragments (two dwords: tokens 0, 1 and 2, 3 of the quad).
+template <int FMT, int CT, int D, int S_>
+__device__ __forceinline__ u32x4 part_key(uint32_t w, uint32_t ks) {
+    using L = KvTile<FMT, D>;
+    const uint32_t a[1] = {ks};
+    return key_frag<FMT, CT, (S_ * 8 / L::G) % L::KG>(w, a);
+}
+template <int FMT, int CT, int D, int Q>
+__device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, u32x2& even, u32x2& odd) {
+    float s[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if constexpr (FMT == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((vs >> (8 * i)) & 0xFFu);
+    }
+    uint32_t a[4];  // elements 2 Q, 2 Q + 1 of the four tokens
+    if constexpr (D == 64) {
+        a[0] = codes16<CT, Q>(v[0], s[0]);
+        a[1] = codes16<CT, Q + 2>(v[0], s[1]);
+        a[2] = codes16<CT, Q>(v[1], s[2]);
+        a[3] = codes16<CT, Q + 2>(v[1], s[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = codes16<CT, Q>(v[i], s[i]);
+    }
+    even = u32x2{low_halves(a[0], a[1]), low_halves(a[2], a[3])};
+    odd = u32x2{high_halves(a[0], a[1]), high_halves(a[2], a[3])};
+    if constexpr (FMT == 0) {
+        const f16x2 s01 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)vs, 1.0f, false);
+        const f16x2 s23 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)vs, 1.0f, true);
+        even = u32x2{mul_f16x2(even.x, s01), mul_f16x2(even.y, s23)};
+        odd = u32x2{mul_f16x2(odd.x, s01), mul_f16x2(odd.y, s23)};
+    }
+}
 
 template <int FMT, int ACT, int D, int MT, int NW, int TT>
 __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs cache) {
@@ -869,8 +908,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
     auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36); };
     auto load_pages = [&](int t) { return pages[page_of(max(0, min(t + lane, t1 - 1)))]; };
     int window_pages = steps > 0 ? load_pages(t0) : 0, window_first = t0;
-    TilePart<FMT, D, WPT> raw;
-    int raw_bad = 0, raw_clear = 0;  // tiles of the step without keys; whether this wave's tile runs past them
+    using Part = TilePart<FMT, D, WPT>;
+    Part raw;
+    const int half = sub & 1, chunk0 = sub >> 1;  // this wave's token half and first chunk
+    int raw_bad = 0, raw_left = 0;  // tiles of the step without keys; keys that this wave's tile holds from its start
     auto fetch = [&](int step) {
         const int ts = t0 + step * TT;
         if (ts + TT - window_first > 64) {
@@ -887,88 +928,66 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
             if (x == my_tile) page = bad ? 0 : p;
         }
         const int t = min(ts + my_tile, t1 - 1);
-        raw_clear = (raw_bad >> my_tile & 1) || (t + 1) * kKvTile > it.len;
+        raw_left = (raw_bad >> my_tile & 1) ? 0 : it.len - t * kKvTile;
         const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + h) * cache.tiles_per_page +
                                             (t - page_of(t) * cache.tiles_per_page)) * (int64_t)L::kBytes;
-        using P = TilePart<FMT, D, WPT>;
-        const int u = sub & 1, c = sub >> 1;
 #pragma unroll
-        for (int f = 0; f < P::KF; ++f)
-            raw.k[f] = *reinterpret_cast<const u32x4*>(tile + (D == 64 ? 0 : (WPT == 4 ? c : f) * 2 + u) * 1024 +
-                                                       lane * 16);
+        for (int n = 0; n < Part::N; ++n) {
+            const int c = chunk0 + n;
+            if constexpr (D == 64) {
+                const u32x2 k = *reinterpret_cast<const u32x2*>(tile + half * 8 + lane * 16);
+                const u32x2 v = *reinterpret_cast<const u32x2*>(tile + L::kCodes + half * 8 + lane * 16);
+                raw.k[n][0] = k.x;
+                raw.k[n][1] = k.y;
+                raw.v[n][0] = v.x;
+                raw.v[n][1] = v.y;
+            } else {
+                const u32x4 k = *reinterpret_cast<const u32x4*>(tile + (c * 2 + half) * 1024 + lane * 16);
+                const u32x4 v = *reinterpret_cast<const u32x4*>(tile + L::kCodes + (c * 2 + half) * 1024 + lane * 16);
 #pragma unroll
-        for (int f = 0; f < P::VF; ++f)
-            raw.v[f] = *reinterpret_cast<const u32x4*>(tile + L::kCodes + (WPT == 4 ? c * 2 + f : f) * 1024 + lane * 16);
-        const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j);
-        if constexpr (L::kKsLane == 2) raw.ks[0] = *reinterpret_cast<const uint16_t*>(ks);
-        else if constexpr (L::kKsLane == 4) raw.ks[0] = *reinterpret_cast<const uint32_t*>(ks);
-        else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(ks);
-            raw.ks[0] = w.x;
-            raw.ks[1] = w.y;
-        }
-#pragma unroll
-        for (int x = 0; x < P::VC; ++x) {
-            const int g = (WPT == 4 ? c : x) * (L::CH / L::G) + r * L::VD / L::G;
-            raw.vs[x] = *reinterpret_cast<const u32x2*>(tile + L::kVs + (g * 4 + j) * 8);
+                for (int e = 0; e < 4; ++e) {
+                    raw.k[n][e] = k[e];
+                    raw.v[n][e] = v[e];
+                }
+            }
+            const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j) + (c * 2 + half) * L::KG;
+            if constexpr (L::KG == 2) raw.ks[n] = *reinterpret_cast<const uint16_t*>(ks);
+            else raw.ks[n] = *ks;
+            const int g = c * (L::CH / L::G) + r * L::VD / L::G;
+            raw.vs[n] = *reinterpret_cast<const uint32_t*>(tile + L::kVs + (g * 4 + j) * 8 + half * 4);
         }
     };
-    // raw -> fragments in LDS buffer `buf`; `step` is the step that raw holds
-    auto spread = [&](int buf, int step) {
-        using P = TilePart<FMT, D, WPT>;
+    // raw -> fragments in LDS buffer `buf`
+    auto spread = [&](int buf) {
         u32x4(*out)[64] = lds[buf][my_tile];
-        TileRegs<FMT, D> x;  // only what this wave loaded is used
+        const int left = raw_left - 16 * half - 4 * j;  // value tokens of the quad that exist (clear_values)
+        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 #pragma unroll
-        for (int c = 0; c < L::C; ++c) x.vs[c] = raw.vs[WPT == 4 ? 0 : c];
-#pragma unroll
-        for (int e = 0; e < (L::kKsLane + 3) / 4; ++e) x.ks[e] = raw.ks[e];
-        if (raw_clear) {
-            const int tok0 = (t0 + step * TT + my_tile) * kKvTile;
-            clear_values<FMT, D>(x, tok0, j, (raw_bad >> my_tile & 1) ? 0 : it.len);
-        }
-        auto part = [&](auto uc, auto cc) {  // keys of tokens 16 u ..; half u of the value elements
-            constexpr int u = decltype(uc)::value, c = decltype(cc)::value;
-            constexpr int kf = D == 64 ? 0 : (WPT == 4 ? 0 : c), vf = D == 64 ? 0 : (WPT == 4 ? 0 : c * 2);
-            if constexpr (D == 64) {
-                x.k[0] = raw.k[0];
-                x.v[0] = raw.v[0];
-            } else {
-                x.k[c * 2 + u] = raw.k[kf];
-                x.v[c * 2] = raw.v[vf];
-                x.v[c * 2 + 1] = raw.v[vf + 1];
-            }
-            auto key = [&](auto sc) {
-                constexpr int s = decltype(sc)::value;
-                out[u * F + c * S + s][lane] = key_step<FMT, CT, D, u, c, s>(x);
-            };
-            key(std::integral_constant<int, 0>{});
-            key(std::integral_constant<int, 1>{});
+        for (int n = 0; n < Part::N; ++n) {
+            const int c = chunk0 + n;
+            u32x4(*ko)[64] = out + half * F + c * S;
+            ko[0][lane] = part_key<FMT, CT, D, 0>(raw.k[n][0], raw.ks[n]);
+            ko[1][lane] = part_key<FMT, CT, D, 1>(raw.k[n][1], raw.ks[n]);
             if constexpr (S == 4) {
-                key(std::integral_constant<int, 2>{});
-                key(std::integral_constant<int, 3>{});
+                ko[2][lane] = part_key<FMT, CT, D, 2>(raw.k[n][2], raw.ks[n]);
+                ko[3][lane] = part_key<FMT, CT, D, 3>(raw.k[n][3], raw.ks[n]);
             }
+            const uint32_t vs = raw.vs[n] & keep;
             auto value = [&](auto qc) {
                 constexpr int q = decltype(qc)::value;
-                u32x4 even, odd;
-                value_frags<FMT, CT, D, c, q>(x, even, odd);
-                out[2 * F + c * L::VD + 2 * q][lane] = even;
-                out[2 * F + c * L::VD + 2 * q + 1][lane] = odd;
+                u32x2 even, odd;
+                part_value<FMT, CT, D, q>(raw.v[n], vs, even, odd);
+                u32x4* vo = &out[2 * F + c * L::VD + 2 * q][lane];
+                reinterpret_cast<u32x2*>(vo)[half] = even;
+                reinterpret_cast<u32x2*>(vo + 64)[half] = odd;
             };
-            constexpr int Q = L::VD / 4;  // pairs of value elements of half a chunk
-            value(std::integral_constant<int, u * Q>{});
-            if constexpr (Q == 2) value(std::integral_constant<int, u * Q + 1>{});
-        };
-        auto chunk = [&](auto uc) {
-            if constexpr (WPT == 4) {
-                if (sub >> 1) part(uc, std::integral_constant<int, 1>{});
-                else part(uc, std::integral_constant<int, 0>{});
-            } else {
-                part(uc, std::integral_constant<int, 0>{});
-                if constexpr (L::C == 2) part(uc, std::integral_constant<int, 1>{});
+            value(std::integral_constant<int, 0>{});
+            value(std::integral_constant<int, 1>{});
+            if constexpr (L::VD == 8) {
+                value(std::integral_constant<int, 2>{});
+                value(std::integral_constant<int, 3>{});
             }
-        };
-        if (sub & 1) chunk(std::integral_constant<int, 1>{});
-        else chunk(std::integral_constant<int, 0>{});
+        }
     };
 
     if (steps > 0) fetch(0);
@@ -989,9 +1008,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
     }
     int cur_bad = 0;
     if (steps > 0) {
-        spread(0, 0);
+        spread(0);
         cur_bad = raw_bad;
-        if (steps > 1) fetch(1);
+        fetch(min(1, steps - 1));
     }
 
     for (int step = 0; step < steps; ++step) {
@@ -1012,15 +1031,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
                     for (int mt = 0; mt < MT; ++mt) sc[mt][2 * x + u] = mfma<CT>(kf, qf[mt][f], sc[mt][2 * x + u]);
                 }
             }
-        const bool edge = cur_bad || tok0 + TT * kKvTile > hi_all || tok0 < lo_all;
+        // the last steps spread a step again that nothing reads: no branches
+        // between the products and the dequantization
+        spread(buf ^ 1);
         const int bad = cur_bad;
-        if (step + 1 < steps) {
-            spread(buf ^ 1, step + 1);
-            cur_bad = raw_bad;
-            if (step + 2 < steps) fetch(step + 2);
-        }
+        const bool edge = bad || tok0 + TT * kKvTile > hi_all || tok0 < lo_all;
+        cur_bad = raw_bad;
+        fetch(min(step + 2, steps - 1));
 
-        u32x4 pf[MT][TT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (edge) {
@@ -1045,9 +1063,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
 #pragma unroll
                 for (int y = 0; y < OT; ++y) o[mt][y] *= down;
             }
-            const float off = kBias - m[mt];
+        }
 #pragma unroll
-            for (int x = 0; x < TT; ++x) {
+        for (int x = 0; x < TT; ++x) {
+            u32x4 pf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float off = kBias - m[mt];
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -1055,17 +1077,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
                     l[mt] += p[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pf[mt][x][e] = pack_out<CT>(p[2 * e], p[2 * e + 1]);
+                for (int e = 0; e < 4; ++e) pf[mt][e] = pack_out<CT>(p[2 * e], p[2 * e + 1]);
             }
-        }
-#pragma unroll
-        for (int x = 0; x < TT; ++x)
 #pragma unroll
             for (int y = 0; y < OT; ++y) {
                 const u32x4 vf = in[x][2 * F + y][lane];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) o[mt][y] = mfma<CT>(vf, pf[mt][x], o[mt][y]);
+                for (int mt = 0; mt < MT; ++mt) o[mt][y] = mfma<CT>(vf, pf[mt], o[mt][y]);
             }
+        }
     }
 
     // ---- outputs: lane (r, j) holds 2 VD.. consecutive elements of its row
