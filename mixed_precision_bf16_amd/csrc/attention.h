@@ -15,6 +15,9 @@
 // 2^(kBias + kSlack), in range for FP16, and kBias moves the point where FP16
 // probabilities vanish to 2^-(24 + kBias) of the largest one.
 #pragma once
+#include <type_traits>
+#include <utility>
+
 #include "kv_layout.h"
 
 namespace fp4 {
@@ -31,6 +34,7 @@ constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 12
 #endif
 constexpr int kItemCost = FP4_ITEM_COST;
 constexpr int kTiledRows = 128;        // query rows of a workgroup of the tiled kernel
+constexpr int kAhead = 4;              // fragments of LDS read ahead by the tiled kernel
 constexpr int kTeam = 16;              // shares of an item that are joined at a time
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
 
@@ -244,25 +248,27 @@ struct QueryRow {
     // Converts them to the matrix-core type; returns the factor that turns the
     // accumulated products into base-2 scores (kept normal: a factor of 0
     // would turn a hidden key's -Inf into NaN).
-    __device__ static __forceinline__ float convert(u32x4 (&f)[kFrags], float scale) {
+    // A row lies in four lanes 16 apart (N = D / 32 fragments), or in two 32 apart.
+    template <int N>
+    __device__ static __forceinline__ float convert(u32x4 (&f)[N], float scale) {
         if constexpr (attn_type(FMT, ACT) == 1 && ACT == 0) {
             // BF16 queries on the FP16 matrix cores: a power of two brings the
             // row's largest element to 2^13 .. 2^14, so that every element
             // down to 2^-27 of it converts exactly.
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kFrags; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t p = f[i][e];
                     top = fmaxf(top, fmaxf(fabsf(__uint_as_float(p << 16)), fabsf(__uint_as_float(p & 0xFFFF0000u))));
                 }
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            if constexpr (N == kFrags) top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
             const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < kFrags; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint32_t p = f[i][x];
@@ -772,38 +778,71 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
     }
 }
 
+// f(0), f(1), .. f(N - 1) with the numbers as compile-time constants.
+template <class Fn, int... I>
+__device__ __forceinline__ void unrolled_(Fn&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class Fn>
+__device__ __forceinline__ void unrolled(Fn&& f) {
+    unrolled_(f, std::make_integer_sequence<int, N>{});
+}
+
 // ------------------------------------------------------------ tiled kernel
-// Many query rows a sequence (prompts, chunks).  A workgroup takes 16 MT rows
-// a wave of one (sequence, row block, KV head) and walks over the keys in
-// steps of TT tiles.  Each key and value is dequantized once per workgroup:
-// the waves share a step's fragments through LDS, where a fragment is the
-// 1 KiB that a wave reads with one 16-byte load a lane, without bank
-// conflicts.  Two LDS buffers and one barrier a step: while step i is
-// multiplied, step i + 1 is dequantized into the other buffer and the codes of
-// step i + 2 are loaded.  Scores, softmax and probabilities stay in registers,
-// as in the streaming kernel.
+// Many query rows a sequence (prompts, chunks).  A workgroup takes 32 rows a
+// wave of one (sequence, row block, KV head) and walks over the keys in steps
+// of TT tiles.  Each key and value is dequantized once per workgroup: the
+// waves share a step's fragments through LDS, where a fragment is the 1 KiB
+// that a wave reads with one 16-byte load a lane, without bank conflicts.  Two
+// LDS buffers and one barrier a step: while step i is multiplied, step i + 1 is
+// dequantized into the other buffer and the codes of step i + 2 are loaded.
+//
+// The products are 32x32x16: on this GPU vector instructions of other waves run
+// beside them, while beside the 16x16x32 form they mostly wait (measured with
+// four waves a SIMD, per 16384 products: four FP4 converts alone 19.5 cycles,
+// with the 16x16x32 form 27.8, with half a 32x32x16 one 23.4; two exponentials
+// 19.2, 27.6, 21.7).
+//   S^T = K Q^T: with lane = 32 h + t, step i of a chunk takes the eight
+//   elements of octet (j, s) of token t, j = 2 (i / S) + h, s = i mod S, where
+//   octet (j, s) is dword s of the codes of lane (t mod 16, j);
+//   O^T = V^T P^T: row 2 r + e of block q is element VD r + 2 q + e, product
+//   step u takes tokens 16 u + 4 h .. + 3 and 16 u + 8 + 4 h .. + 3, whose
+//   probabilities lane 32 h + . holds after S^T.
 //
 // A tile's dequantization is dealt to WPT waves by token half u (tokens 16 u ..
-// 16 u + 15) and, with four waves, by chunk: each loads whole fragments of
-// codes and writes whole key fragments and its half (8 bytes a lane) of the
-// value fragments.
+// 16 u + 15) and, with four waves, by chunk, or where there is only one by the
+// halves of its octets and value elements.
 template <int FMT, int D, int WPT>
 struct TilePart {
     using L = KvTile<FMT, D>;
-    static constexpr int N = WPT == 4 ? 1 : L::C;  // chunks
-    static constexpr int W = D == 64 ? 2 : 4;      // dwords of a lane's codes of one chunk and half
-    uint32_t k[N][W], v[N][W];
-    uint32_t ks[N];  // the KG key scales of each chunk in the low bytes
+    static constexpr bool kHalf = WPT == 4 && L::C == 1;       // half the elements
+    static constexpr int N = WPT == 4 ? 1 : L::C;              // chunks
+    static constexpr int SP = kHalf ? L::KD / 16 : L::KD / 8;  // octets of a lane and chunk
+    static constexpr int VP = kHalf ? L::VD / 4 : L::VD / 2;   // pairs of value elements of a chunk
+    static constexpr int VW = D == 64 ? 2 : 4;                 // dwords of a lane's value codes
+    uint32_t k[N][SP], v[N][VW];
+    uint32_t ks[N];  // the key scales of each chunk in the low bytes
     uint32_t vs[N];  // the scales of the four value tokens
 };
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+template <int CT>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+    if constexpr (CT == 0)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+}
+
 // Fragments of a part, chunk n: key steps, and the halves of the value
 // fragments (two dwords: tokens 0, 1 and 2, 3 of the quad).
-template <int FMT, int CT, int D, int S_>
+template <int FMT, int CT, int D, int S_, bool kHalf>
 __device__ __forceinline__ u32x4 part_key(uint32_t w, uint32_t ks) {
     using L = KvTile<FMT, D>;
     const uint32_t a[1] = {ks};
-    return key_frag<FMT, CT, (S_ * 8 / L::G) % L::KG>(w, a);
+    return key_frag<FMT, CT, kHalf ? 0 : (S_ * 8 / L::G) % L::KG>(w, a);
 }
 template <int FMT, int CT, int D, int Q>
 __device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, u32x2& even, u32x2& odd) {
@@ -832,18 +871,21 @@ __device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, u32x2
     }
 }
 
-template <int FMT, int ACT, int D, int MT, int NW, int TT>
-__global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs cache) {
+template <int FMT, int ACT, int D, int NW, int TT, int WAVES>
+__global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, KvArgs cache) {
     using L = KvTile<FMT, D>;
     constexpr int CT = attn_type(FMT, ACT);
-    constexpr int R = 16 * MT * NW, F = D / 32, S = L::KD / 8, OT = D / 16, WPT = NW / TT;
-    static_assert(WPT == 2 || (WPT == 4 && L::C == 2), "a tile is dequantized by two waves, or by two for each chunk");
-    constexpr int kTileFrags = 2 * F + OT;  // 1 KiB fragments of a tile
+    constexpr int R = 32 * NW, S = L::KD / 8, WPT = NW / TT;
+    constexpr int F = D / 16;    // product steps of a tile's scores
+    constexpr int OB = D / 32;   // blocks of 32 value elements
+    static_assert(WPT == 2 || WPT == 4, "a tile is dequantized by two or four waves");
+    constexpr int kTileFrags = F + 2 * OB;  // 1 KiB fragments of a tile
     __shared__ u32x4 lds[2][TT][kTileFrags][64];
     __shared__ int lds_scan[NW], lds_found[5];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, j = lane >> 4;
+    const int r = lane & 15, j = lane >> 4;         // as the codes lie in a tile
+    const int row32 = lane & 31, h32 = lane >> 5;   // as the products take them
     const int kv_heads = cache.kv_heads;
 
     // ---- the item: sequences in order, their last row blocks (the longest
@@ -892,14 +934,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
     const int t0 = first_lo / kKvTile, t1 = (min(last_hi, it.len) + kKvTile - 1) / kKvTile;
     const int steps = max(0, (t1 - t0 + TT - 1) / TT);
 
-    // ---- query rows of this wave
-    const int my0 = wave * 16 * MT;
-    u32x4 qf[MT][F];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int x = my0 + 16 * mt + r, di = token_of(x), i = i0 + di, g = x + g0 - di * a.group;
+    // ---- query row of this lane (32 rows a wave)
+    const int my0 = wave * 32, my = my0 + row32;
+    u32x4 qf[F];
+    {
+        const int di = token_of(my), i = i0 + di, g = my + g0 - di * a.group;
         const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs;
-        QueryRow<FMT, ACT, D>::load(qf[mt], src, x < rows, j);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int c = f / (2 * S), x = f % (2 * S);
+            qf[f] = u32x4{0u, 0u, 0u, 0u};
+            if (my < rows) qf[f] = *reinterpret_cast<const u32x4*>(src + c * L::CH + L::KD * (2 * (x / S) + h32) + 8 * (x % S));
+        }
     }
 
     // ---- loads of this wave's part of a step
@@ -910,7 +956,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
     int window_pages = steps > 0 ? load_pages(t0) : 0, window_first = t0;
     using Part = TilePart<FMT, D, WPT>;
     Part raw;
-    const int half = sub & 1, chunk0 = sub >> 1;  // this wave's token half and first chunk
+    // this wave's token half, first chunk and half of the elements
+    const int half = sub & 1, chunk0 = Part::kHalf ? 0 : sub >> 1, quarter = Part::kHalf ? sub >> 1 : 0;
     int raw_bad = 0, raw_left = 0;  // tiles of the step without keys; keys that this wave's tile holds from its start
     auto fetch = [&](int step) {
         const int ts = t0 + step * TT;
@@ -934,81 +981,80 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
 #pragma unroll
         for (int n = 0; n < Part::N; ++n) {
             const int c = chunk0 + n;
-            if constexpr (D == 64) {
-                const u32x2 k = *reinterpret_cast<const u32x2*>(tile + half * 8 + lane * 16);
-                const u32x2 v = *reinterpret_cast<const u32x2*>(tile + L::kCodes + half * 8 + lane * 16);
+            const uint8_t* kc = tile + (D == 64 ? half * 8 : (c * 2 + half) * 1024) + lane * 16 + quarter * 4 * Part::SP;
+            if constexpr (Part::SP == 1) {
+                raw.k[n][0] = *reinterpret_cast<const uint32_t*>(kc);
+            } else if constexpr (Part::SP == 2) {
+                const u32x2 k = *reinterpret_cast<const u32x2*>(kc);
                 raw.k[n][0] = k.x;
                 raw.k[n][1] = k.y;
+            } else {
+                const u32x4 k = *reinterpret_cast<const u32x4*>(kc);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) raw.k[n][e] = k[e];
+            }
+            const uint8_t* vc = tile + L::kCodes + (D == 64 ? half * 8 : (c * 2 + half) * 1024) + lane * 16;
+            if constexpr (D == 64) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(vc);
                 raw.v[n][0] = v.x;
                 raw.v[n][1] = v.y;
             } else {
-                const u32x4 k = *reinterpret_cast<const u32x4*>(tile + (c * 2 + half) * 1024 + lane * 16);
-                const u32x4 v = *reinterpret_cast<const u32x4*>(tile + L::kCodes + (c * 2 + half) * 1024 + lane * 16);
+                const u32x4 v = *reinterpret_cast<const u32x4*>(vc);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    raw.k[n][e] = k[e];
-                    raw.v[n][e] = v[e];
-                }
+                for (int e = 0; e < 4; ++e) raw.v[n][e] = v[e];
             }
             const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j) + (c * 2 + half) * L::KG;
-            if constexpr (L::KG == 2) raw.ks[n] = *reinterpret_cast<const uint16_t*>(ks);
+            if constexpr (L::KG == 2 && Part::kHalf) raw.ks[n] = ks[quarter];
+            else if constexpr (L::KG == 2) raw.ks[n] = *reinterpret_cast<const uint16_t*>(ks);
             else raw.ks[n] = *ks;
             const int g = c * (L::CH / L::G) + r * L::VD / L::G;
             raw.vs[n] = *reinterpret_cast<const uint32_t*>(tile + L::kVs + (g * 4 + j) * 8 + half * 4);
         }
     };
-    // raw -> fragments in LDS buffer `buf`
-    auto spread = [&](int buf) {
+    // raw -> fragments in LDS buffer `buf`, in kPieces pieces: the key steps, then
+    // pairs of value fragments, of each chunk
+    constexpr int kPieces = Part::N * (Part::SP + Part::VP);
+    auto spread = [&](int buf, auto piece) {
+        constexpr int n = decltype(piece)::value / (Part::SP + Part::VP), p = decltype(piece)::value % (Part::SP + Part::VP);
         u32x4(*out)[64] = lds[buf][my_tile];
-        const int left = raw_left - 16 * half - 4 * j;  // value tokens of the quad that exist (clear_values)
-        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        const int c = chunk0 + n;
+        if constexpr (p < Part::SP) {
+            const int x = quarter * Part::SP + p;  // octet (j, x) of token 16 half + r
+            out[c * 2 * S + (j >> 1) * S + x][32 * (j & 1) + 16 * half + r] =
+                part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n]);
+        } else {
+            constexpr int q = p - Part::SP;
+            const int left = raw_left - 16 * half - 4 * j;  // value tokens of the quad that exist (clear_values)
+            const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            uint32_t codes[Part::VW];
 #pragma unroll
-        for (int n = 0; n < Part::N; ++n) {
-            const int c = chunk0 + n;
-            u32x4(*ko)[64] = out + half * F + c * S;
-            ko[0][lane] = part_key<FMT, CT, D, 0>(raw.k[n][0], raw.ks[n]);
-            ko[1][lane] = part_key<FMT, CT, D, 1>(raw.k[n][1], raw.ks[n]);
-            if constexpr (S == 4) {
-                ko[2][lane] = part_key<FMT, CT, D, 2>(raw.k[n][2], raw.ks[n]);
-                ko[3][lane] = part_key<FMT, CT, D, 3>(raw.k[n][3], raw.ks[n]);
-            }
-            const uint32_t vs = raw.vs[n] & keep;
-            auto value = [&](auto qc) {
-                constexpr int q = decltype(qc)::value;
-                u32x2 even, odd;
-                part_value<FMT, CT, D, q>(raw.v[n], vs, even, odd);
-                u32x4* vo = &out[2 * F + c * L::VD + 2 * q][lane];
-                reinterpret_cast<u32x2*>(vo)[half] = even;
-                reinterpret_cast<u32x2*>(vo + 64)[half] = odd;
-            };
-            value(std::integral_constant<int, 0>{});
-            value(std::integral_constant<int, 1>{});
-            if constexpr (L::VD == 8) {
-                value(std::integral_constant<int, 2>{});
-                value(std::integral_constant<int, 3>{});
-            }
+            for (int e = 0; e < Part::VW; ++e)
+                codes[e] = Part::kHalf ? raw.v[n][e] >> (quarter * 8 * Part::VP) : raw.v[n][e];
+            u32x2 even, odd;
+            part_value<FMT, CT, D, q>(codes, raw.vs[n] & keep, even, odd);
+            const int block = c * (L::VD / 2) + quarter * Part::VP + q;
+            u32x2* vo = reinterpret_cast<u32x2*>(&out[F + block * 2 + half][32 * (j & 1) + 2 * r]) + (j >> 1);
+            vo[0] = even;
+            vo[2] = odd;
         }
     };
 
     if (steps > 0) fetch(0);
-    float fac[MT], m[MT], l[MT];
-    RowRange range[MT];
-    f32x4 o[MT][OT];
-    const int my_rows = min(16 * MT, rows - my0);  // may be below 1
+    const float fac = QueryRow<FMT, ACT, D>::convert(qf, a.scale);
+    const RowRange range = range_of(my);
+    float m = kNoMax, l = 0.0f;
+    f32x16 o[OB];
+#pragma unroll
+    for (int x = 0; x < OB; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[x][e] = 0.0f;
+    // keys that every row of this wave sees
+    const int my_rows = min(32, rows - my0);  // may be below 1
     const int hi_all = __builtin_amdgcn_readfirstlane(range_of(min(my0, rows - 1)).hi);
     const int lo_all = __builtin_amdgcn_readfirstlane(range_of(max(0, my0 + max(my_rows, 1) - 1)).lo);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        fac[mt] = QueryRow<FMT, ACT, D>::convert(qf[mt], a.scale);
-        range[mt] = range_of(my0 + 16 * mt + r);
-        m[mt] = kNoMax;
-        l[mt] = 0.0f;
-#pragma unroll
-        for (int x = 0; x < OT; ++x) o[mt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
     int cur_bad = 0;
     if (steps > 0) {
-        spread(0);
+        unrolled<kPieces>([&](auto p) { spread(0, p); });
         cur_bad = raw_bad;
         fetch(min(1, steps - 1));
     }
@@ -1017,107 +1063,112 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tiled(AttnArgs a, KvArgs
         __syncthreads();  // buffer `step` is written, the other one is read out
         const int buf = step & 1, tok0 = (t0 + step * TT) * kKvTile;
         const u32x4(*in)[kTileFrags][64] = lds[buf];
-        f32x4 sc[MT][2 * TT];
+        // Scores.  The order is fixed by hand: fragments are read kAhead before
+        // their products, and the next step's dequantization goes in between.
+        // (The last step spreads a step again that nothing reads.)
+        f32x16 sc[TT];
+        u32x4 ring[kAhead];
+        constexpr int kKeyFrags = TT * F, kValueFrags = TT * 2 * OB;
+        // keys: step by step of each tile; values: for each tile and half u the blocks
+        auto key_at = [&](int e) { return in[e / F][e % F][lane]; };
+        auto value_at = [&](int e) { return in[e / (2 * OB)][F + (e % OB) * 2 + e / OB % 2][lane]; };
 #pragma unroll
-        for (int x = 0; x < TT; ++x)
+        for (int e = 0; e < kAhead; ++e) ring[e] = key_at(e);
+        __builtin_amdgcn_sched_barrier(0);
+        unrolled<kKeyFrags>([&](auto ec) {
+            constexpr int e = decltype(ec)::value, x = e / F, f = e % F;
+            constexpr int p0 = e * kPieces / kKeyFrags, p1 = (e + 1) * kPieces / kKeyFrags;
+            if constexpr (f == 0) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) sc[mt][2 * x + u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    const u32x4 kf = in[x][u * F + f][lane];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) sc[mt][2 * x + u] = mfma<CT>(kf, qf[mt][f], sc[mt][2 * x + u]);
-                }
+                for (int z = 0; z < 16; ++z) sc[x][z] = 0.0f;
             }
-        // the last steps spread a step again that nothing reads: no branches
-        // between the products and the dequantization
-        spread(buf ^ 1);
+            sc[x] = mfma32<CT>(ring[e % kAhead], qf[f], sc[x]);
+            if constexpr (e + kAhead < kKeyFrags) ring[e % kAhead] = key_at(e + kAhead);
+            unrolled<p1 - p0>([&](auto p) { spread(buf ^ 1, std::integral_constant<int, p0 + decltype(p)::value>{}); });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) ring[e] = value_at(e);
         const int bad = cur_bad;
         const bool edge = bad || tok0 + TT * kKvTile > hi_all || tok0 < lo_all;
         cur_bad = raw_bad;
         fetch(min(step + 2, steps - 1));
 
+        if (edge) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            if (edge) {
+            for (int x = 0; x < TT; ++x)
 #pragma unroll
-                for (int e = 0; e < 8 * TT; ++e) {
-                    const int tok = tok0 + 16 * (e >> 2) + 4 * j + (e & 3);
-                    const bool see = tok >= range[mt].lo && tok < range[mt].hi && tok < it.len && !(bad >> (e >> 3) & 1);
-                    if (!see) sc[mt][e >> 2][e & 3] = -__builtin_inff();
+                for (int e = 0; e < 16; ++e) {
+                    const int tok = tok0 + 32 * x + 8 * (e >> 2) + 4 * h32 + (e & 3);
+                    const bool see = tok >= range.lo && tok < range.hi && tok < it.len && !(bad >> x & 1);
+                    if (!see) sc[x][e] = -__builtin_inff();
                 }
-            }
-            float top = sc[mt][0][0];
-#pragma unroll
-            for (int e = 1; e < 8 * TT; ++e) top = fmaxf(top, sc[mt][e >> 2][e & 3]);
-            top *= fac[mt];
-            if (__any(top > m[mt] + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float mn = fmaxf(m[mt], top);
-                const float down = exp2_(m[mt] - mn);
-                m[mt] = mn;
-                l[mt] *= down;
-#pragma unroll
-                for (int y = 0; y < OT; ++y) o[mt][y] *= down;
-            }
         }
+        float top = sc[0][0];
 #pragma unroll
-        for (int x = 0; x < TT; ++x) {
-            u32x4 pf[MT];
+        for (int e = 1; e < 16 * TT; ++e) top = fmaxf(top, sc[e >> 4][e & 15]);
+        top *= fac;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float mn = fmaxf(m, top);
+            const float down = exp2_(m - mn);
+            m = mn;
+            l *= down;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const float off = kBias - m[mt];
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = exp2_(fmaf(sc[mt][2 * x + (e >> 2)][e & 3], fac[mt], off));
-                    l[mt] += p[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pf[mt][e] = pack_out<CT>(p[2 * e], p[2 * e + 1]);
-            }
-#pragma unroll
-            for (int y = 0; y < OT; ++y) {
-                const u32x4 vf = in[x][2 * F + y][lane];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) o[mt][y] = mfma<CT>(vf, pf[mt], o[mt][y]);
-            }
+            for (int y = 0; y < OB; ++y) o[y] *= down;
         }
+        // Probabilities of the first 16 keys, then the products of 16 keys with
+        // the next ones' probabilities in between.
+        const float off = kBias - m;
+        u32x4 pf[2 * TT];
+        auto weigh = [&](int u, int pair) {  // two of a lane's eight keys of half-tile u
+            const int e = 8 * (u & 1) + 2 * pair;
+            const float p0 = exp2_(fmaf(sc[u >> 1][e], fac, off)), p1 = exp2_(fmaf(sc[u >> 1][e + 1], fac, off));
+            l += p0 + p1;
+            pf[u][pair] = pack_out<CT>(p0, p1);
+        };
+#pragma unroll
+        for (int pair = 0; pair < 4; ++pair) weigh(0, pair);
+        __builtin_amdgcn_sched_barrier(0);
+        unrolled<kValueFrags>([&](auto ec) {
+            constexpr int e = decltype(ec)::value, u = e / OB, y = e % OB;
+            constexpr int w0 = y * 4 / OB, w1 = (y + 1) * 4 / OB;
+            o[y] = mfma32<CT>(ring[e % kAhead], pf[u], o[y]);
+            if constexpr (e + kAhead < kValueFrags) ring[e % kAhead] = value_at(e + kAhead);
+            if constexpr (u + 1 < 2 * TT) unrolled<w1 - w0>([&](auto w) { weigh(u + 1, w0 + decltype(w)::value); });
+            __builtin_amdgcn_sched_barrier(0);
+        });
     }
 
-    // ---- outputs: lane (r, j) holds 2 VD.. consecutive elements of its row
+    // ---- outputs: row 2 r + e of block q is element VD r + 2 q + e of its chunk;
+    // lane 32 h + . holds rows 8 g + 4 h + i
+    l += __shfl_xor(l, 32, 64);
+    if (my < rows) {
+        const int di = token_of(my), i = i0 + di, head = h * a.group + my + g0 - di * a.group;
+        float lse;
+        const float f = finish_row(m, l, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
+        uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs;
+        constexpr int Q = L::VD / 2;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        l[mt] += __shfl_xor(l[mt], 16, 64);
-        l[mt] += __shfl_xor(l[mt], 32, 64);
-        const int x = my0 + 16 * mt + r;
-        if (x < rows) {
-            const int di = token_of(x), i = i0 + di, head = h * a.group + x + g0 - di * a.group;
-            float lse;
-            const float f = finish_row(m[mt], l[mt], a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
-            uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs;
+        for (int c = 0; c < L::C; ++c)
 #pragma unroll
-            for (int c = 0; c < L::C; ++c)
+            for (int g = 0; g < 4; ++g)
 #pragma unroll
-                for (int reg = 0; reg < 4; ++reg) {
-                    uint32_t w[L::VD / 2];
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w[Q];
 #pragma unroll
-                    for (int k = 0; k < L::VD; k += 2)
-                        w[k / 2] = pack_out<ACT>(o[mt][c * L::VD + k][reg] * f, o[mt][c * L::VD + k + 1][reg] * f);
-                    uint16_t* to = dst + c * L::CH + L::VD * (4 * j + reg);
-                    if constexpr (L::VD == 8) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+                    for (int q = 0; q < Q; ++q)
+                        w[q] = pack_out<ACT>(o[c * Q + q][4 * g + 2 * x] * f, o[c * Q + q][4 * g + 2 * x + 1] * f);
+                    uint16_t* to = dst + c * L::CH + L::VD * (4 * g + 2 * h32 + x);
+                    if constexpr (Q == 4) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
                     else *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
                 }
-            if (a.lse && j == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
-        }
+        if (a.lse && h32 == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
     }
 }
 
-// Compiled shapes of the tiled kernel: X(D, MT, NW, TT).
-#define FP4_ATTN_TILED(X) X(64, 2, 4, 2) X(128, 2, 4, 2) X(256, 1, 8, 2)
+// Compiled shapes of the tiled kernel: X(D, NW, TT, WAVES).
+#define FP4_ATTN_TILED(X) X(64, 4, 2, 2) X(128, 4, 2, 2) X(256, 4, 1, 1)
 
 // Compiled shapes of the streaming kernel: X(D, MT), blocks of 16 MT query rows.
 #define FP4_ATTN_SHAPES(X) X(64, 1) X(64, 2) X(64, 4) X(128, 1) X(128, 2) X(128, 4) X(256, 1) X(256, 2)
