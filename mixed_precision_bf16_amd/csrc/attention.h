@@ -33,7 +33,6 @@ constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 12
 #define FP4_ITEM_COST 3
 #endif
 constexpr int kItemCost = FP4_ITEM_COST;
-constexpr int kTiledRows = 128;        // query rows of a workgroup of the tiled kernel
 constexpr int kAhead = 4;              // fragments of LDS read ahead by the tiled kernel
 constexpr int kTeam = 16;              // shares of an item that are joined at a time
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
@@ -871,60 +870,91 @@ __device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, u32x2
     }
 }
 
-template <int FMT, int ACT, int D, int NW, int TT, int WAVES>
+template <int FMT, int ACT, int D, int RW, int NW, int TT, int WAVES>
 __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, KvArgs cache) {
     using L = KvTile<FMT, D>;
     constexpr int CT = attn_type(FMT, ACT);
-    constexpr int R = 32 * NW, S = L::KD / 8, WPT = NW / TT;
-    constexpr int F = D / 16;    // product steps of a tile's scores
-    constexpr int OB = D / 32;   // blocks of 32 value elements
+    constexpr bool k32 = RW == 32;  // rows of a wave: 32x32x16 products, else 16x16x32
+    constexpr int R = RW * NW, S = L::KD / 8, WPT = NW / TT;
+    constexpr int F = D / 16;               // key fragments of a tile, and value fragments
+    constexpr int QF = k32 ? F : F / 2;     // query fragments of a row: product steps
+    constexpr int OB = k32 ? D / 32 : D / 16;  // blocks of the output's elements
+    constexpr int NS = k32 ? 16 : 8;        // scores of a lane and tile
+    using Acc = typename std::conditional<k32, f32x16, f32x4>::type;
     static_assert(WPT == 2 || WPT == 4, "a tile is dequantized by two or four waves");
-    constexpr int kTileFrags = F + 2 * OB;  // 1 KiB fragments of a tile
+    constexpr int kTileFrags = 2 * F;  // 1 KiB fragments of a tile
     __shared__ u32x4 lds[2][TT][kTileFrags][64];
     __shared__ int lds_scan[NW], lds_found[5];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, j = lane >> 4;         // as the codes lie in a tile
-    const int row32 = lane & 31, h32 = lane >> 5;   // as the products take them
+    const int prow = lane % RW, ph = lane / RW;     // as the products take them
     const int kv_heads = cache.kv_heads;
 
-    // ---- the item: sequences in order, their last row blocks (the longest
-    // ones) first, the KV heads of a block next to each other
-    {
+    // ---- the item, longest first: a block's level is its row block plus the
+    // sequence's earlier keys, in row blocks; the KV heads of a block are next to
+    // each other
+    const int block = (int)blockIdx.x / kv_heads, h = (int)blockIdx.x - block * kv_heads;
+    int b, rb;
+    Seq it;
+    if (a.batch <= 64) {  // every wave by itself, a sequence a lane
+        const Seq x = sequence_of<R>(a, lane);
+        const int base = min(max(x.len - x.n, 0) / (R / a.group + 1), 1 << 24);
+        auto count = [&](int level) {  // blocks at this level or above
+            int n = min(max(x.blocks + base - level, 0), x.blocks);
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
+            return n;
+        };
+        int lo = 0, hi = x.blocks > 0 ? x.blocks + base : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) hi = max(hi, __shfl_xor(hi, d, 64));
+        if (block >= count(0)) return;
+        while (hi - lo > 1) {  // the highest level `lo` with count(lo) > block
+            const int mid = (lo + hi) >> 1;
+            if (count(mid) > block) lo = mid;
+            else hi = mid;
+        }
+        const unsigned long long at = __ballot(x.blocks + base > lo && base <= lo && x.blocks > 0);
+        const int nth = block - count(lo + 1);
+        const bool mine = (at >> lane & 1) && __popcll(at & ((1ull << lane) - 1)) == nth;
+        b = __ffsll(__ballot(mine)) - 1;
+        rb = lo - __shfl(base, b, 64);
+        it = sequence_from<R>(a, __shfl(x.q0, b, 64), __shfl(x.n, b, 64), __shfl(x.len, b, 64));
+    } else {  // sequences in order, their last blocks first
         int before = 0;
         bool there = false;
         for (int base = 0; base < a.batch && !there; base += 64 * NW) {
-            const int b = base + threadIdx.x;
-            Seq x = sequence_of<R>(a, b);
-            const int n = x.blocks * kv_heads;
-            int p = wave_scan(n);
+            const Seq x = sequence_of<R>(a, base + threadIdx.x);
+            int p = wave_scan(x.blocks);
             __syncthreads();
             if (lane == 63) lds_scan[wave] = p;
             __syncthreads();
-            p += before - n;
+            p += before - x.blocks;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 p += w < wave ? lds_scan[w] : 0;
                 before += lds_scan[w];
             }
-            if ((int)blockIdx.x >= p && (int)blockIdx.x < p + n) {
-                lds_found[0] = b;
+            if (block >= p && block < p + x.blocks) {
+                lds_found[0] = base + threadIdx.x;
                 lds_found[1] = x.q0;
                 lds_found[2] = x.n;
                 lds_found[3] = x.len;
                 lds_found[4] = p;
             }
-            there = (int)blockIdx.x < before;  // the same in every thread
+            there = block < before;  // the same in every thread
         }
         if (!there) return;
         __syncthreads();
+        b = lds_found[0];
+        it = sequence_from<R>(a, lds_found[1], lds_found[2], lds_found[3]);
+        rb = it.blocks - 1 - (block - lds_found[4]);
     }
-    const int b = __builtin_amdgcn_readfirstlane(lds_found[0]);
-    const Seq it = sequence_from<R>(a, __builtin_amdgcn_readfirstlane(lds_found[1]),
-                                    __builtin_amdgcn_readfirstlane(lds_found[2]),
-                                    __builtin_amdgcn_readfirstlane(lds_found[3]));
-    const int item = (int)blockIdx.x - __builtin_amdgcn_readfirstlane(lds_found[4]);
-    const int rb = it.blocks - 1 - item / kv_heads, h = item % kv_heads;
+    b = __builtin_amdgcn_readfirstlane(b);
+    rb = __builtin_amdgcn_readfirstlane(rb);
+    it = sequence_from<R>(a, __builtin_amdgcn_readfirstlane(it.q0), __builtin_amdgcn_readfirstlane(it.n),
+                          __builtin_amdgcn_readfirstlane(it.len));
     const int rows = min(R, it.n * a.group - rb * R);
     const int i0 = rb * R / a.group, g0 = rb * R - i0 * a.group;
     auto token_of = [&](int x) { return (int)(((float)(x + g0) + 0.5f) * a.inv_group); };
@@ -934,17 +964,18 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     const int t0 = first_lo / kKvTile, t1 = (min(last_hi, it.len) + kKvTile - 1) / kKvTile;
     const int steps = max(0, (t1 - t0 + TT - 1) / TT);
 
-    // ---- query row of this lane (32 rows a wave)
-    const int my0 = wave * 32, my = my0 + row32;
-    u32x4 qf[F];
+    // ---- query row of this lane
+    const int my0 = wave * RW, my = my0 + prow;
+    u32x4 qf[QF];
     {
         const int di = token_of(my), i = i0 + di, g = my + g0 - di * a.group;
         const uint16_t* src = a.q + (int64_t)(it.q0 + i) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs;
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const int c = f / (2 * S), x = f % (2 * S);
+        for (int f = 0; f < QF; ++f) {
+            constexpr int per = k32 ? 2 * S : S;  // product steps of a chunk
+            const int c = f / per, x = f % per, lane_j = k32 ? 2 * (x / S) + ph : ph;
             qf[f] = u32x4{0u, 0u, 0u, 0u};
-            if (my < rows) qf[f] = *reinterpret_cast<const u32x4*>(src + c * L::CH + L::KD * (2 * (x / S) + h32) + 8 * (x % S));
+            if (my < rows) qf[f] = *reinterpret_cast<const u32x4*>(src + c * L::CH + L::KD * lane_j + 8 * (x % S));
         }
     }
 
@@ -1020,8 +1051,9 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         const int c = chunk0 + n;
         if constexpr (p < Part::SP) {
             const int x = quarter * Part::SP + p;  // octet (j, x) of token 16 half + r
-            out[c * 2 * S + (j >> 1) * S + x][32 * (j & 1) + 16 * half + r] =
-                part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n]);
+            const u32x4 f = part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n]);
+            if constexpr (k32) out[c * 2 * S + (j >> 1) * S + x][32 * (j & 1) + 16 * half + r] = f;
+            else out[half * (F / 2) + c * S + x][lane] = f;
         } else {
             constexpr int q = p - Part::SP;
             const int left = raw_left - 16 * half - 4 * j;  // value tokens of the quad that exist (clear_values)
@@ -1033,9 +1065,15 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
             u32x2 even, odd;
             part_value<FMT, CT, D, q>(codes, raw.vs[n] & keep, even, odd);
             const int block = c * (L::VD / 2) + quarter * Part::VP + q;
-            u32x2* vo = reinterpret_cast<u32x2*>(&out[F + block * 2 + half][32 * (j & 1) + 2 * r]) + (j >> 1);
-            vo[0] = even;
-            vo[2] = odd;
+            if constexpr (k32) {
+                u32x2* vo = reinterpret_cast<u32x2*>(&out[F + block * 2 + half][32 * (j & 1) + 2 * r]) + (j >> 1);
+                vo[0] = even;
+                vo[2] = odd;
+            } else {
+                u32x2* vo = reinterpret_cast<u32x2*>(&out[F + 2 * block][lane]) + half;
+                vo[0] = even;
+                vo[128] = odd;
+            }
         }
     };
 
@@ -1043,13 +1081,11 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     const float fac = QueryRow<FMT, ACT, D>::convert(qf, a.scale);
     const RowRange range = range_of(my);
     float m = kNoMax, l = 0.0f;
-    f32x16 o[OB];
+    Acc o[OB];
 #pragma unroll
-    for (int x = 0; x < OB; ++x)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[x][e] = 0.0f;
+    for (int x = 0; x < OB; ++x) o[x] = Acc(0.0f);
     // keys that every row of this wave sees
-    const int my_rows = min(32, rows - my0);  // may be below 1
+    const int my_rows = min(RW, rows - my0);  // may be below 1
     const int hi_all = __builtin_amdgcn_readfirstlane(range_of(min(my0, rows - 1)).hi);
     const int lo_all = __builtin_amdgcn_readfirstlane(range_of(max(0, my0 + max(my_rows, 1) - 1)).lo);
     int cur_bad = 0;
@@ -1063,27 +1099,25 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         __syncthreads();  // buffer `step` is written, the other one is read out
         const int buf = step & 1, tok0 = (t0 + step * TT) * kKvTile;
         const u32x4(*in)[kTileFrags][64] = lds[buf];
-        // Scores.  The order is fixed by hand: fragments are read kAhead before
-        // their products, and the next step's dequantization goes in between.
-        // (The last step spreads a step again that nothing reads.)
-        f32x16 sc[TT];
+        // The order is fixed by hand: fragments are read kAhead before their
+        // products, and the next step's dequantization goes in between.  (The
+        // last step spreads a step again that nothing reads.)
+        constexpr int kFrags = TT * F;
+        Acc sc[k32 ? TT : 2 * TT];  // k32: a tile, else 16 keys each
         u32x4 ring[kAhead];
-        constexpr int kKeyFrags = TT * F, kValueFrags = TT * 2 * OB;
-        // keys: step by step of each tile; values: for each tile and half u the blocks
+        // value fragments, k32: for each tile and half u the blocks
         auto key_at = [&](int e) { return in[e / F][e % F][lane]; };
-        auto value_at = [&](int e) { return in[e / (2 * OB)][F + (e % OB) * 2 + e / OB % 2][lane]; };
+        auto value_at = [&](int e) { return in[e / F][F + (k32 ? (e % OB) * 2 + e / OB % 2 : e % F)][lane]; };
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) ring[e] = key_at(e);
         __builtin_amdgcn_sched_barrier(0);
-        unrolled<kKeyFrags>([&](auto ec) {
-            constexpr int e = decltype(ec)::value, x = e / F, f = e % F;
-            constexpr int p0 = e * kPieces / kKeyFrags, p1 = (e + 1) * kPieces / kKeyFrags;
-            if constexpr (f == 0) {
-#pragma unroll
-                for (int z = 0; z < 16; ++z) sc[x][z] = 0.0f;
-            }
-            sc[x] = mfma32<CT>(ring[e % kAhead], qf[f], sc[x]);
-            if constexpr (e + kAhead < kKeyFrags) ring[e % kAhead] = key_at(e + kAhead);
+        unrolled<kFrags>([&](auto ec) {
+            constexpr int e = decltype(ec)::value, x = e / QF, f = e % QF;
+            constexpr int p0 = e * kPieces / kFrags, p1 = (e + 1) * kPieces / kFrags;
+            if constexpr (f == 0) sc[x] = Acc(0.0f);
+            if constexpr (k32) sc[x] = mfma32<CT>(ring[e % kAhead], qf[f], sc[x]);
+            else sc[x] = mfma<CT>(ring[e % kAhead], qf[f], sc[x]);
+            if constexpr (e + kAhead < kFrags) ring[e % kAhead] = key_at(e + kAhead);
             unrolled<p1 - p0>([&](auto p) { spread(buf ^ 1, std::integral_constant<int, p0 + decltype(p)::value>{}); });
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -1094,21 +1128,21 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         cur_bad = raw_bad;
         fetch(min(step + 2, steps - 1));
 
+        constexpr int A = k32 ? 16 : 4;  // scores of an accumulator
         if (edge) {
 #pragma unroll
-            for (int x = 0; x < TT; ++x)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int tok = tok0 + 32 * x + 8 * (e >> 2) + 4 * h32 + (e & 3);
-                    const bool see = tok >= range.lo && tok < range.hi && tok < it.len && !(bad >> x & 1);
-                    if (!see) sc[x][e] = -__builtin_inff();
-                }
+            for (int e = 0; e < NS * TT; ++e) {
+                const int key = tok0 + (k32 ? 8 : 16) * (e >> 2) + 4 * ph + (e & 3);
+                const bool see = key >= range.lo && key < range.hi && key < it.len && !(bad >> (e / NS) & 1);
+                if (!see) sc[e / A][e % A] = -__builtin_inff();
+            }
         }
         float top = sc[0][0];
 #pragma unroll
-        for (int e = 1; e < 16 * TT; ++e) top = fmaxf(top, sc[e >> 4][e & 15]);
+        for (int e = 1; e < NS * TT; ++e) top = fmaxf(top, sc[e / A][e % A]);
         top *= fac;
         if (__any(top > m + kSlack)) {
+            if constexpr (!k32) top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             const float mn = fmaxf(m, top);
             const float down = exp2_(m - mn);
@@ -1117,58 +1151,67 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
 #pragma unroll
             for (int y = 0; y < OB; ++y) o[y] *= down;
         }
-        // Probabilities of the first 16 keys, then the products of 16 keys with
-        // the next ones' probabilities in between.
+        // Probabilities of a lane's first eight keys, then the products of eight
+        // with the next ones' probabilities in between.
         const float off = kBias - m;
-        u32x4 pf[2 * TT];
-        auto weigh = [&](int u, int pair) {  // two of a lane's eight keys of half-tile u
-            const int e = 8 * (u & 1) + 2 * pair;
-            const float p0 = exp2_(fmaf(sc[u >> 1][e], fac, off)), p1 = exp2_(fmaf(sc[u >> 1][e + 1], fac, off));
+        constexpr int kEights = NS * TT / 8;
+        u32x4 pf[kEights];
+        auto weigh = [&](int u, int pair) {  // two of eight keys
+            const int e = 8 * u + 2 * pair;
+            const float p0 = exp2_(fmaf(sc[e / A][e % A], fac, off)), p1 = exp2_(fmaf(sc[e / A][e % A + 1], fac, off));
             l += p0 + p1;
             pf[u][pair] = pack_out<CT>(p0, p1);
         };
 #pragma unroll
         for (int pair = 0; pair < 4; ++pair) weigh(0, pair);
         __builtin_amdgcn_sched_barrier(0);
-        unrolled<kValueFrags>([&](auto ec) {
+        unrolled<kFrags>([&](auto ec) {
             constexpr int e = decltype(ec)::value, u = e / OB, y = e % OB;
             constexpr int w0 = y * 4 / OB, w1 = (y + 1) * 4 / OB;
-            o[y] = mfma32<CT>(ring[e % kAhead], pf[u], o[y]);
-            if constexpr (e + kAhead < kValueFrags) ring[e % kAhead] = value_at(e + kAhead);
-            if constexpr (u + 1 < 2 * TT) unrolled<w1 - w0>([&](auto w) { weigh(u + 1, w0 + decltype(w)::value); });
+            if constexpr (k32) o[y] = mfma32<CT>(ring[e % kAhead], pf[u], o[y]);
+            else o[y] = mfma<CT>(ring[e % kAhead], pf[u], o[y]);
+            if constexpr (e + kAhead < kFrags) ring[e % kAhead] = value_at(e + kAhead);
+            if constexpr (u + 1 < kEights) unrolled<w1 - w0>([&](auto w) { weigh(u + 1, w0 + decltype(w)::value); });
             __builtin_amdgcn_sched_barrier(0);
         });
     }
 
-    // ---- outputs: row 2 r + e of block q is element VD r + 2 q + e of its chunk;
-    // lane 32 h + . holds rows 8 g + 4 h + i
+    // ---- outputs.  k32: row 2 r + e of block q is element VD r + 2 q + e of its
+    // chunk, and lane 32 h + . holds rows 8 g + 4 h + i; else row r of block q is
+    // element VD r + q, and lane 16 h + . holds rows 4 h + i.
+    if constexpr (!k32) l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     if (my < rows) {
         const int di = token_of(my), i = i0 + di, head = h * a.group + my + g0 - di * a.group;
         float lse;
         const float f = finish_row(m, l, a.sinks != nullptr, a.sinks ? a.sinks[head] : 0.0f, lse) * a.v_alpha;
         uint16_t* dst = a.out + (int64_t)(it.q0 + i) * a.o_ts + (int64_t)head * a.o_hs;
-        constexpr int Q = L::VD / 2;
+        constexpr int V = L::VD;
 #pragma unroll
         for (int c = 0; c < L::C; ++c)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int x = 0; x < (k32 ? 8 : 4); ++x) {
+                uint32_t w[V / 2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t w[Q];
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-                        w[q] = pack_out<ACT>(o[c * Q + q][4 * g + 2 * x] * f, o[c * Q + q][4 * g + 2 * x + 1] * f);
-                    uint16_t* to = dst + c * L::CH + L::VD * (4 * g + 2 * h32 + x);
-                    if constexpr (Q == 4) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
-                    else *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+                for (int q = 0; q < V / 2; ++q) {
+                    if constexpr (k32)
+                        w[q] = pack_out<ACT>(o[c * V / 2 + q][2 * x] * f, o[c * V / 2 + q][2 * x + 1] * f);
+                    else
+                        w[q] = pack_out<ACT>(o[c * V + 2 * q][x] * f, o[c * V + 2 * q + 1][x] * f);
                 }
-        if (a.lse && h32 == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
+                const int r0 = k32 ? 4 * (x / 2) + 2 * ph + x % 2 : 4 * ph + x;
+                uint16_t* to = dst + c * L::CH + V * r0;
+                if constexpr (V == 8) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+                else *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+            }
+        if (a.lse && ph == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
     }
 }
 
-// Compiled shapes of the tiled kernel: X(D, NW, TT, WAVES).
-#define FP4_ATTN_TILED(X) X(64, 4, 2, 2) X(128, 4, 2, 2) X(256, 4, 1, 1)
+// Compiled shapes of the tiled kernel: X(D, RW, NW, TT, WAVES): NW
+// waves of RW rows, TT tiles a step.
+#define FP4_ATTN_TILED(X) X(64, 32, 8, 4, 2) X(128, 32, 8, 4, 2) X(256, 16, 8, 2, 2)
+constexpr int tiled_rows(int D) { return D == 256 ? 128 : 256; }
 
 // Compiled shapes of the streaming kernel: X(D, MT), blocks of 16 MT query rows.
 #define FP4_ATTN_SHAPES(X) X(64, 1) X(64, 2) X(64, 4) X(128, 1) X(128, 2) X(128, 4) X(256, 1) X(256, 2)

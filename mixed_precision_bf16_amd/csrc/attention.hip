@@ -25,7 +25,8 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t each = x.max_q > 0 ? std::min(x.max_q, x.q_rows) : x.q_rows;
     const int64_t rows = each * group;
     p->MT = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
-    // the tiled kernel (128 rows a workgroup) where its items fill the GPU
+    // the tiled kernel where its items fill the GPU
+    const int64_t kTiledRows = tiled_rows((int)D);
     const int64_t tiled_items = (x.q_rows * group / kTiledRows + x.batch) * c.kv_heads;
     p->tiled = rows > 64 && x.q_rows * group / kTiledRows * c.kv_heads >= 256;
     if (p->tiled) {
