@@ -56,9 +56,10 @@ struct AttnArgs {
     float scale;               // scale * k_alpha * log2(e)
     float v_alpha;
     float inv_group;           // 1 / group
-    int grid;                  // workgroups: as many as the GPU holds
+    int grid;                  // workgroups; in the streaming kernel as many as the GPU holds
+    int splits;                // tiled kernel: most shares of an item
     uint32_t tag;
-    float* ws_o;               // [2 * grid][rows][D]
+    float* ws_o;               // [2 * grid][rows][D]; tiled kernel: [grid][D / 4][rows][4] and so on
     float* ws_ml;              // [2 * grid][rows][2]
     unsigned long long* words; // [2 * grid]
 };
@@ -894,7 +895,8 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     // ---- the item, longest first: a block's level is its row block plus the
     // sequence's earlier keys, in row blocks; the KV heads of a block are next to
     // each other
-    const int block = (int)blockIdx.x / kv_heads, h = (int)blockIdx.x - block * kv_heads;
+    const int share = (int)blockIdx.x % a.splits, head_block = (int)blockIdx.x / a.splits;
+    const int block = head_block / kv_heads, h = head_block - block * kv_heads;
     int b, rb;
     Seq it;
     if (a.batch <= 64) {  // every wave by itself, a sequence a lane
@@ -962,7 +964,11 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     const int last_hi = __builtin_amdgcn_readfirstlane(range_of(rows - 1).hi);
     const int first_lo = __builtin_amdgcn_readfirstlane(range_of(0).lo);
     const int t0 = first_lo / kKvTile, t1 = (min(last_hi, it.len) + kKvTile - 1) / kKvTile;
-    const int steps = max(0, (t1 - t0 + TT - 1) / TT);
+    // Steps [s0, s1) of this share of the item; a share has four steps at least.
+    const int all_steps = max(0, (t1 - t0 + TT - 1) / TT);
+    const int shares = min(a.splits, max(1, all_steps / 4));
+    if (share >= shares) return;
+    const int s0 = all_steps * share / shares, steps = all_steps * (share + 1) / shares - s0;
 
     // ---- query row of this lane
     const int my0 = wave * RW, my = my0 + prow;
@@ -984,14 +990,14 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     const int my_tile = wave / WPT, sub = wave % WPT;
     auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * a.tpp_magic) >> 36); };
     auto load_pages = [&](int t) { return pages[page_of(max(0, min(t + lane, t1 - 1)))]; };
-    int window_pages = steps > 0 ? load_pages(t0) : 0, window_first = t0;
+    int window_pages = steps > 0 ? load_pages(t0 + s0 * TT) : 0, window_first = t0 + s0 * TT;
     using Part = TilePart<FMT, D, WPT>;
     Part raw;
     // this wave's token half, first chunk and half of the elements
     const int half = sub & 1, chunk0 = Part::kHalf ? 0 : sub >> 1, quarter = Part::kHalf ? sub >> 1 : 0;
     int raw_bad = 0, raw_left = 0;  // tiles of the step without keys; keys that this wave's tile holds from its start
     auto fetch = [&](int step) {
-        const int ts = t0 + step * TT;
+        const int ts = t0 + (s0 + step) * TT;
         if (ts + TT - window_first > 64) {
             window_pages = load_pages(ts);
             window_first = ts;
@@ -1097,7 +1103,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
 
     for (int step = 0; step < steps; ++step) {
         __syncthreads();  // buffer `step` is written, the other one is read out
-        const int buf = step & 1, tok0 = (t0 + step * TT) * kKvTile;
+        const int buf = step & 1, tok0 = (t0 + (s0 + step) * TT) * kKvTile;
         const u32x4(*in)[kTileFrags][64] = lds[buf];
         // The order is fixed by hand: fragments are read kAhead before their
         // products, and the next step's dequantization goes in between.  (The
@@ -1174,6 +1180,52 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
             if constexpr (u + 1 < kEights) unrolled<w1 - w0>([&](auto w) { weigh(u + 1, w0 + decltype(w)::value); });
             __builtin_amdgcn_sched_barrier(0);
         });
+    }
+
+    // ---- join the shares of an item: each keeps its sums as they lie in its
+    // threads, and the last to arrive adds them in their order
+    if (shares > 1) {
+        constexpr int kQuads = OB * (k32 ? 4 : 1), T = 64 * NW;
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.ws_o, a.grid * kQuads * T * 16);  // below 2^31 bytes
+        const __amdgpu_buffer_rsrc_t rm = make_rsrc(a.ws_ml, a.grid * T * 8);
+        const int first = head_block * a.splits;  // slot of share 0
+        unrolled<kQuads>([&](auto qc) {
+            constexpr int q = decltype(qc)::value, y = k32 ? q / 4 : q, e = k32 ? q % 4 * 4 : 0;
+            const f32x4 w = {o[y][e], o[y][e + 1], o[y][e + 2], o[y][e + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
+                                                   (((first + share) * kQuads + q) * T + threadIdx.x) * 16, 0,
+                                                   kDeviceCoherent);
+        });
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(m), __float_as_uint(l)}, rm,
+                                              ((first + share) * T + threadIdx.x) * 8, 0, kDeviceCoherent);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) lds_scan[0] = split_arrive(a.words + head_block, a.tag, shares);
+        __syncthreads();
+        if (!lds_scan[0]) return;
+        asm volatile("" ::: "memory");
+        float top = kNoMax;
+        for (int x = 0; x < shares; ++x)
+            top = fmaxf(top, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                                 rm, ((first + x) * T + threadIdx.x) * 8, 0, kDeviceCoherent)));
+        m = top;
+        l = 0.0f;
+#pragma unroll
+        for (int y = 0; y < OB; ++y) o[y] = Acc(0.0f);
+        for (int x = 0; x < shares; ++x) {
+            const u32x2 ml = __builtin_amdgcn_raw_buffer_load_b64(rm, ((first + x) * T + threadIdx.x) * 8, 0,
+                                                                  kDeviceCoherent);
+            const float w = exp2_(__uint_as_float(ml.x) - top);
+            l += w * __uint_as_float(ml.y);
+            unrolled<kQuads>([&](auto qc) {
+                constexpr int q = decltype(qc)::value, y = k32 ? q / 4 : q, e = k32 ? q % 4 * 4 : 0;
+                const f32x4 v = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(ro, (((first + x) * kQuads + q) * T + threadIdx.x) * 16, 0,
+                                                                 kDeviceCoherent));
+#pragma unroll
+                for (int z = 0; z < 4; ++z) o[y][e + z] += w * v[z];
+            });
+        }
     }
 
     // ---- outputs.  k32: row 2 r + e of block q is element VD r + 2 q + e of its

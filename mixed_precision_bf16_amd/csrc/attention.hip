@@ -10,7 +10,7 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs
 
 struct AttnPlan {
     bool tiled;
-    int MT, grid;
+    int MT, grid, splits;
     size_t ml_off, word_off, ws_bytes;
 };
 
@@ -25,16 +25,26 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t each = x.max_q > 0 ? std::min(x.max_q, x.q_rows) : x.q_rows;
     const int64_t rows = each * group;
     p->MT = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
-    // the tiled kernel where its items fill the GPU
-    const int64_t kTiledRows = tiled_rows((int)D);
-    const int64_t tiled_items = (x.q_rows * group / kTiledRows + x.batch) * c.kv_heads;
-    p->tiled = rows > 64 && x.q_rows * group / kTiledRows * c.kv_heads >= 256;
+    // The tiled kernel, its items cut into shares where they do not fill the
+    // GPU.  Measured (us, streaming / tiled; 64 query and 8 KV heads of 128, 8192
+    // keys): 32 query tokens 49 / 60, 64 (512 rows) 62 / 62, 128 95 / 75, 512
+    // 279 / 147; head size 256 (16, 4): 128 (512 rows) 63 / 74, 256 94 / 78.  With
+    // many sequences its partly filled blocks pay earlier: 32 sequences of 16
+    // tokens (128 rows), 4000 keys 133 / 118.
+    const int64_t tiled = tiled_rows((int)D);
+    const int64_t tiled_items = (x.q_rows * group / tiled + x.batch) * c.kv_heads;
+    p->tiled = rows >= (D == 256 ? 768 : 512) || (rows >= 128 && x.batch * c.kv_heads >= 128);
     if (p->tiled) {
-        if (tiled_items >= (int64_t(1) << 31)) return FP4_ERR_SHAPE;
-        p->grid = (int)tiled_items;
-        p->ml_off = p->word_off = p->ws_bytes = 0;
+        p->splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, 320 / tiled_items));
+        if (tiled_items * p->splits >= (int64_t(1) << 31)) return FP4_ERR_SHAPE;
+        p->grid = (int)(tiled_items * p->splits);
+        const size_t slots = p->splits > 1 ? (size_t)p->grid : 0;
+        p->ml_off = slots * tiled * D * 4;
+        p->word_off = p->ml_off + slots * 512 * 8;
+        p->ws_bytes = p->word_off + (p->splits > 1 ? (size_t)tiled_items * 8 : 0);
         return FP4_OK;
     }
+    p->splits = 1;
     const int64_t R = 16 * p->MT;
     // every sequence has at most one partly filled row block
     const int64_t items = (x.q_rows * group / R + x.batch) * c.kv_heads;
@@ -116,6 +126,7 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.v_alpha = c.v_alpha;
     a.inv_group = 1.0f / a.group;
     a.grid = p.grid;
+    a.splits = p.splits;
     a.tag = next_split_tag();
     char* ws = static_cast<char*>(x->workspace);
     a.ws_o = reinterpret_cast<float*>(ws);
