@@ -440,25 +440,23 @@ def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: 
     return KVCache(data, pages, page_size, kv_heads, head_dim, fmt, k_alpha, v_alpha)
 
 
-class _OnStream:
-    """Device and stream of a call: the tensors' device is made current for the
-    library call, and what the wrapper allocates belongs to the stream that the
-    kernels run on."""
+class _Guard:
+    """Context of a call on another device than the current one, or on a given
+    stream: the device is made current for the library call, and what the
+    wrapper allocates belongs to the stream that the kernels run on."""
 
     __slots__ = ("handle", "_guards")
 
     def __init__(self, device, stream):
         import torch
-        self._guards = []
-        if torch.cuda.current_device() != device.index:
-            self._guards.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
+        self._guards = [torch.cuda.device(device)]
+        if stream is not None:
             if stream.device != device:
                 raise ValueError(f"stream must be a stream of {device}")
-            self.handle = stream.cuda_stream
             self._guards.append(torch.cuda.stream(stream))
+            self.handle = stream.cuda_stream
+        else:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
 
     def __enter__(self):
         for g in self._guards:
@@ -468,6 +466,28 @@ class _OnStream:
     def __exit__(self, *exc):
         for g in reversed(self._guards):
             g.__exit__(*exc)
+
+
+class _Current:
+    """The same for the current stream of the current device: no state to set."""
+
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return None
+
+
+def _on_stream(device, stream):
+    import torch
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return _Current(torch._C._cuda_getCurrentRawStream(device.index))
+    return _Guard(device, stream)
 
 
 def _act_type(dtype, what: str) -> int:
@@ -510,7 +530,7 @@ def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
     kt, kh = _rows(k, "k", n, cache.kv_heads, cache.head_dim, dev)
     vt, vh = _rows(v, "v", n, cache.kv_heads, cache.head_dim, dev)
     sp = _vector(slots, "slots", n, torch.int64, dev)
-    with _OnStream(dev, stream) as s:
+    with _on_stream(dev, stream) as s:
         st = lib().fp4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), sp, n, kt, kh, vt, vh, act, s)
     if st:
         _check(st, "fp4_kv_append")
@@ -530,12 +550,12 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
         raise ValueError("k_out and v_out must have the requested type")
     n = slots.shape[0] if slots.dim() == 1 else -1
     sp = _vector(slots, "slots", n, torch.int64, dev)
-    with _OnStream(dev, stream) as s:
+    with _on_stream(dev, stream) as s:
         shape = (n, cache.kv_heads, cache.head_dim)
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=dev)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=dev)
+            v_out = torch.empty_like(k_out) if k_out.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
         kt, kh = _rows(k_out, "k_out", *shape, dev)
         vt, vh = _rows(v_out, "v_out", *shape, dev)
         st = lib().fp4_kv_read(cache._ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), kt, kh, vt, vh, act, s)
@@ -556,23 +576,21 @@ def _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, wi
             or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
         raise ValueError(f"page_table must be an int32 matrix [batch][columns] on {dev} with contiguous rows")
     batch, columns = page_table.shape
-    a = _AttentionArgs()
-    a.q, a.q_token_stride, a.q_head_stride = q.data_ptr(), qt, qh
-    a.page_table, a.page_columns = page_table.data_ptr(), columns
-    a.page_stride = page_table.stride(0) if batch > 1 else columns
-    a.seq_lens = _vector(seq_lens, "seq_lens", batch, torch.int32, dev)
+    offsets = sink = None
     if q_offsets is not None:
-        a.q_offsets = _vector(q_offsets, "q_offsets", batch + 1, torch.int32, dev)
-        a.max_q = max_q if max_q is not None else rows
+        offsets = _vector(q_offsets, "q_offsets", batch + 1, torch.int32, dev)
+        if max_q is None:
+            max_q = rows
     else:
         if batch and rows % batch:
             raise ValueError("q_rows must be a multiple of the batch without q_offsets")
-        a.max_q = rows // batch if batch else 0
+        max_q = rows // batch if batch else 0
     if sinks is not None:
-        a.sinks = _vector(sinks, "sinks", heads, torch.float32, dev)
-    a.batch, a.q_rows, a.q_heads, a.window, a.causal, a.act_type = batch, rows, heads, window, int(causal), act
-    a.scale = cache.head_dim ** -0.5 if scale is None else scale
-    return a
+        sink = _vector(sinks, "sinks", heads, torch.float32, dev)
+    return _AttentionArgs(q.data_ptr(), None, None, page_table.data_ptr(),
+                          _vector(seq_lens, "seq_lens", batch, torch.int32, dev), offsets, sink, batch, rows, heads,
+                          max_q, columns, page_table.stride(0) if batch > 1 else columns, qt, qh, 0, 0, window,
+                          1 if causal else 0, act, cache.head_dim ** -0.5 if scale is None else scale, None, 0)
 
 
 def attention_workspace_size(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None) -> int:
@@ -604,13 +622,18 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks)
     dev = cache.data.device
     rows, heads, dim = q.shape
-    with _OnStream(dev, stream) as s:
+    with _on_stream(dev, stream) as s:
         if out is None:
-            out = (torch.empty if q_offsets is None else torch.zeros)((rows, heads, dim), dtype=q.dtype, device=dev)
+            if q_offsets is not None:
+                out = torch.zeros((rows, heads, dim), dtype=q.dtype, device=dev)
+            elif q.is_contiguous():
+                out = torch.empty_like(q)
+            else:
+                out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
         elif out.dtype != q.dtype:
             raise ValueError("out must have q's type")
-        a.out = out.data_ptr()
-        a.out_token_stride, a.out_head_stride = _rows(out, "out", rows, heads, dim, dev)
+        ot, oh = _rows(out, "out", rows, heads, dim, dev)
+        a.out, a.out_token_stride, a.out_head_stride = out.data_ptr(), ot, oh
         if lse is not None:
             if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
                 raise ValueError(f"lse must be a contiguous float32 tensor [{rows}][{heads}] on {dev}")
