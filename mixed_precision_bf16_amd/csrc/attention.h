@@ -64,6 +64,26 @@ struct AttnArgs {
     unsigned long long* words; // [2 * grid]
 };
 
+// ------------------------------------------------------------ arrival words
+// As split_arrive (the word is (launch tag, count), any other tag counts as 0,
+// the last arrival leaves 0), with the tag installed well before the arrival,
+// under the shadow of the first loads: the arrival itself is then one atomic.
+// Every workgroup claims its words before it arrives, so they carry the tag.
+__device__ __forceinline__ void claim_word(unsigned long long* w, unsigned long long seen, uint32_t tag) {
+    const unsigned long long mine = (unsigned long long)tag << 32;
+    if ((seen >> 32) != (unsigned long long)tag)  // fails only if another workgroup has installed the tag
+        __hip_atomic_compare_exchange_strong(w, &seen, mine, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool arrive_word(unsigned long long* w, int count) {
+    const uint32_t n = (uint32_t)__hip_atomic_fetch_add(w, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+    if (n == (uint32_t)count) __hip_atomic_store(w, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return n == (uint32_t)count;
+}
+__device__ __forceinline__ unsigned long long peek_word(unsigned long long* w) {
+    return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ------------------------------------------------------------ one key tile
 template <int FMT, int D>
 struct TileRegs {
@@ -453,6 +473,17 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         if (u0 >= u1) continue;
         const int rb = item / kv_heads, h = item - rb * kv_heads;  // heads of a row block are neighbours
         const int wg0 = unit0 / per, parts = (unit0 + it.units - 1) / per - wg0 + 1, part = (int)blockIdx.x - wg0;
+        // Partial sums: an item that goes on in the next workgroup is the last of
+        // its first one (slot 2 wg0 + 1) and the first of the others.
+        auto slot_of = [&](int p) { return 2 * (wg0 + p) + (p == 0 ? 1 : 0); };
+        // words: the slot of the team's first part; for the teams, that of part 1
+        const int p0 = part / kTeam * kTeam, teams = (parts + kTeam - 1) / kTeam, size = min(kTeam, parts - p0);
+        unsigned long long *team_word = a.words + slot_of(p0), *teams_word = a.words + slot_of(1);
+        unsigned long long seen_team = 0, seen_teams = 0;
+        if (parts > 1 && threadIdx.x == 0) {
+            seen_team = peek_word(team_word);
+            seen_teams = peek_word(teams_word);
+        }
 
         // ---- query rows and this wave's tiles.  The page numbers of the next
         // 64 tiles are one load (lane x: tile x), and the loads of a tile are
@@ -507,6 +538,11 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             l[mt] = 0.0f;
 #pragma unroll
             for (int x = 0; x < OT; ++x) o[mt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        if (parts > 1 && threadIdx.x == 0) {
+            claim_word(team_word, seen_team, a.tag);
+            if (teams > 1) claim_word(teams_word, seen_teams, a.tag);
         }
 
         for (int t = ta; t < tb; t += kAttnWaves) {
@@ -624,9 +660,6 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                     u32x2{pack_out<ACT>(ox[e] * f, ox[e + 1] * f), pack_out<ACT>(ox[e + 2] * f, ox[e + 3] * f)};
             if (a.lse && od == 0) a.lse[(int64_t)(it.q0 + i) * a.q_heads + head] = lse;
         };
-        // Partial sums: an item that goes on in the next workgroup is the last of
-        // its first one (slot 2 wg0 + 1) and the first of the others.
-        auto slot_of = [&](int p) { return 2 * (wg0 + p) + (p == 0 ? 1 : 0); };
         auto keep_row = [&](int slot, int row, float mx, float lx, const float (&ox)[E]) {
             const uint32_t at = slot * R + row;
 #pragma unroll
@@ -686,10 +719,10 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             // ---- join the shares of the item: sixteen by their last workgroup, and
             // where there are more than sixteen, those sums by the last of all
             // as split_finish: this thread's stores are complete, then one arrival
-            auto arrive = [&](int word, int count) {
+            auto arrive = [&](unsigned long long* word, int count) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                 __syncthreads();
-                if (threadIdx.x == 0) lds_last = split_arrive(a.words + word, a.tag, count);
+                if (threadIdx.x == 0) lds_last = arrive_word(word, count);
                 __syncthreads();
                 asm volatile("" ::: "memory");
                 return lds_last != 0;
@@ -768,11 +801,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                     }
                 }
             };
-            const int p0 = part / kTeam * kTeam, teams = (parts + kTeam - 1) / kTeam, size = min(kTeam, parts - p0);
-            // words: the slot of the team's first part; for the teams, that of part 1
-            if (arrive(slot_of(p0), size)) {
+            if (arrive(team_word, size)) {
                 join(p0, 1, size, teams == 1);
-                if (teams > 1 && arrive(slot_of(1), teams)) join(0, kTeam, teams, true);
+                if (teams > 1 && arrive(teams_word, teams)) join(0, kTeam, teams, true);
             }
         }
     }
@@ -985,6 +1016,10 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         }
     }
 
+    unsigned long long* word = a.words + head_block;
+    unsigned long long seen = 0;
+    if (shares > 1 && threadIdx.x == 0) seen = peek_word(word);
+
     // ---- loads of this wave's part of a step
     const int32_t* pages = a.page_table + (int64_t)b * a.table_stride;
     const int my_tile = wave / WPT, sub = wave % WPT;
@@ -1101,6 +1136,8 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         fetch(min(1, steps - 1));
     }
 
+    if (shares > 1 && threadIdx.x == 0) claim_word(word, seen, a.tag);
+
     for (int step = 0; step < steps; ++step) {
         __syncthreads();  // buffer `step` is written, the other one is read out
         const int buf = step & 1, tok0 = (t0 + (s0 + step) * TT) * kKvTile;
@@ -1200,7 +1237,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
                                               ((first + share) * T + threadIdx.x) * 8, 0, kDeviceCoherent);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (threadIdx.x == 0) lds_scan[0] = split_arrive(a.words + head_block, a.tag, shares);
+        if (threadIdx.x == 0) lds_scan[0] = arrive_word(word, shares);
         __syncthreads();
         if (!lds_scan[0]) return;
         asm volatile("" ::: "memory");
