@@ -101,14 +101,24 @@ __device__ __forceinline__ int key_scale_lane(int r, int j) {
     return (j * L::KD / (L::G > L::KD ? L::G : L::KD) * 16 + r) * L::kKsLane;
 }
 
-template <int FMT, int D>
+// kOnce: codes that one workgroup reads once (a single row block, decode) go
+// past the caches; with several row blocks they are read again.  64 sequences
+// of 16 .. 8192 keys 75 -> 65 us, one of 131071 39 -> 36 us; four query tokens
+// (two row tiles) would lose 3 %.
+template <bool kOnce>
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
+    if constexpr (kOnce) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    else return *reinterpret_cast<const u32x4*>(p);
+}
+
+template <int FMT, int D, bool kOnce>
 __device__ __forceinline__ void load_tile(TileRegs<FMT, D>& t, const uint8_t* __restrict__ tile, int lane) {
     using L = KvTile<FMT, D>;
     const int r = lane & 15, j = lane >> 4;
 #pragma unroll
-    for (int f = 0; f < L::F; ++f) t.k[f] = *reinterpret_cast<const u32x4*>(tile + f * 1024 + lane * 16);
+    for (int f = 0; f < L::F; ++f) t.k[f] = load_codes<kOnce>(tile + f * 1024 + lane * 16);
 #pragma unroll
-    for (int f = 0; f < L::F; ++f) t.v[f] = *reinterpret_cast<const u32x4*>(tile + L::kCodes + f * 1024 + lane * 16);
+    for (int f = 0; f < L::F; ++f) t.v[f] = load_codes<kOnce>(tile + L::kCodes + f * 1024 + lane * 16);
     const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j);
     if constexpr (L::kKsLane == 2) t.ks[0] = *reinterpret_cast<const uint16_t*>(ks);
     else if constexpr (L::kKsLane == 4) t.ks[0] = *reinterpret_cast<const uint32_t*>(ks);
@@ -518,7 +528,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             page = next_bad ? 0 : page;
             const uint8_t* tile = cache.data + (((int64_t)page * kv_heads + h) * cache.tiles_per_page +
                                                 (t - page_of(t) * cache.tiles_per_page)) * (int64_t)L::kBytes;
-            load_tile<FMT, D>(next, tile, lane);
+            load_tile<FMT, D, MT == 1>(next, tile, lane);
         };
         if (ta < tb) fetch(ta);
         float fac[MT], m[MT], l[MT];

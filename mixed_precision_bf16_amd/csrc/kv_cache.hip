@@ -55,7 +55,11 @@ __device__ __forceinline__ uint8_t* kv_tile_of(const KvArgs& c, int64_t slot, in
 // One thread quantizes one block of G elements of a key or value row
 // (quantize_block, the rule of fp4_quantize) and scatters its codes and scale
 // into the tile.  Four neighbouring lanes take four consecutive tokens, whose
-// value codes are neighbours in the tile.
+// value codes are neighbours in the tile, so that the four-byte (D = 64:
+// two-byte) pieces of a wave merge into whole lines in L2.  8192 tokens of 8
+// heads of 128 (43 MB) take 12.7 us, 3.4 TB/s: bound by those scattered stores;
+// one token takes 6.2 us, latency (slot, row, scale, one division an element
+// where alpha is no power of two).
 template <int FMT, int ACT, int D>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs c, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v,
@@ -68,13 +72,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs c, const uint16_t
     const int h = blockIdx.y >> 1;
     const bool is_v = blockIdx.y & 1;
     if (token >= tokens) return;
-    const int64_t slot = slots[token];
-    if (slot < 0 || slot >= c.slots) return;
+    const int64_t slot = slots[token];  // used only after the rows' loads are under way
     const uint16_t* src = is_v ? v + token * v_ts + h * v_hs : k + token * k_ts + h * k_hs;
     const u32x4* p = reinterpret_cast<const u32x4*>(src + g * G);
     u32x4 raw[G / 8];
 #pragma unroll
     for (int i = 0; i < G / 8; ++i) raw[i] = p[i];
+    if (slot < 0 || slot >= c.slots) return;
     float x[G];
 #pragma unroll
     for (int i = 0; i < G / 2; ++i) widen2<ACT>(raw[i / 4][i % 4], x[2 * i], x[2 * i + 1]);
@@ -124,8 +128,12 @@ __device__ __forceinline__ u32x4 read_eight(uint32_t w, uint32_t sb, float alpha
 }
 
 // One thread reads eight elements of a key row and of a value row: a wave
-// writes whole rows with 16-byte stores.
-template <int FMT, int ACT, int D>
+// writes whole rows with 16-byte stores.  Bound by the bytes: 65536 tokens of 8
+// heads of 128 (NVFP4 to BF16, 344 MB) take 49 us, 7.0 TB/s.  kFar: outputs too
+// large for the caches go past them (81 us otherwise); 8192 tokens take 8.9 us
+// either way, and their reader finds them.  Two and four rows a thread were no
+// faster (52 us past the caches, 67 and 72 us through them).
+template <int FMT, int ACT, int D, bool kFar>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, const int64_t* __restrict__ slots, int tokens,
                                                       uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                       int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs) {
@@ -136,25 +144,29 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, const int64_t* _
     const int h = blockIdx.y;
     if (token >= tokens) return;
     const int64_t slot = slots[token];
-    u32x4 ko = {0u, 0u, 0u, 0u}, vo = {0u, 0u, 0u, 0u};
+    uint32_t kw = 0, vw = 0, ks = 0, vs = 0;  // zeros for a slot outside the cache
     if (slot >= 0 && slot < c.slots) {
         int t;
         const uint8_t* tile = kv_tile_of(c, slot, h, L::kBytes, t);
-        if (k)
-            ko = read_eight<FMT, ACT>(*reinterpret_cast<const uint32_t*>(tile + L::k_code(t, d)),
-                                      tile[L::k_scale(t, g)], c.k_alpha);
+        if (k) {
+            kw = *reinterpret_cast<const uint32_t*>(tile + L::k_code(t, d));
+            ks = tile[L::k_scale(t, g)];
+        }
         if (v) {
-            uint32_t w;
             if constexpr (D == 64)
-                w = *reinterpret_cast<const uint16_t*>(tile + L::v_code(t, d)) |
-                    ((uint32_t)*reinterpret_cast<const uint16_t*>(tile + L::v_code(t, d + 4)) << 16);
+                vw = *reinterpret_cast<const uint16_t*>(tile + L::v_code(t, d)) |
+                     ((uint32_t)*reinterpret_cast<const uint16_t*>(tile + L::v_code(t, d + 4)) << 16);
             else
-                w = *reinterpret_cast<const uint32_t*>(tile + L::v_code(t, d));
-            vo = read_eight<FMT, ACT>(w, tile[L::v_scale(t, g)], c.v_alpha);
+                vw = *reinterpret_cast<const uint32_t*>(tile + L::v_code(t, d));
+            vs = tile[L::v_scale(t, g)];
         }
     }
-    if (k) *reinterpret_cast<u32x4*>(k + token * k_ts + h * k_hs + d) = ko;
-    if (v) *reinterpret_cast<u32x4*>(v + token * v_ts + h * v_hs + d) = vo;
+    auto store = [](uint16_t* p, const u32x4& x) {
+        if constexpr (kFar) __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(p));
+        else *reinterpret_cast<u32x4*>(p) = x;
+    };
+    if (k) store(k + token * k_ts + h * k_hs + d, read_eight<FMT, ACT>(kw, ks, c.k_alpha));
+    if (v) store(v + token * v_ts + h * v_hs + d, read_eight<FMT, ACT>(vw, vs, c.v_alpha));
 }
 
 // Row strides (elements) of a [tokens][heads][D] array: 16-byte aligned rows.
@@ -170,6 +182,9 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs
     const bool head_major = (tokens == 1 || ts >= D) && (heads == 1 || hs >= (tokens - 1) * ts + D);
     return token_major || head_major;
 }
+
+// Outputs above this many bytes are stored past the caches.
+constexpr int64_t kReadFar = int64_t(64) << 20;
 
 // Tokens a launch covers: its work-items are counted in 32 bits.
 constexpr int64_t kKvSliceTokens = int64_t(1) << 20;
@@ -187,8 +202,12 @@ template <int FMT, int ACT, int D>
 static void read_t(const KvArgs& c, const int64_t* slots, int tokens, uint16_t* k, uint16_t* v, int64_t k_ts,
                    int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s) {
     const int64_t threads = (int64_t)tokens * (D / 8);
-    kv_read_kernel<FMT, ACT, D><<<dim3((unsigned)((threads + 255) / 256), c.kv_heads), dim3(256), 0, s>>>(
-        c, slots, tokens, k, v, k_ts, k_hs, v_ts, v_hs);
+    const dim3 grid((unsigned)((threads + 255) / 256), c.kv_heads), block(256);
+    const int64_t bytes = (int64_t)tokens * c.kv_heads * D * 2 * ((k != nullptr) + (v != nullptr));
+    if (bytes > kReadFar)
+        kv_read_kernel<FMT, ACT, D, true><<<grid, block, 0, s>>>(c, slots, tokens, k, v, k_ts, k_hs, v_ts, v_hs);
+    else
+        kv_read_kernel<FMT, ACT, D, false><<<grid, block, 0, s>>>(c, slots, tokens, k, v, k_ts, k_hs, v_ts, v_hs);
 }
 
 // Calls F<FMT, ACT, D>(args...) for the run-time format, type and head size.

@@ -616,20 +616,15 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     kernel.  window > 0: only the last `window` positions up to the query's
     own.  scale: head_dim ** -0.5 by default.  sinks: float32 [q_heads].
     Returns out ([q_rows][q_heads][head_dim] of q's type) or (out, lse) with
-    lse float32 [q_rows][q_heads].  What the wrapper allocates is zero-filled
-    (lse: -inf) when q_offsets may leave rows out."""
+    lse float32 [q_rows][q_heads]; rows that q_offsets gives to no sequence are
+    not written (in what the wrapper allocates they hold anything)."""
     import torch
     a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks)
     dev = cache.data.device
     rows, heads, dim = q.shape
     with _on_stream(dev, stream) as s:
         if out is None:
-            if q_offsets is not None:
-                out = torch.zeros((rows, heads, dim), dtype=q.dtype, device=dev)
-            elif q.is_contiguous():
-                out = torch.empty_like(q)
-            else:
-                out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+            out = torch.empty_like(q) if q.is_contiguous() else torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
         elif out.dtype != q.dtype:
             raise ValueError("out must have q's type")
         ot, oh = _rows(out, "out", rows, heads, dim, dev)
@@ -638,10 +633,7 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
             if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
                 raise ValueError(f"lse must be a contiguous float32 tensor [{rows}][{heads}] on {dev}")
         elif return_lse:
-            if q_offsets is None:
-                lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
-            else:
-                lse = torch.full((rows, heads), float("-inf"), dtype=torch.float32, device=dev)
+            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if lse is not None:
             a.lse = lse.data_ptr()
         ref = ctypes.byref(a)
