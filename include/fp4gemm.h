@@ -42,7 +42,7 @@
  *     "host" pointers must be ordinary host memory.
  *   - Functions are reentrant and thread-safe; the only global state is a
  *     per-device "is gfx950" cache, an atomic launch counter that tags the
- *     split-K arrival words, a 64-entry cache of the kernel shape chosen per
+ *     arrival words of split-K and of split attention, a 64-entry cache of the kernel shape chosen per
  *     (m, N, K, format) (behind a mutex), and the tuning overrides
  *     FP4GEMM_DECODE / FP4GEMM_PREFILL, read from the environment once per
  *     process.
@@ -371,7 +371,8 @@ typedef struct fp4_attention_args {
     const int32_t* page_table; /* device [batch][page_columns]; an entry outside [0, pages) holds no keys */
     const int32_t* seq_lens;   /* device [batch]; clamped to [0, page_columns * page_size] */
     const int32_t* q_offsets;  /* device [batch + 1]: query rows of sequence b are q_offsets[b] .. q_offsets[b + 1] - 1,
-                                  clamped to [0, q_rows]; NULL: q_rows / batch rows each.  Ranges must not overlap. */
+                                  clamped to [0, q_rows]; NULL: q_rows / batch rows each.  Where they
+                                  decrease, rows are left unwritten */
     const float* sinks;        /* device [q_heads] or NULL: exp(sink) is added to the softmax sum */
     int64_t batch, q_rows, q_heads;
     int64_t max_q;             /* about the most query tokens of a sequence (0: unknown).  Only chooses
@@ -386,8 +387,9 @@ typedef struct fp4_attention_args {
     size_t workspace_bytes;
 } fp4_attention_args;
 
-/* Workspace of fp4_attention: a function of the cache's shape and of batch,
- * q_rows, q_heads, max_q and page_columns only (no device is queried).  Its
+/* Workspace of fp4_attention: a function of the cache's shape, of batch,
+ * q_rows, q_heads, max_q and page_columns, and of whether q_offsets is NULL
+ * (no device is queried; 0 for some shapes).  Its
  * contents need no initialization and are not preserved; calls that may run
  * at the same time need separate workspaces. */
 int fp4_attention_workspace_size(const fp4_kv_cache* cache, const fp4_attention_args* args, size_t* bytes);

@@ -354,14 +354,18 @@ __device__ __forceinline__ Seq sequence_from(const AttnArgs& a, int q0, int n, i
     return x;
 }
 
-// Sequence b; one without queries for b past the batch.
+// Sequence b; one without queries for b past the batch.  `bad` is set where the
+// query offsets decrease: their sequences would overlap, and the sums over all
+// sequences that the host has bounded would not hold.
 template <int R>
-__device__ __forceinline__ Seq sequence_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ Seq sequence_of(const AttnArgs& a, int b, bool& bad) {
     if (b >= a.batch) return Seq{};
     int q0 = b * a.q_each, n = a.q_each;
     if (a.q_offsets) {
         q0 = min(max(a.q_offsets[b], 0), a.q_rows);
-        n = min(max(a.q_offsets[b + 1], q0), a.q_rows) - q0;
+        n = min(max(a.q_offsets[b + 1], 0), a.q_rows) - q0;
+        bad |= n < 0;
+        n = max(n, 0);
     }
     return sequence_from<R>(a, q0, n, min(max(a.seq_lens[b], 0), a.max_keys));
 }
@@ -428,15 +432,17 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
     };
     // A position is a unit or one of the kItemCost places before an item's units.
     auto cost = [&](const Seq& x) { return (x.units + kItemCost) * x.blocks * kv_heads; };
-    const Seq own = sequence_of<R>(a, threadIdx.x);
+    bool bad_offsets = false;
+    const Seq own = sequence_of<R>(a, threadIdx.x, bad_offsets);
     const int own_cost = cost(own);
     int total;
     const int own_first = scan(own_cost, total);
     for (int base = kAttnThreads; base < a.batch; base += kAttnThreads) {
         int sum;
-        scan(cost(sequence_of<R>(a, base + threadIdx.x)), sum);
+        scan(cost(sequence_of<R>(a, base + threadIdx.x, bad_offsets)), sum);
         total += sum;
     }
+    if (a.q_offsets && __syncthreads_or(bad_offsets)) return;  // nothing is written
     const int per = (total + a.grid - 1) / a.grid;
     const int begin = blockIdx.x * per;  // grid * per < 2^31 (checked on the host)
     if (begin >= total) return;
@@ -454,7 +460,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         if (begin >= own_first && begin < own_first + own_cost) found(own, threadIdx.x, own_first);
     } else {
         for (int base = 0, before = 0; before <= begin; base += kAttnThreads) {  // ends: begin < total
-            const Seq x = sequence_of<R>(a, base + threadIdx.x);
+            const Seq x = sequence_of<R>(a, base + threadIdx.x, bad_offsets);
             const int n = cost(x);
             int sum;
             const int first = before + scan(n, sum);
@@ -474,7 +480,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         while (item >= it.blocks * kv_heads) {  // the next sequence that has work
             seq_first += cost(it);
             if (seq_first >= end) return;
-            it = sequence_of<R>(a, ++b);  // positions remain, so there is one
+            it = sequence_of<R>(a, ++b, bad_offsets);  // positions remain, so there is one
             item = 0;
         }
         const int unit0 = seq_first + item * (it.units + kItemCost) + kItemCost;  // position of the item's first unit
@@ -941,13 +947,12 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     int b, rb;
     Seq it;
     if (a.batch <= 64) {  // every wave by itself, a sequence a lane
-        const Seq x = sequence_of<R>(a, lane);
+        bool bad_offsets = false;
+        const Seq x = sequence_of<R>(a, lane, bad_offsets);
+        if (__any(bad_offsets)) return;  // nothing is written
         const int base = min(max(x.len - x.n, 0) / (R / a.group + 1), 1 << 24);
         auto count = [&](int level) {  // blocks at this level or above
-            int n = min(max(x.blocks + base - level, 0), x.blocks);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
-            return n;
+            return __builtin_amdgcn_readlane(wave_scan(min(max(x.blocks + base - level, 0), x.blocks)), 63);
         };
         int lo = 0, hi = x.blocks > 0 ? x.blocks + base : 0;
 #pragma unroll
@@ -968,7 +973,9 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         int before = 0;
         bool there = false;
         for (int base = 0; base < a.batch && !there; base += 64 * NW) {
-            const Seq x = sequence_of<R>(a, base + threadIdx.x);
+            bool bad_offsets = false;
+            const Seq x = sequence_of<R>(a, base + threadIdx.x, bad_offsets);
+            if (__syncthreads_or(bad_offsets)) return;  // the same for all shares of a block
             int p = wave_scan(x.blocks);
             __syncthreads();
             if (lane == 63) lds_scan[wave] = p;

@@ -22,7 +22,8 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
         x.page_columns > (int64_t(1) << 31) || x.page_columns * c.page_size >= (int64_t(1) << 31))
         return FP4_ERR_SHAPE;
     const int64_t group = x.q_heads / c.kv_heads;
-    const int64_t each = x.max_q > 0 ? std::min(x.max_q, x.q_rows) : x.q_rows;
+    int64_t each = x.max_q > 0 ? std::min(x.max_q, x.q_rows) : x.q_rows;
+    if (!x.q_offsets && x.batch > 0) each = x.q_rows / x.batch;
     const int64_t rows = each * group;
     p->MT = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
     // The tiled kernel, its items cut into shares where they do not fill the
@@ -36,7 +37,7 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     p->tiled = rows >= (D == 256 ? 768 : 512) || (rows >= 128 && x.batch * c.kv_heads >= 128);
     if (p->tiled) {
         p->splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, 320 / tiled_items));
-        if (tiled_items * p->splits >= (int64_t(1) << 31)) return FP4_ERR_SHAPE;
+        if (tiled_items * p->splits >= (int64_t(1) << 23)) return FP4_ERR_SHAPE;  // a launch's work-items fit 32 bits
         p->grid = (int)(tiled_items * p->splits);
         const size_t slots = p->splits > 1 ? (size_t)p->grid : 0;
         p->ml_off = slots * tiled * D * 4;
@@ -127,7 +128,8 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.inv_group = 1.0f / a.group;
     a.grid = p.grid;
     a.splits = p.splits;
-    a.tag = next_split_tag();
+    // spread over all 32 bits: a word of an unused workspace is unlikely to carry it
+    a.tag = next_split_tag() * 2654435761u;
     char* ws = static_cast<char*>(x->workspace);
     a.ws_o = reinterpret_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float*>(ws + p.ml_off);

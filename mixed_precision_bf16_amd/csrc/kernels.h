@@ -1286,7 +1286,11 @@ __device__ __forceinline__ float e4m3_decode(uint32_t byte) {
 }
 
 // One block of G elements x: its codes (element i in nibble i) and, returned,
-// its scale byte.  x: BF16 or FP16 values (at most 11 significant bits).
+// its scale byte.  x: BF16 or FP16 values.  The arguments below are worded for
+// BF16's 8 significant bits; with FP16's 11 they hold as well: |x| and a
+// midpoint times a 4-bit significand are integers below 2^11 and 2^7 times
+// powers of two, so they are equal or differ by at least 2^-11 relative, over
+// 4000 ulps of FP32.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize_block(const float (&x)[FMT == 0 ? 16 : 32], float alpha,
                                                    uint32_t (&out)[FMT == 0 ? 2 : 4]) {

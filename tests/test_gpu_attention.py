@@ -288,6 +288,50 @@ def test_offsets_out_of_range_are_clamped():
     p.check(p.run(offsets=off))
 
 
+@pytest.mark.parametrize("rows,max_q,off", [(6, 1, [0, 6, 2, 6]), (1400, 1400, [0, 1400, 700, 1400])])
+def test_offsets_that_decrease_write_nothing(rows, max_q, off):
+    p = Problem([50, 60, 70], [2, 2, 2], 0, BF16, seed=22)
+    q = torch.zeros((rows, 8, 128), dtype=BF16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((rows, 8), 7.0, device="cuda")
+    args = (q, p.cache(), torch.from_numpy(p.table).cuda(), torch.tensor(p.lens, dtype=torch.int32, device="cuda"))
+    F.attention(*args, q_offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_q=max_q, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7) and torch.all(lse == 7)
+
+
+def test_a_query_of_nan_stays_alone():
+    for news, max_q in (([3, 1], 3), ([70, 64], None)):
+        p = Problem([200, 300], news, 0, BF16, seed=23)
+        want = p.run(max_q=max_q)
+        p.q[1, 2, 5] = float("nan")
+        p.q[2, 3, :] = float("inf")
+        got = p.run(max_q=max_q)
+        keep = torch.ones(got[1].shape, dtype=torch.bool, device="cuda")
+        keep[1, 2] = keep[2, 3] = False
+        assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep], want[1][keep])
+        assert torch.all(torch.isnan(got[0][1, 2])) and torch.all(torch.isnan(got[0][2, 3]))
+
+
+@pytest.mark.parametrize("B", [70, 600])
+def test_prompts_of_many_sequences(B):
+    """More sequences than a wave's lanes: blocks in the order of the sequences."""
+    rng = np.random.Generator(np.random.PCG64(B))
+    news = [int(x) for x in rng.integers(0, 40, B)]
+    lens = [n + int(x) for n, x in zip(news, rng.integers(0, 60, B))]
+    p = Problem(lens, news, 1, BF16, 64, 4, 4, 32, seed=B)
+    got = p.run(max_q=64)
+    few = sorted({0, 1, B // 2, 63, 64, 65, B - 2, B - 1})
+    one = Problem.__new__(Problem)
+    for b in few:
+        one.__dict__.update(p.__dict__)
+        lo, hi = int(p.offsets[b]), int(p.offsets[b + 1])
+        if lo == hi:
+            continue
+        one.lens, one.table, one.q = [p.lens[b]], p.table[b:b + 1], p.q[lo:hi]
+        one.offsets = np.array([0, hi - lo], np.int32)
+        one.check((got[0][lo:hi], got[1][lo:hi]))
+
+
 def test_graph_replay_follows_the_data():
     """A captured step (append, attention) replayed with other lengths, tokens
     and queries, the program's own work between the replays; a second graph
