@@ -29,10 +29,9 @@ constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // Waves per SIMD that the streaming kernel's registers allow; the GPU then holds
 // 256 times as many of its workgroups (a workgroup has a wave on each SIMD).
 constexpr int attn_waves(int D, int MT) { return D * MT <= 64 ? 4 : D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1; }
-#ifndef FP4_ITEM_COST
-#define FP4_ITEM_COST 3
-#endif
-constexpr int kItemCost = FP4_ITEM_COST;
+// Units that the fixed cost of an item is worth (1: windowed layer 14.7 us, 3:
+// 11.0, 5: 10.9; 64 sequences 76, 75, 77).
+constexpr int kItemCost = 3;
 constexpr int kAhead = 4;              // fragments of LDS read ahead by the tiled kernel
 constexpr int kTeam = 16;              // shares of an item that are joined at a time
 constexpr int kUnitTiles = kAttnWaves;  // tiles of a work unit: one per wave
@@ -332,6 +331,19 @@ __device__ __forceinline__ RowRange row_range(int i, int n, int len, int causal,
 // short sequences load it evenly, whatever the lengths on the device are.  An
 // item that falls into several workgroups is joined by the one that arrives
 // last, from the FP32 partial sums of all, in their order.
+//
+// Bound by HBM while it streams: 12 waves a CU, each with the next tile's 4.6 KB
+// under way, read 7 TB/s; around that a workgroup spends 1.3 us on the scan of
+// the sequences, 1.5 us to its first tile, 1 us to join its waves and 2 us to
+// keep a partial sum and arrive.  Measured (MI355X, kernel time, 64 query and 8
+// KV heads of 128): 64 sequences of 16 .. 8192 keys, NVFP4, 59 us (304 MB, 5.1
+// TB/s); one sequence of 131071 keys, MXFP4, 35 us (143 MB, 4.1 TB/s; its 94
+// partial sums a head are joined in two stages of sixteen, which costs 6 us
+// against 11 us in one); one of 1000 keys 9 us, latency; four query tokens each
+// over 16 sequences of 1000 .. 5000 keys 28 us, where two row tiles bring the
+// vector work of a tile above its load time.  Tried: shares of equal length
+// dispatched one a workgroup (77 us for the first case, where this took 75) and
+// drawn from an atomic counter (115 us and more: all workgroups queue at it).
 struct Seq {
     int q0, n;       // first query row, query tokens
     int len;         // keys
@@ -848,7 +860,16 @@ __device__ __forceinline__ void unrolled(Fn&& f) {
 // beside them, while beside the 16x16x32 form they mostly wait (measured with
 // four waves a SIMD, per 16384 products: four FP4 converts alone 19.5 cycles,
 // with the 16x16x32 form 27.8, with half a 32x32x16 one 23.4; two exponentials
-// 19.2, 27.6, 21.7).
+// 19.2, 27.6, 21.7).  Head size 256 takes the 16x16x32 form with 16 rows a wave:
+// the accumulators of 32 rows and their queries leave no registers for two
+// waves a SIMD (six prompts: 253 us with one wave, 207 with spills, 180 so).
+//
+// Bound by power: a chunk of 2048 tokens over 8192 keys (NVFP4, 64 and 8 heads
+// of 128) takes 452 us in a row of calls, 1065 TFLOP/s against 1311 of a large
+// library product, with the clock down to 1.8 GHz; the matrix cores are busy 43 %
+// of the cycles, the vector units 48 %.  So what saves work counts more than what
+// overlaps it: 256 rows a workgroup instead of 128 (570 -> 537 us, half the
+// dequantization) and steps of four tiles instead of two (-> 490 us).
 //   S^T = K Q^T: with lane = 32 h + t, step i of a chunk takes the eight
 //   elements of octet (j, s) of token t, j = 2 (i / S) + h, s = i mod S, where
 //   octet (j, s) is dword s of the codes of lane (t mod 16, j);

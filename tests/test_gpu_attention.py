@@ -381,6 +381,49 @@ def test_graph_replay_follows_the_data():
         assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
 
 
+def test_graph_replay_of_a_split_chunk():
+    """The tiled kernel with shares of the keys, captured once, replayed over
+    other lengths (also ones too short to share)."""
+    p = Problem([3000, 2000], [70, 70], 1, FP16, 128, 1, 8, 64, seed=24)
+    q, cache, table = p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(F.attention_workspace_size(q, cache, table, lens), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    out, lse = torch.empty_like(q), torch.empty((140, 8), device="cuda")
+    F.attention(q, cache, table, lens, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        F.attention(q, cache, table, lens, out=out, lse=lse, workspace=ws)
+    for a, b in ((3000, 2000), (70, 1999), (513, 69), (0, 2000), (2999, 128)):
+        lens.copy_(torch.tensor([a, b], dtype=torch.int32))
+        want = F.attention(q, cache, table, lens, return_lse=True)
+        torch.cuda.synchronize()
+        out.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, interleaved."""
+    ps = [Problem([4000, 50], [1, 1], 0, BF16, seed=25), Problem([2500], [70], 0, BF16, 128, 1, 8, seed=26)]
+    want = [p.run() for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    args = [(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+             torch.tensor(p.lens, dtype=torch.int32, device="cuda")) for p in ps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(F.attention(*args[i], scale=ps[i].scale, stream=s, return_lse=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
+
+
 def _appended(cache, kv, H, slots):
     c = F.KVCache(cache.data.clone(), cache.pages, cache.page_size, cache.kv_heads, cache.head_dim, cache.fmt)
     F.kv_append(c, kv[:, :H], kv[:, H:], slots)
