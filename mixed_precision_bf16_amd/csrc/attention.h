@@ -866,8 +866,8 @@ __device__ __forceinline__ void unrolled(Fn&& f) {
 //
 // Bound by power: a chunk of 2048 tokens over 8192 keys (NVFP4, 64 and 8 heads
 // of 128) takes 452 us in a row of calls, 1065 TFLOP/s against 1311 of a large
-// library product, with the clock down to 1.8 GHz; the matrix cores are busy 43 %
-// of the cycles, the vector units 48 %.  So what saves work counts more than what
+// library product, with the clock down to 1.75 GHz; the matrix cores are busy 51 %
+// of the cycles, the vector units as long.  So what saves work counts more than what
 // overlaps it: 256 rows a workgroup instead of 128 (570 -> 537 us, half the
 // dequantization) and steps of four tiles instead of two (-> 490 us).
 //   S^T = K Q^T: with lane = 32 h + t, step i of a chunk takes the eight
