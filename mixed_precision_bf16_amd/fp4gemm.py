@@ -9,6 +9,7 @@ the library is missing or the device is not gfx950, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -404,6 +405,7 @@ def gemm_native(A, wq, sq, N: int, K: int, out=None, workspace=None, stream=None
 
 
 # ------------------------------------------------- FP4 key/value cache, attention
+@functools.lru_cache(maxsize=256)
 def kv_cache_size(pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int) -> int:
     """Bytes of a cache of this shape (fp4_kv_cache_size)."""
     b = _c_sz()
@@ -552,12 +554,16 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
     sp = _vector(slots, "slots", n, torch.int64, dev)
     with _on_stream(dev, stream) as s:
         shape = (n, cache.kv_heads, cache.head_dim)
+        kt = vt = cache.kv_heads * cache.head_dim  # strides of what is allocated here
+        kh = vh = cache.head_dim
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            kt, kh = _rows(k_out, "k_out", *shape, dev)
         if v_out is None:
-            v_out = torch.empty_like(k_out) if k_out.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
-        kt, kh = _rows(k_out, "k_out", *shape, dev)
-        vt, vh = _rows(v_out, "v_out", *shape, dev)
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            vt, vh = _rows(v_out, "v_out", *shape, dev)
         st = lib().fp4_kv_read(cache._ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), kt, kh, vt, vh, act, s)
     if st:
         _check(st, "fp4_kv_read")
@@ -625,9 +631,11 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     with _on_stream(dev, stream) as s:
         if out is None:
             out = torch.empty_like(q) if q.is_contiguous() else torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+            ot, oh = heads * dim, dim
         elif out.dtype != q.dtype:
             raise ValueError("out must have q's type")
-        ot, oh = _rows(out, "out", rows, heads, dim, dev)
+        else:
+            ot, oh = _rows(out, "out", rows, heads, dim, dev)
         a.out, a.out_token_stride, a.out_head_stride = out.data_ptr(), ot, oh
         if lse is not None:
             if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
