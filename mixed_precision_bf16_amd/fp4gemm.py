@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 
 import numpy as np
 
@@ -41,6 +42,10 @@ class _AttentionArgs(ctypes.Structure):
                 ("q_head_stride", _c_i64), ("out_token_stride", _c_i64), ("out_head_stride", _c_i64),
                 ("window", _c_i64), ("causal", ctypes.c_int32), ("act_type", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("workspace", _c_vp), ("workspace_bytes", _c_sz)]
+
+
+# the same structure as bytes, which is quicker to fill
+_PACK_ATTENTION = struct.Struct("@7Q11q2if4x2Q")
 
 
 # name -> (restype, argtypes); mirrors include/fp4gemm.h
@@ -74,9 +79,8 @@ _SIGNATURES = {
                                      _c_i64, _c_i64, ctypes.c_int, _c_vp]),
     "fp4_kv_read": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
                                    _c_i64, _c_i64, ctypes.c_int, _c_vp]),
-    "fp4_attention_workspace_size": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), ctypes.POINTER(_AttentionArgs),
-                                                    ctypes.POINTER(_c_sz)]),
-    "fp4_attention": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), ctypes.POINTER(_AttentionArgs), _c_vp]),
+    "fp4_attention_workspace_size": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, ctypes.POINTER(_c_sz)]),
+    "fp4_attention": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_vp]),
 }
 
 STATUS = {0: "FP4_OK", 1: "FP4_ERR_NULL", 2: "FP4_ERR_SHAPE", 3: "FP4_ERR_FORMAT", 4: "FP4_ERR_VALUE",
@@ -570,7 +574,9 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
     return k_out, v_out
 
 
-def _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks):
+def _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q):
+    """Checks of the tensors that every call has; (device, activation type,
+    pointers, sizes, query strides) as fp4_attention_args takes them."""
     import torch
     dev = cache.data.device
     if q.dim() != 3:
@@ -582,7 +588,7 @@ def _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, wi
             or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
         raise ValueError(f"page_table must be an int32 matrix [batch][columns] on {dev} with contiguous rows")
     batch, columns = page_table.shape
-    offsets = sink = None
+    offsets = 0
     if q_offsets is not None:
         offsets = _vector(q_offsets, "q_offsets", batch + 1, torch.int32, dev)
         if max_q is None:
@@ -591,21 +597,33 @@ def _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, wi
         if batch and rows % batch:
             raise ValueError("q_rows must be a multiple of the batch without q_offsets")
         max_q = rows // batch if batch else 0
-    if sinks is not None:
-        sink = _vector(sinks, "sinks", heads, torch.float32, dev)
-    return _AttentionArgs(q.data_ptr(), None, None, page_table.data_ptr(),
-                          _vector(seq_lens, "seq_lens", batch, torch.int32, dev), offsets, sink, batch, rows, heads,
-                          max_q, columns, page_table.stride(0) if batch > 1 else columns, qt, qh, 0, 0, window,
-                          1 if causal else 0, act, cache.head_dim ** -0.5 if scale is None else scale, None, 0)
+    pointers = page_table.data_ptr(), _vector(seq_lens, "seq_lens", batch, torch.int32, dev), offsets
+    sizes = batch, rows, heads, max_q, columns, page_table.stride(0) if batch > 1 else columns
+    return dev, act, pointers, sizes, (qt, qh)
+
+
+def _pack_attention(*fields) -> bytes:
+    try:
+        return _PACK_ATTENTION.pack(*fields)
+    except struct.error as e:
+        raise ValueError(f"attention: {e}") from None
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(kv_heads, page_size, head_dim, fmt, batch, rows, heads, max_q, columns, offsets) -> int:
+    c = _KVCacheDesc(None, 1, page_size, kv_heads, head_dim, fmt, 1.0, 1.0)
+    a = _pack_attention(0, 0, 0, 0, 0, 4 if offsets else 0, 0, batch, rows, heads, max_q, columns, columns, 0, 0, 0, 0,
+                        0, 1, 0, 1.0, 0, 0)
+    b = _c_sz()
+    _check(lib().fp4_attention_workspace_size(ctypes.byref(c), a, ctypes.byref(b)), "fp4_attention_workspace_size")
+    return b.value
 
 
 def attention_workspace_size(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None) -> int:
     """Bytes of workspace that attention() needs for these shapes."""
-    a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, True, 0, None, None)
-    b = _c_sz()
-    _check(lib().fp4_attention_workspace_size(cache._ref, ctypes.byref(a), ctypes.byref(b)),
-           "fp4_attention_workspace_size")
-    return b.value
+    _, _, _, sizes, _ = _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q)
+    return _attention_workspace(cache.kv_heads, cache.page_size, cache.head_dim, cache.fmt, *sizes[:5],
+                                q_offsets is not None)
 
 
 def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None, causal: bool = True,
@@ -625,9 +643,9 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     lse float32 [q_rows][q_heads]; rows that q_offsets gives to no sequence are
     not written (in what the wrapper allocates they hold anything)."""
     import torch
-    a = _attention_args(q, cache, page_table, seq_lens, q_offsets, max_q, causal, window, scale, sinks)
-    dev = cache.data.device
+    dev, act, pointers, sizes, strides = _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q)
     rows, heads, dim = q.shape
+    sink = _vector(sinks, "sinks", heads, torch.float32, dev) if sinks is not None else 0
     with _on_stream(dev, stream) as s:
         if out is None:
             out = torch.empty_like(q) if q.is_contiguous() else torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
@@ -636,25 +654,22 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
             raise ValueError("out must have q's type")
         else:
             ot, oh = _rows(out, "out", rows, heads, dim, dev)
-        a.out, a.out_token_stride, a.out_head_stride = out.data_ptr(), ot, oh
         if lse is not None:
             if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
                 raise ValueError(f"lse must be a contiguous float32 tensor [{rows}][{heads}] on {dev}")
         elif return_lse:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
-        if lse is not None:
-            a.lse = lse.data_ptr()
-        ref = ctypes.byref(a)
         if workspace is None:
-            b = _c_sz()
-            _check(lib().fp4_attention_workspace_size(cache._ref, ref, ctypes.byref(b)),
-                   "fp4_attention_workspace_size")
-            workspace = torch.empty(b.value, dtype=torch.uint8, device=dev)
+            need = _attention_workspace(cache.kv_heads, cache.page_size, dim, cache.fmt, *sizes[:5],
+                                        q_offsets is not None)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         elif not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        a.workspace = workspace.data_ptr()
-        a.workspace_bytes = workspace.numel() * workspace.element_size()
-        st = lib().fp4_attention(cache._ref, ref, s)
+        args = _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0, *pointers, sink,
+                               *sizes, *strides, ot, oh, window, 1 if causal else 0, act,
+                               dim ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size())
+        st = lib().fp4_attention(cache._ref, args, s)
     if st:
         _check(st, "fp4_attention")
     return (out, lse) if return_lse else out

@@ -194,6 +194,17 @@ def test_workspace_depends_on_shapes_only():
     assert size() == size(causal=0, window=0, act_type=1, scale=3.0)
 
 
+def test_packed_arguments_are_the_structure():
+    values = list(range(1, 8)) + list(range(11, 22)) + [1, 0, 0.5, 31, 32]
+    raw = F._pack_attention(*values)
+    assert len(raw) == ctypes.sizeof(F._AttentionArgs)
+    a = F._AttentionArgs.from_buffer_copy(raw)
+    assert [getattr(a, n) for n, _ in F._AttentionArgs._fields_] == values
+    for at, bad in ((17, 1 << 63), (10, 2.5)):
+        with pytest.raises(ValueError):
+            F._pack_attention(*values[:at], bad, *values[at + 1:])
+
+
 def test_binding_refuses_host_tensors():
     c = torch.zeros(F.kv_cache_size(1, 32, 1, 64, 0), dtype=torch.uint8)
     with pytest.raises(ValueError):
