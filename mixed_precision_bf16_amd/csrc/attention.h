@@ -13,7 +13,10 @@
 // only when a score exceeds the running maximum by more than kSlack binary
 // orders, which a wave decides together: probabilities stay below
 // 2^(kBias + kSlack), in range for FP16, and kBias moves the point where FP16
-// probabilities vanish to 2^-(24 + kBias) of the largest one.
+// probabilities vanish to 2^-(24 + kBias) of the largest one.  The one rounding
+// below 32 bits before the output's is that of the probabilities to the
+// matrix-core type (half a step: 2^-11, with BF16 2^-8, the size of the output's
+// own); their sum takes them unrounded, so that the log-sum-exp keeps FP32.
 #pragma once
 #include <type_traits>
 #include <utility>
