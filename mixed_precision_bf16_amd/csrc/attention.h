@@ -60,7 +60,7 @@ struct AttnArgs {
     float inv_group;           // 1 / group
     int grid;                  // workgroups; in the streaming kernel as many as the GPU holds
     int splits;                // tiled kernel: most shares of an item
-    uint32_t tag;
+    unsigned long long tag;    // of the arrival words
     float* ws_o;               // [2 * grid][rows][D]; tiled kernel: [grid][D / 4][rows][4] and so on
     float* ws_ml;              // [2 * grid][rows][2]
     unsigned long long* words; // [2 * grid]
@@ -71,14 +71,14 @@ struct AttnArgs {
 // the last arrival leaves 0), with the tag installed well before the arrival,
 // under the shadow of the first loads: the arrival itself is then one atomic.
 // Every workgroup claims its words before it arrives, so they carry the tag.
-__device__ __forceinline__ void claim_word(unsigned long long* w, unsigned long long seen, uint32_t tag) {
-    const unsigned long long mine = (unsigned long long)tag << 32;
-    if ((seen >> 32) != (unsigned long long)tag)  // fails only if another workgroup has installed the tag
-        __hip_atomic_compare_exchange_strong(w, &seen, mine, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+__device__ __forceinline__ void claim_word(unsigned long long* w, unsigned long long seen, unsigned long long tag) {
+    if (!carries_tag(seen, tag))  // the exchange fails only if another workgroup has installed the tag
+        __hip_atomic_compare_exchange_strong(w, &seen, tag, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
                                              __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ bool arrive_word(unsigned long long* w, int count) {
-    const uint32_t n = (uint32_t)__hip_atomic_fetch_add(w, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+__device__ __forceinline__ bool arrive_word(unsigned long long* w, int count, unsigned long long tag) {
+    const uint32_t n =
+        (uint32_t)(__hip_atomic_fetch_add(w, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - tag) + 1u;
     if (n == (uint32_t)count) __hip_atomic_store(w, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return n == (uint32_t)count;
 }
@@ -753,7 +753,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             auto arrive = [&](unsigned long long* word, int count) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                 __syncthreads();
-                if (threadIdx.x == 0) lds_last = arrive_word(word, count);
+                if (threadIdx.x == 0) lds_last = arrive_word(word, count, a.tag);
                 __syncthreads();
                 asm volatile("" ::: "memory");
                 return lds_last != 0;
@@ -1278,7 +1278,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
                                               ((first + share) * T + threadIdx.x) * 8, 0, kDeviceCoherent);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (threadIdx.x == 0) lds_scan[0] = arrive_word(word, shares);
+        if (threadIdx.x == 0) lds_scan[0] = arrive_word(word, shares, a.tag);
         __syncthreads();
         if (!lds_scan[0]) return;
         asm volatile("" ::: "memory");

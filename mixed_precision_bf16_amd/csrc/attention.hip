@@ -55,6 +55,7 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t most = 256 * attn_waves((int)D, p->MT);
     if (items > (int64_t(1) << 30) || items * (units + kItemCost) >= (int64_t(1) << 31) - most) return FP4_ERR_SHAPE;
     p->grid = (int)std::max<int64_t>(1, std::min(most, items * units));
+    static_assert(256 * attn_waves(64, 1) / kTeam < 1 << kCountBits && kTeam < 1 << kCountBits, "arrivals at a word");
     const size_t slots = 2 * (size_t)p->grid;
     p->ml_off = slots * R * D * 4;
     p->word_off = p->ml_off + slots * R * 8;
@@ -128,8 +129,7 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.inv_group = 1.0f / a.group;
     a.grid = p.grid;
     a.splits = p.splits;
-    // spread over all 32 bits: a word of an unused workspace is unlikely to carry it
-    a.tag = next_split_tag() * 2654435761u;
+    a.tag = next_split_tag();
     char* ws = static_cast<char*>(x->workspace);
     a.ws_o = reinterpret_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float*>(ws + p.ml_off);

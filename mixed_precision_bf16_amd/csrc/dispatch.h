@@ -11,7 +11,7 @@ namespace fp4 {
 // Shared by the C entries of every translation unit (fp4gemm.hip).
 int check_device();         // FP4_OK when the current device is a gfx950
 int launch_status();        // FP4_OK / FP4_ERR_HIP from the launches since the last hipGetLastError
-uint32_t next_split_tag();  // launch tag of split-K arrival words: unique per launch, never 0
+uint64_t next_split_tag();  // launch tag of arrival words (above their count): unique per launch, never 0
 bool alpha_ok(float alpha);
 
 // Decode kernel: TN n-tiles per wave, NWN waves per K group, NWK K groups per
@@ -59,10 +59,10 @@ struct MoeArgs {
 // its K split itself (arrival words after the partials, `tag` unique to the
 // launch); the prefill kernel leaves the partials to reduce_partials.
 bool launch_decode_bf16(int fmt, int MB, const DecodeShape& d, const void* A, const void* wq, const void* sq,
-                        void* C, float* P, int M, int N, int K, int KB, int SB, int NT, float alpha, uint32_t tag,
+                        void* C, float* P, int M, int N, int K, int KB, int SB, int NT, float alpha, uint64_t tag,
                         hipStream_t s);
 bool launch_decode_f16(int fmt, int MB, const DecodeShape& d, const void* A, const void* wq, const void* sq, void* C,
-                       float* P, int M, int N, int K, int KB, int SB, int NT, float alpha, uint32_t tag,
+                       float* P, int M, int N, int K, int KB, int SB, int NT, float alpha, uint64_t tag,
                        hipStream_t s);
 bool launch_prefill_bf16(int fmt, const PrefillShape& t, const void* A, const void* wq, const void* sq, void* C,
                          float* P, int M, int N, int K, int KB, int SB, int NT, float alpha, hipStream_t s);

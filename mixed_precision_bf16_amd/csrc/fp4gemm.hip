@@ -128,11 +128,14 @@ static size_t decode_workspace_bytes(const DecodeShape& d, int64_t M, int64_t N,
     return split_counter_floats(d.s, int(M), int(N)) * sizeof(float) + (size_t)groups * 8;
 }
 
-// Launch tags of the split-K arrival words: unique per launch (never 0).
-static std::atomic<uint32_t> g_split_tag{0};
-uint32_t next_split_tag() {
-    uint32_t t;
-    do t = g_split_tag.fetch_add(1, std::memory_order_relaxed) + 1;
+// Launch tags of the arrival words: unique per launch (never 0).  The odd
+// factor permutes the 52-bit numbers and spreads them over all bits, so that
+// no kind of bytes that a workspace may hold (small integers, sizes, repeated
+// floats) is likelier than another to carry a tag.
+static std::atomic<uint64_t> g_split_tag{0};
+uint64_t next_split_tag() {
+    uint64_t t;
+    do t = (g_split_tag.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7ull << kCountBits;
     while (t == 0);
     return t;
 }
@@ -341,7 +344,7 @@ static int launch_gemm(const GemmPlan& plan, int fmt, int act, const void* A, co
     if (plan.kind == GemmPlan::kDecode) {
         const DecodeShape& d = plan.d;
         float* P = d.s > 1 ? static_cast<float*>(ws) : nullptr;
-        const uint32_t tag = P ? next_split_tag() : 0u;
+        const uint64_t tag = P ? next_split_tag() : 0;
         const bool ok =
             act == 0 ? launch_decode_bf16(fmt, plan.MB, d, A, wq, sq, C, P, M, N, K, KB, SB, NT, alpha, tag, s)
                      : launch_decode_f16(fmt, plan.MB, d, A, wq, sq, C, P, M, N, K, KB, SB, NT, alpha, tag, s);

@@ -226,16 +226,25 @@ __device__ __forceinline__ u32x4 load_scale_block(__amdgpu_buffer_rsrc_t r, int 
 // order s = 0, 1, ... (device-coherent loads), scales by alpha and writes
 // the output.  Because every access to the partials and to the arrival word
 // is device-coherent, no cache-wide write-back or invalidate is needed.
-// The arrival word is (tag << 32) | count with a tag unique to the launch
-// (never 0): a word holding any other tag (stale words of earlier launches,
-// partial sums of other shapes, uninitialized memory) counts as zero, so the
-// workspace needs no initialization.  The last arrival writes 0 instead of
-// the full count, so a launch replayed with the same tag (a captured HIP
-// graph bakes the tag into the kernel arguments) finds the word at zero
-// again.  The arrival words follow the partials at a 256-byte aligned
-// offset (in floats):
+// The arrival word holds a tag of 52 bits, unique to the launch and never 0,
+// above a count of 12 bits: a word holding any other tag (stale words of
+// earlier launches, partial sums of other shapes, uninitialized memory) counts
+// as zero, so the workspace needs no initialization.  (Bytes that no launch
+// wrote carry the tag with a chance of 2^-52 a word.  Such a word would lose
+// its output without an error, and a call can use hundreds of words, so the
+// tag takes every bit that the count can spare.)  The last arrival writes 0
+// instead of the full count, so a launch replayed with the same tag (a captured
+// HIP graph bakes the tag into the kernel arguments) finds the word at zero
+// again.  The arrival words follow the partials at a 256-byte aligned offset
+// (in floats):
 __host__ __device__ inline size_t split_counter_floats(int S, int M, int N) {
     return ((size_t)S * (size_t)M * (size_t)N + 63) / 64 * 64;
+}
+
+constexpr int kCountBits = 12;  // of an arrival word; a tag has zeros there (next_split_tag)
+
+__device__ __forceinline__ bool carries_tag(unsigned long long word, unsigned long long tag) {
+    return (word ^ tag) >> kCountBits == 0;
 }
 
 // Partial plane ks of an S-way split (M x N FP32, M * N < 2^29).
@@ -269,14 +278,13 @@ __device__ __forceinline__ void store_partial(__amdgpu_buffer_rsrc_t pl, const f
 // with a compare-exchange that installs (tag, 1).  Workgroups that arrive
 // together thus pay at most one failed exchange each, then one add, instead
 // of retrying an exchange once per earlier arrival.
-__device__ __forceinline__ bool split_arrive(unsigned long long* w, uint32_t tag, int S) {
-    const unsigned long long mine = (unsigned long long)tag << 32;
+__device__ __forceinline__ bool split_arrive(unsigned long long* w, unsigned long long tag, int S) {
     unsigned long long cur = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     for (;;) {  // a failed exchange means another workgroup changed the word: at most S - 1 turns
         uint32_t cnt;
-        if ((cur >> 32) == (unsigned long long)tag) {
-            cnt = (uint32_t)__hip_atomic_fetch_add(w, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
-        } else if (__hip_atomic_compare_exchange_strong(w, &cur, S == 1 ? 0ull : mine | 1ull, __ATOMIC_RELAXED,
+        if (carries_tag(cur, tag)) {
+            cnt = (uint32_t)(__hip_atomic_fetch_add(w, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - tag) + 1u;
+        } else if (__hip_atomic_compare_exchange_strong(w, &cur, S == 1 ? 0ull : tag | 1ull, __ATOMIC_RELAXED,
                                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) {
             cnt = 1u;
         } else {
@@ -340,7 +348,7 @@ __device__ __forceinline__ void split_sum(const float* P, uint16_t* __restrict__
 template <int ACT, int kThreads>
 __device__ __forceinline__ void split_finish(const float* P, uint16_t* __restrict__ C, int M, int N, int S, int grp,
                                              int m_begin, int m_end, int n_begin, int n_end, float alpha,
-                                             uint32_t tag) {
+                                             unsigned long long tag) {
     __shared__ int last;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this thread's partial stores are complete
     __syncthreads();
@@ -440,7 +448,7 @@ __global__ __launch_bounds__(64 * NWN * NWK) void gemm_decode(const uint16_t* __
                                                              const uint8_t* __restrict__ sq,
                                                              uint16_t* __restrict__ C, float* __restrict__ P, int M,
                                                              int N, int K, int KB, int SB, int NT, int S,
-                                                             float alpha, uint32_t tag, MoeArgs moe = MoeArgs{}) {
+                                                             float alpha, unsigned long long tag, MoeArgs moe = MoeArgs{}) {
     typedef u32x4 SW;
     constexpr int kRows = 16 * MB;  // activation rows; one 1 KiB load per row per block
     // Activation load instructions per wave per block (row wn + NWN u).  When
