@@ -396,9 +396,16 @@ int fp4_attention_workspace_size(const fp4_kv_cache* cache, const fp4_attention_
 
 /* out = softmax(scale * q . K^T + mask) . V over the cache, on `stream`.
  * Accumulation, softmax and sums in FP32; the products run on the 16-bit
- * matrix cores (BF16 activations with MXFP4 caches: BF16, else FP16; scales
- * of an MXFP4 cache above 2^125, with FP16 activations above 2^13, act as
- * that).  A query row that sees no key gives out 0 and lse -Inf (or the
+ * matrix cores (BF16 activations with MXFP4 caches: BF16, else FP16), on code *
+ * scale products that are exact but for these limits of MXFP4 caches:
+ *   FP16 activations: rows are taken in FP16's range, in units of alpha /
+ *   2^floor(log2 alpha), whatever alpha is.  Blocks of elements from 2^16 on
+ *   (infinities, rows written from BF16) act as if their scale were 2^13 in
+ *   these units, and blocks below 2^-20 throughout round to multiples of 2^-24.
+ *   BF16 activations: blocks written from infinities act as if their scale
+ *   were at most 2^125, blocks below 2^-124 as if it were at least 2^-127, and
+ *   values above 2^112 / keys can overflow the FP32 sums.
+ * A query row that sees no key gives out 0 and lse -Inf (or the
  * sink's logarithm, out 0).  Rows of q that belong to no sequence leave out
  * and lse as they were.  All sizes that depend on the data (seq_lens,
  * q_offsets, page_table) stay on the device: a call captured in a HIP graph

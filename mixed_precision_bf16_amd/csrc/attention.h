@@ -5,9 +5,15 @@
 //   out = sum_j p_j v_j / l,  lse = m + ln l.
 //
 // Both products run on the 16-bit matrix cores with FP32 accumulation, on
-// keys and values dequantized in registers (every code x scale product is
-// exact in the type used): FP16 for NVFP4 caches and for FP16 activations,
-// BF16 for MXFP4 caches with BF16 activations (E8M0 scales need its range).
+// keys and values dequantized in registers: FP16 for NVFP4 caches and for FP16
+// activations, BF16 for MXFP4 caches with BF16 activations (E8M0 scales need
+// its range).  Every NVFP4 code x scale product is exact in FP16.  An E8M0
+// scale takes alpha's exponent e = floor(log2 alpha) along into the convert, so
+// that the 16-bit values have the size of the rows themselves, whatever alpha
+// is, and only alpha / 2^e, in [1, 2), is applied in FP32: exact in BF16, and in
+// FP16 for every block whose largest element is at least 2^-20 and below 2^16.
+// (In FP16 the codes of smaller blocks round to multiples of 2^-24, the step of
+// FP16 rows themselves, and those of larger ones saturate.)
 // The softmax runs in FP32 in base 2 with one pass over the keys: a running
 // maximum m and sum l per query row.  Rows of the accumulators are rescaled
 // only when a score exceeds the running maximum by more than kSlack binary
@@ -55,8 +61,9 @@ struct AttnArgs {
     int max_keys;              // table_cols * page_size
     int window, causal;
     uint64_t tpp_magic;        // ceil(2^36 / tiles_per_page): the page of tile t < 2^26 is t * magic >> 36
-    float scale;               // scale * k_alpha * log2(e)
-    float v_alpha;
+    int k_exp, v_exp;          // MXFP4: exponents of k_alpha and v_alpha, which the block scales take along; else 0
+    float scale;               // scale * k_alpha / 2^k_exp * log2(e)
+    float v_alpha;             // v_alpha / 2^v_exp
     float inv_group;           // 1 / group
     int grid;                  // workgroups; in the streaming kernel as many as the GPU holds
     int splits;                // tiled kernel: most shares of an item
@@ -136,13 +143,14 @@ __device__ __forceinline__ void load_tile(TileRegs<FMT, D>& t, const uint8_t* __
     }
 }
 
-// E8M0 byte b -> the convert's FP32 scale operand.  The byte saturates at the
-// largest scale whose products stay finite in the matrix-core type (2^125 in
-// BF16, 2^13 in FP16), so that a key that was written as an infinity cannot
-// reach the queries that do not see it as 0 x Inf.
+// E8M0 byte b, times 2^e -> the convert's FP32 scale operand, of which it takes
+// the exponent field (0 stands for 2^-127).  The scale saturates at the largest
+// one whose products stay finite in the matrix-core type (2^125 in BF16, 2^13
+// in FP16), so that a key that was written as an infinity cannot reach the
+// queries that do not see it as 0 x Inf.
 template <int CT>
-__device__ __forceinline__ float e8m0_scale(uint32_t b) {
-    return __uint_as_float(min(b, CT == 0 ? 252u : 140u) << 23);
+__device__ __forceinline__ float e8m0_scale(uint32_t b, int e) {
+    return __uint_as_float((uint32_t)min(max((int)b + e, 0), CT == 0 ? 252 : 140) << 23);
 }
 
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
@@ -169,9 +177,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, f16x2 s) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * s);
 }
 
-// Byte B of the lane's key scales as the dequantization takes it.
+// Eight codes times byte B of the lane's key scales (E8M0: and 2^e).
 template <int FMT, int CT, int B, int N>
-__device__ __forceinline__ u32x4 key_frag(uint32_t w, const uint32_t (&ks)[N]) {
+__device__ __forceinline__ u32x4 key_frag(uint32_t w, const uint32_t (&ks)[N], int e) {
     u32x4 o;
     if constexpr (FMT == 0) {
         // two E4M3 scales -> FP16 (exact), one of them for both halves; code x scale is exact in FP16
@@ -182,7 +190,7 @@ __device__ __forceinline__ u32x4 key_frag(uint32_t w, const uint32_t (&ks)[N]) {
         o.z = mul_f16x2(codes_f16<2>(w, 1.0f), s);
         o.w = mul_f16x2(codes_f16<3>(w, 1.0f), s);
     } else {
-        const float s = e8m0_scale<CT>((ks[B / 4] >> (8 * (B % 4))) & 0xFFu);
+        const float s = e8m0_scale<CT>((ks[B / 4] >> (8 * (B % 4))) & 0xFFu, e);
         o.x = codes16<CT, 0>(w, s);
         o.y = codes16<CT, 1>(w, s);
         o.z = codes16<CT, 2>(w, s);
@@ -194,17 +202,17 @@ __device__ __forceinline__ u32x4 key_frag(uint32_t w, const uint32_t (&ks)[N]) {
 // Key fragment of tokens 16 U .. , chunk CK, product step S (elements
 // CH CK + KD j + 8 S .. + 7 of lane (r, j)).
 template <int FMT, int CT, int D, int U, int CK, int S>
-__device__ __forceinline__ u32x4 key_step(const TileRegs<FMT, D>& t) {
+__device__ __forceinline__ u32x4 key_step(const TileRegs<FMT, D>& t, int e) {
     using L = KvTile<FMT, D>;
     constexpr int byte = CK * 2 * L::KG + U * L::KG + (S * 8 / L::G) % L::KG;
-    if constexpr (D == 64) return key_frag<FMT, CT, byte>(t.k[0][2 * U + S], t.ks);
-    else return key_frag<FMT, CT, byte>(t.k[CK * 2 + U][S], t.ks);
+    if constexpr (D == 64) return key_frag<FMT, CT, byte>(t.k[0][2 * U + S], t.ks, e);
+    else return key_frag<FMT, CT, byte>(t.k[CK * 2 + U][S], t.ks, e);
 }
 
 // Two d-fragments (elements VD r + 2 Q, + 1 of chunk CK) of O^T's left operand:
 // lane (r, j) supplies tokens 4 j .. 4 j + 3 and 16 + 4 j .. .
 template <int FMT, int CT, int D, int CK, int Q>
-__device__ __forceinline__ void value_frags(const TileRegs<FMT, D>& t, u32x4& even, u32x4& odd) {
+__device__ __forceinline__ void value_frags(const TileRegs<FMT, D>& t, int e, u32x4& even, u32x4& odd) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         uint32_t a[4];  // elements 2 Q, 2 Q + 1 of the four tokens
@@ -228,7 +236,7 @@ __device__ __forceinline__ void value_frags(const TileRegs<FMT, D>& t, u32x4& ev
         } else {
             float s[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((sb >> (8 * i)) & 0xFFu);
+            for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((sb >> (8 * i)) & 0xFFu, e);
             if constexpr (D == 64) {
                 a[0] = codes16<CT, Q>(t.v[0][2 * u], s[0]);
                 a[1] = codes16<CT, Q + 2>(t.v[0][2 * u], s[1]);
@@ -591,7 +599,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
 #pragma unroll
                 for (int u = 0; u < 2; ++u) sc[mt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
             auto keys = [&](auto uc, auto cc, auto stc) {
-                const u32x4 kf = key_step<FMT, CT, D, decltype(uc)::value, decltype(cc)::value, decltype(stc)::value>(x);
+                const u32x4 kf = key_step<FMT, CT, D, decltype(uc)::value, decltype(cc)::value, decltype(stc)::value>(x, a.k_exp);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     sc[mt][decltype(uc)::value] =
@@ -653,7 +661,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
             auto values = [&](auto cc, auto qc) {
                 constexpr int ck = decltype(cc)::value, q = decltype(qc)::value;
                 u32x4 even, odd;
-                value_frags<FMT, CT, D, ck, q>(x, even, odd);
+                value_frags<FMT, CT, D, ck, q>(x, a.v_exp, even, odd);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     o[mt][ck * L::VD + 2 * q] = mfma<CT>(even, pf[mt], o[mt][ck * L::VD + 2 * q]);
@@ -910,17 +918,17 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f
 // Fragments of a part, chunk n: key steps, and the halves of the value
 // fragments (two dwords: tokens 0, 1 and 2, 3 of the quad).
 template <int FMT, int CT, int D, int S_, bool kHalf>
-__device__ __forceinline__ u32x4 part_key(uint32_t w, uint32_t ks) {
+__device__ __forceinline__ u32x4 part_key(uint32_t w, uint32_t ks, int e) {
     using L = KvTile<FMT, D>;
     const uint32_t a[1] = {ks};
-    return key_frag<FMT, CT, kHalf ? 0 : (S_ * 8 / L::G) % L::KG>(w, a);
+    return key_frag<FMT, CT, kHalf ? 0 : (S_ * 8 / L::G) % L::KG>(w, a, e);
 }
 template <int FMT, int CT, int D, int Q>
-__device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, u32x2& even, u32x2& odd) {
+__device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, int e, u32x2& even, u32x2& odd) {
     float s[4] = {1.0f, 1.0f, 1.0f, 1.0f};
     if constexpr (FMT == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((vs >> (8 * i)) & 0xFFu);
+        for (int i = 0; i < 4; ++i) s[i] = e8m0_scale<CT>((vs >> (8 * i)) & 0xFFu, e);
     }
     uint32_t a[4];  // elements 2 Q, 2 Q + 1 of the four tokens
     if constexpr (D == 64) {
@@ -1133,7 +1141,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         const int c = chunk0 + n;
         if constexpr (p < Part::SP) {
             const int x = quarter * Part::SP + p;  // octet (j, x) of token 16 half + r
-            const u32x4 f = part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n]);
+            const u32x4 f = part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n], a.k_exp);
             if constexpr (k32) out[c * 2 * S + (j >> 1) * S + x][32 * (j & 1) + 16 * half + r] = f;
             else out[half * (F / 2) + c * S + x][lane] = f;
         } else {
@@ -1145,7 +1153,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
             for (int e = 0; e < Part::VW; ++e)
                 codes[e] = Part::kHalf ? raw.v[n][e] >> (quarter * 8 * Part::VP) : raw.v[n][e];
             u32x2 even, odd;
-            part_value<FMT, CT, D, q>(codes, raw.vs[n] & keep, even, odd);
+            part_value<FMT, CT, D, q>(codes, raw.vs[n] & keep, a.v_exp, even, odd);
             const int block = c * (L::VD / 2) + quarter * Part::VP + q;
             if constexpr (k32) {
                 u32x2* vo = reinterpret_cast<u32x2*>(&out[F + block * 2 + half][32 * (j & 1) + 2 * r]) + (j >> 1);

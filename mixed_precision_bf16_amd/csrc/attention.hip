@@ -1,5 +1,7 @@
 // C entry of the attention over the FP4 key/value cache: checks, shape choice,
 // launch (include/fp4gemm.h, fp4_attention).
+#include <cmath>
+
 #include "attention.h"
 
 namespace fp4 {
@@ -124,8 +126,11 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.window = (int)std::min<int64_t>(x->window, a.max_keys);
     a.causal = x->causal;
     a.tpp_magic = ((uint64_t(1) << 36) + c.tiles_per_page - 1) / c.tiles_per_page;
-    a.scale = x->scale * c.k_alpha * kLog2e;
-    a.v_alpha = c.v_alpha;
+    const bool nv = cache->format == FP4_NVFP4;
+    a.k_exp = nv ? 0 : std::ilogb(c.k_alpha);
+    a.v_exp = nv ? 0 : std::ilogb(c.v_alpha);
+    a.scale = x->scale * std::ldexp(c.k_alpha, -a.k_exp) * kLog2e;
+    a.v_alpha = std::ldexp(c.v_alpha, -a.v_exp);
     a.inv_group = 1.0f / a.group;
     a.grid = p.grid;
     a.splits = p.splits;
@@ -136,7 +141,6 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.words = reinterpret_cast<unsigned long long*>(ws + p.word_off);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    const bool nv = cache->format == FP4_NVFP4;
     const auto launch = nv ? (x->act_type == 0 ? launch_attention_nv_bf16 : launch_attention_nv_f16)
                            : (x->act_type == 0 ? launch_attention_mx_bf16 : launch_attention_mx_f16);
     if (!launch((int)D, p.MT, p.tiled, a, c, s)) return FP4_ERR_SHAPE;

@@ -597,3 +597,98 @@ def test_kernels_agree():
     a, b = p.run(max_q=1), p.run()
     assert torch.all((a[0].float() - b[0].float()).abs() <= 2.0 ** -9 * b[0].float().abs() + 2.0 ** -10)
     assert torch.all((a[1] - b[1]).abs() <= 2.0 ** -18 * (1 + b[1].abs()))
+
+
+PAIRS = [(0, BF16), (0, FP16), (1, BF16), (1, FP16)]
+
+
+def _rows_of_all_sizes(fmt, dtype, D, alpha, seed):
+    """One key a sequence, 2 heads, the size of its rows 2^-13 .. 2^14: (cache, table, slots)."""
+    B, H = 28, 2
+    gen = torch.Generator("cuda").manual_seed(seed)
+    kv = torch.rand((2, B, H, D), device="cuda", generator=gen) * 2 - 1
+    kv *= 2.0 ** torch.arange(-13, 15, device="cuda")[:, None, None]
+    cache = F.new_kv_cache(B, 32, H, D, fmt, alpha, alpha)
+    cache.data.fill_(0xFF)
+    slots = torch.randperm(B, device="cuda", generator=gen) * 32
+    F.kv_append(cache, kv[0].to(dtype), kv[1].to(dtype), slots)
+    return cache, (slots // 32).to(torch.int32)[:, None].contiguous(), slots
+
+
+ALPHAS = [1.0, 0.37, 1e-3, 2.0 ** -20, 3000.0, 4096.0]
+
+
+@pytest.mark.parametrize("alpha", ALPHAS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt,dtype", PAIRS)
+@pytest.mark.parametrize("n", [1, 96])
+def test_values_come_out_as_they_are_read_back(fmt, dtype, D, alpha, n):
+    """One key and queries of zero: its weight is exactly 1, and the output is
+    its value row, the same bits as the read-back gives, whatever alpha and the
+    rows' size are (both scale the exact code x scale by alpha in FP32, once)."""
+    cache, table, slots = _rows_of_all_sizes(fmt, dtype, D, alpha, D)
+    v = F.kv_read(cache, slots, dtype=dtype)[1]
+    B = len(slots)
+    q = torch.zeros((B * n, 2 * 8, D), dtype=dtype, device="cuda")
+    out = F.attention(q, cache, table, torch.ones(B, dtype=torch.int32, device="cuda"), causal=False)
+    want = v.repeat_interleave(8, 1).repeat_interleave(n, 0)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("alpha", ALPHAS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt,dtype", PAIRS)
+@pytest.mark.parametrize("n", [1, 96])
+def test_keys_weigh_as_they_are_read_back(fmt, dtype, D, alpha, n):
+    """One key and queries with a single 1: the log-sum-exp is scale times one
+    element x of the key row, exact but for these FP32 roundings (half a step,
+    2^-24 relative, each): scale alpha, log2 e itself, times it, the score, 8 - m
+    (its share of m), m plus the logarithm, ln 2 itself, times it, 8 in all; and
+    next to 0 those that stay, in units of 2^-24: 8 - m in [8, 16) 8 ln 2, the
+    exponential 2, the logarithm of a sum next to 1 2, at most 12."""
+    cache, table, slots = _rows_of_all_sizes(fmt, dtype, D, alpha, D + 1)
+    B = len(slots)
+    q = torch.zeros((B, n, 2 * 8, D), dtype=dtype, device="cuda")
+    at = torch.arange(16, device="cuda") * 37 % D
+    q[:, :, torch.arange(16, device="cuda"), at] = 1.0
+    _, lse = F.attention(q.reshape(B * n, 16, D), cache, table, torch.ones(B, dtype=torch.int32, device="cuda"),
+                         causal=False, return_lse=True)
+    k = oracle.kv_read_reference(cache.data.cpu().numpy(), slots.cpu().numpy(), 2, D, 32, fmt, alpha, alpha)[0]
+    k = k.repeat(8, 1)[:, np.arange(16), at.cpu().numpy()]
+    want = np.repeat(k * float(np.float32(D ** -0.5)), n, 0)
+    off = np.abs(lse.double().cpu().numpy() - want)
+    assert np.all(off <= 8 * 2.0 ** -24 * np.abs(want) + 12 * 2.0 ** -24)
+
+
+def _of_size(lens, news, k_size, v_size, ka, va, fmt, dtype, D=128, H=2, group=4, seed=0):
+    """A Problem whose rows have the given sizes, whatever the alphas are."""
+    p = Problem(lens, news, fmt, dtype, D, H, group, 64, seed, strength=1.5 / k_size)
+    p.ka, p.va = ka, va
+    slots = np.concatenate([p.slots(b, np.arange(x)) for b, x in enumerate(lens)])
+    x = np.random.Generator(np.random.PCG64(seed + 1)).standard_normal((2, len(slots), H, D)).astype(np.float32)
+    x[0] *= k_size
+    x[1] *= v_size
+    p.data[:] = 0xFF
+    oracle.kv_write_reference(p.data, slots, x[0], x[1], 64, fmt, ka, va)
+    p.k[slots], p.v[slots] = oracle.kv_read_reference(p.data, slots, H, D, 64, fmt, ka, va)
+    return p
+
+
+@pytest.mark.parametrize("ka,va,k_size,v_size", [(1e-3, 1e-3, 100.0, 100.0), (1024.0, 1024.0, 0.01, 1e-4),
+                                                 (4096.0, 2.0 ** 20, 1.0, 0.03), (2.0 ** -20, 2.0 ** -30, 1.0, 50.0)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("news,lens,group", [([1, 1], [70, 100], 4), ([70, 64], [100, 70], 8)])
+def test_alphas_far_from_the_rows_size(ka, va, k_size, v_size, dtype, news, lens, group):
+    p = _of_size(lens, news, k_size, v_size, ka, va, 1, dtype, group=group, seed=41)
+    got = p.run()
+    torch.cuda.synchronize()
+    _check_sampled(p, got)
+
+
+@pytest.mark.parametrize("fmt,dtype,ka,va", [(0, BF16, 0.02, 0.7), (0, FP16, 1.3, 0.01), (1, BF16, 0.3, 1.9),
+                                             (1, FP16, 2.0, 0.5), (1, FP16, 0.003, 700.0)])
+def test_alphas_of_prompts(fmt, dtype, ka, va):
+    p = Problem([90, 120], [80, 64], fmt, dtype, 128, 2, 8, ka=ka, va=va, seed=42)
+    got = p.run()
+    torch.cuda.synchronize()
+    _check_sampled(p, got)
