@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 import struct
@@ -421,9 +422,14 @@ class KVCache:
     """A paged FP4 key/value cache of one attention layer: `data` (a contiguous
     uint8 CUDA tensor of kv_cache_size bytes, in the layout that
     include/fp4gemm.h documents) and its shape.  k_alpha / v_alpha are the
-    per-tensor scales of keys and values."""
+    per-tensor scales of keys and values.  All are fixed once the object is
+    made: the library's descriptor holds the data's address and the values."""
 
-    __slots__ = ("data", "pages", "page_size", "kv_heads", "head_dim", "fmt", "k_alpha", "v_alpha", "_desc", "_ref")
+    __slots__ = ("_data", "_pages", "_page_size", "_kv_heads", "_head_dim", "_fmt", "_k_alpha", "_v_alpha", "_desc",
+                 "_ref")
+
+    data, pages, page_size, kv_heads, head_dim, fmt, k_alpha, v_alpha = (
+        property(operator.attrgetter(name)) for name in __slots__[:8])
 
     def __init__(self, data, pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int, k_alpha: float = 1.0,
                  v_alpha: float = 1.0):
@@ -432,8 +438,8 @@ class KVCache:
             raise ValueError("data must be a contiguous uint8 CUDA tensor")
         if data.numel() != kv_cache_size(pages, page_size, kv_heads, head_dim, fmt):
             raise ValueError("data does not have the cache's size")
-        self.data, self.pages, self.page_size, self.kv_heads = data, pages, page_size, kv_heads
-        self.head_dim, self.fmt, self.k_alpha, self.v_alpha = head_dim, fmt, k_alpha, v_alpha
+        self._data, self._pages, self._page_size, self._kv_heads = data, pages, page_size, kv_heads
+        self._head_dim, self._fmt, self._k_alpha, self._v_alpha = head_dim, fmt, k_alpha, v_alpha
         self._desc = _KVCacheDesc(data.data_ptr(), pages, page_size, kv_heads, head_dim, fmt, k_alpha, v_alpha)
         self._ref = ctypes.byref(self._desc)
 
@@ -529,12 +535,12 @@ def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
     outside the cache is skipped, no slot twice)."""
     import torch
     act = _act_type(k.dtype, "k")
-    dev = cache.data.device
+    dev = cache._data.device
     if v.dtype != k.dtype:
         raise ValueError("k and v must have the same type")
     n = k.shape[0]
-    kt, kh = _rows(k, "k", n, cache.kv_heads, cache.head_dim, dev)
-    vt, vh = _rows(v, "v", n, cache.kv_heads, cache.head_dim, dev)
+    kt, kh = _rows(k, "k", n, cache._kv_heads, cache._head_dim, dev)
+    vt, vh = _rows(v, "v", n, cache._kv_heads, cache._head_dim, dev)
     sp = _vector(slots, "slots", n, torch.int64, dev)
     with _on_stream(dev, stream) as s:
         st = lib().fp4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), sp, n, kt, kh, vt, vh, act, s)
@@ -547,7 +553,7 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
     (k, v), each [tokens][kv_heads][head_dim] of `dtype` (bfloat16 by default);
     zeros for a slot outside the cache.  k_out / v_out are filled if given."""
     import torch
-    dev = cache.data.device
+    dev = cache._data.device
     given = [t.dtype for t in (k_out, v_out) if t is not None]
     if dtype is None:
         dtype = given[0] if given else torch.bfloat16
@@ -557,9 +563,9 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
     n = slots.shape[0] if slots.dim() == 1 else -1
     sp = _vector(slots, "slots", n, torch.int64, dev)
     with _on_stream(dev, stream) as s:
-        shape = (n, cache.kv_heads, cache.head_dim)
-        kt = vt = cache.kv_heads * cache.head_dim  # strides of what is allocated here
-        kh = vh = cache.head_dim
+        shape = (n, cache._kv_heads, cache._head_dim)
+        kt = vt = cache._kv_heads * cache._head_dim  # strides of what is allocated here
+        kh = vh = cache._head_dim
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=dev)
         else:
@@ -578,12 +584,12 @@ def _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q):
     """Checks of the tensors that every call has; (device, activation type,
     pointers, sizes, query strides) as fp4_attention_args takes them."""
     import torch
-    dev = cache.data.device
+    dev = cache._data.device
     if q.dim() != 3:
         raise ValueError("q must be a tensor [q_rows][q_heads][head_dim]")
     act = _act_type(q.dtype, "q")
     rows, heads, _ = q.shape
-    qt, qh = _rows(q, "q", rows, heads, cache.head_dim, dev)
+    qt, qh = _rows(q, "q", rows, heads, cache._head_dim, dev)
     if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
             or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
         raise ValueError(f"page_table must be an int32 matrix [batch][columns] on {dev} with contiguous rows")
@@ -622,7 +628,7 @@ def _attention_workspace(kv_heads, page_size, head_dim, fmt, batch, rows, heads,
 def attention_workspace_size(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=None) -> int:
     """Bytes of workspace that attention() needs for these shapes."""
     _, _, _, sizes, _ = _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q)
-    return _attention_workspace(cache.kv_heads, cache.page_size, cache.head_dim, cache.fmt, *sizes[:5],
+    return _attention_workspace(cache._kv_heads, cache._page_size, cache._head_dim, cache._fmt, *sizes[:5],
                                 q_offsets is not None)
 
 
@@ -660,7 +666,7 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
         elif return_lse:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            need = _attention_workspace(cache.kv_heads, cache.page_size, dim, cache.fmt, *sizes[:5],
+            need = _attention_workspace(cache._kv_heads, cache._page_size, dim, cache._fmt, *sizes[:5],
                                         q_offsets is not None)
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         elif not workspace.is_contiguous() or workspace.device != dev:

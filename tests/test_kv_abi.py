@@ -211,3 +211,29 @@ def test_binding_refuses_host_tensors():
         F.KVCache(c, 1, 32, 1, 64, 0)
     with pytest.raises(F.Fp4Error):
         F.kv_cache_size(1, 31, 1, 64, 0)
+
+
+class _DeviceTensor:
+    """What KVCache asks of its tensor, without a GPU."""
+    dtype, is_cuda = torch.uint8, True
+
+    def __init__(self, n, address=4096):
+        self.numel, self.data_ptr, self.is_contiguous = (lambda: n), (lambda: address), (lambda: True)
+
+
+def test_cache_fields_are_fixed():
+    """The descriptor that the calls take holds the data's address, the shape
+    and the scales: none of them can be set past it."""
+    data = _DeviceTensor(F.kv_cache_size(3, 32, 2, 64, 1))
+    c = F.KVCache(data, 3, 32, 2, 64, 1, 0.5, 2.0)
+    want = dict(data=data, pages=3, page_size=32, kv_heads=2, head_dim=64, fmt=1, k_alpha=0.5, v_alpha=2.0)
+    assert {n: getattr(c, n) for n in want} == want
+    for name in want:
+        with pytest.raises(AttributeError):
+            setattr(c, name, _DeviceTensor(data.numel(), 8192) if name == "data" else 64)
+        with pytest.raises(AttributeError):
+            delattr(c, name)
+    assert {n: getattr(c, n) for n in want} == want
+    d = c._desc
+    assert (d.data, d.pages, d.page_size, d.kv_heads, d.head_dim, d.format, d.k_alpha, d.v_alpha) == \
+        (4096, 3, 32, 2, 64, 1, 0.5, 2.0)
