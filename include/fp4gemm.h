@@ -371,8 +371,8 @@ typedef struct fp4_attention_args {
     const int32_t* page_table; /* device [batch][page_columns]; an entry outside [0, pages) holds no keys */
     const int32_t* seq_lens;   /* device [batch]; clamped to [0, page_columns * page_size] */
     const int32_t* q_offsets;  /* device [batch + 1]: query rows of sequence b are q_offsets[b] .. q_offsets[b + 1] - 1,
-                                  clamped to [0, q_rows]; NULL: q_rows / batch rows each.  Where they
-                                  decrease, rows are left unwritten */
+                                  clamped to [0, q_rows]; NULL: q_rows / batch rows each.  If they
+                                  decrease anywhere, nothing is written */
     const float* sinks;        /* device [q_heads] or NULL: exp(sink) is added to the softmax sum */
     int64_t batch, q_rows, q_heads;
     int64_t max_q;             /* about the most query tokens of a sequence (0: unknown).  Only chooses

@@ -1004,10 +1004,11 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     } else {  // sequences in order, their last blocks first
         int before = 0;
         bool there = false;
-        for (int base = 0; base < a.batch && !there; base += 64 * NW) {
+        for (int base = 0; base < a.batch && (!there || a.q_offsets); base += 64 * NW) {
             bool bad_offsets = false;
             const Seq x = sequence_of<R>(a, base + threadIdx.x, bad_offsets);
-            if (__syncthreads_or(bad_offsets)) return;  // the same for all shares of a block
+            if (__syncthreads_or(bad_offsets)) return;  // nothing is written: every block looks at all offsets
+            if (there) continue;
             int p = wave_scan(x.blocks);
             __syncthreads();
             if (lane == 63) lds_scan[wave] = p;

@@ -692,3 +692,38 @@ def test_alphas_of_prompts(fmt, dtype, ka, va):
     got = p.run()
     torch.cuda.synchronize()
     _check_sampled(p, got)
+
+
+@pytest.mark.parametrize("at", [66, 650])
+def test_offsets_that_decrease_late_write_nothing(at):
+    """The same in the tiled kernel where the decrease lies past the sequences
+    that its search for a block looks at in one go."""
+    B = 700
+    p = Problem([40] * B, [1] * B, 0, BF16, 64, 1, 8, 64, seed=45)
+    off = p.offsets.copy()
+    off[at] = 10
+    q = p.q.cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((B, 8), 7.0, device="cuda")
+    F.attention(q, p.cache(), torch.from_numpy(p.table).cuda(), torch.tensor(p.lens, dtype=torch.int32, device="cuda"),
+                q_offsets=torch.from_numpy(off).cuda(), max_q=64, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7) and torch.all(lse == 7)
+
+
+def test_prompts_of_many_sequences_in_shares():
+    """More sequences than a wave's lanes, and few enough blocks that their
+    keys are cut into shares."""
+    news = [1] * 66
+    news[5], news[65], news[40] = 64, 60, 0
+    lens = [70] * 66
+    lens[5], lens[65], lens[0] = 2000, 1300, 900
+    p = Problem(lens, news, 0, BF16, 128, 1, 8, 64, seed=48)
+    got = p.run(max_q=64)
+    torch.cuda.synchronize()
+    _check_sampled(p, got)
+    size = F.attention_workspace_size(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+                                      torch.tensor(p.lens, dtype=torch.int32, device="cuda"),
+                                      q_offsets=torch.from_numpy(p.offsets).cuda(), max_q=64)
+    assert size > 0                                                  # partial sums: shares are used
+    again = p.run(max_q=64, workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
