@@ -33,7 +33,10 @@ namespace fp4 {
 
 constexpr float kBias = 8.0f, kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;  // running maximum before the first visible key
+constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first visible key: no score is lower
+// Scores from here on (base 2) are taken relative to the running maximum before
+// the exponential's own multiply-add, see far_scores.
+constexpr float kFar = 0x1p20f;
 constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // Waves per SIMD that the streaming kernel's registers allow; the GPU then holds
 // 256 times as many of its workgroups (a workgroup has a wave on each SIMD).
@@ -406,6 +409,21 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Probabilities are exp2(s fac + (kBias - m)) with one multiply-add.  The running
+// maximum m is the rounded product of the highest s: what the rounding took, and
+// that of kBias - m, up to 2^-24 |m|, multiplies all probabilities of the row by
+// one power of two, which the sum divides out.  Past 2^24 that factor would leave
+// FP16's range, and then FP32's.  So where a row of the wave has |m| >= kFar, a
+// branch that is not taken otherwise, scores become round(s fac) - m (0 at the
+// maximum) first, and fac 1 and m 0 follow them.  True if some row is there; called
+// when m has changed.
+__device__ __forceinline__ bool far_scores(float m) { return __any(fabsf(m) >= kFar && m != kNoMax); }
+__device__ __forceinline__ float near_score(float s, float fac, float m) {
+#pragma clang fp contract(off)
+    const float x = s * fac;
+    return x - m;
+}
+
 // Final value factor and log-sum-exp of a row from its running maximum m,
 // biased sum l and sink.
 __device__ __forceinline__ float finish_row(float m, float l, bool has_sink, float sink, float& lse) {
@@ -563,6 +581,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
         float fac[MT], m[MT], l[MT];
         RowRange range[MT];
         f32x4 o[MT][OT];
+        int far_rows = 0;                 // bit mt: far_scores
         int lo_all = 0, hi_all = it.len;  // keys that every valid row sees
         {
             const int i1 = i0 + __builtin_amdgcn_readfirstlane(token_of(rows - 1));
@@ -643,15 +662,22 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
                     const float mn = fmaxf(m[mt], top);
                     const float down = exp2_(m[mt] - mn);
                     m[mt] = mn;
+                    if (far_scores(mn)) far_rows |= 1 << mt;
                     l[mt] *= down;
 #pragma unroll
                     for (int y = 0; y < OT; ++y) o[mt][y] *= down;
                 }
-                const float off = kBias - m[mt];
+                float f = fac[mt], off = kBias - m[mt];
+                if (far_rows >> mt & 1) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = near_score(s[e], f, m[mt]);
+                    f = 1.0f;
+                    off = kBias;
+                }
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    p[e] = exp2_(fmaf(s[e], fac[mt], off));
+                    p[e] = exp2_(fmaf(s[e], f, off));
                     l[mt] += p[e];
                 }
 #pragma unroll
@@ -1172,6 +1198,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     const float fac = QueryRow<FMT, ACT, D>::convert(qf, a.scale);
     const RowRange range = range_of(my);
     float m = kNoMax, l = 0.0f;
+    bool far = false;  // far_scores
     Acc o[OB];
 #pragma unroll
     for (int x = 0; x < OB; ++x) o[x] = Acc(0.0f);
@@ -1240,18 +1267,25 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
             const float mn = fmaxf(m, top);
             const float down = exp2_(m - mn);
             m = mn;
+            far = far_scores(mn);
             l *= down;
 #pragma unroll
             for (int y = 0; y < OB; ++y) o[y] *= down;
         }
         // Probabilities of a lane's first eight keys, then the products of eight
         // with the next ones' probabilities in between.
-        const float off = kBias - m;
+        float f = fac, off = kBias - m;
+        if (far) {
+#pragma unroll
+            for (int e = 0; e < NS * TT; ++e) sc[e / A][e % A] = near_score(sc[e / A][e % A], f, m);
+            f = 1.0f;
+            off = kBias;
+        }
         constexpr int kEights = NS * TT / 8;
         u32x4 pf[kEights];
         auto weigh = [&](int u, int pair) {  // two of eight keys
             const int e = 8 * u + 2 * pair;
-            const float p0 = exp2_(fmaf(sc[e / A][e % A], fac, off)), p1 = exp2_(fmaf(sc[e / A][e % A + 1], fac, off));
+            const float p0 = exp2_(fmaf(sc[e / A][e % A], f, off)), p1 = exp2_(fmaf(sc[e / A][e % A + 1], f, off));
             l += p0 + p1;
             pf[u][pair] = pack_out<CT>(p0, p1);
         };

@@ -727,3 +727,30 @@ def test_prompts_of_many_sequences_in_shares():
     assert size > 0                                                  # partial sums: shares are used
     again = p.run(max_q=64, workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda"))
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("size", [-1e35, 1e35, -3e30, 1e12, -1e9, 1e8])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n", [1, 64])
+def test_scores_far_from_zero(fmt, n, size):
+    """Scores of any size, of BF16 queries: of keys whose scores are further
+    apart than 2^20 the highest takes all, rounding included (v's own in the
+    output: half a step), and the log-sum-exp is its score (eight roundings in FP32)."""
+    p = Problem([40, 3], [n, n], fmt, BF16, 128, 1, 8, 64, seed=43)
+    q = torch.zeros((2 * n, 8, 128), dtype=BF16)
+    q[:, :, 5] = size
+    for b in range(2):
+        at = p.slots(b, np.arange(p.lens[b]))
+        k = np.ones((p.lens[b], 1, 128), np.float32)
+        k[:, :, 5] = 2.0 if size < 0 else 1.0
+        k[1, :, 5] = 1.0 if size < 0 else 2.0
+        oracle.kv_write_reference(p.data, at, k, p.v[at].astype(np.float32), 64, fmt)
+        p.k[at], p.v[at] = oracle.kv_read_reference(p.data, at, 1, 128, 64, fmt)
+    p.q = q
+    out, lse = p.run(causal=False)
+    for b in range(2):
+        at = p.slots(b, np.array([1]))
+        v = torch.from_numpy(p.v[at, 0]).cuda().double()[None]
+        s = float(p.k[at, 0, 5][0]) * float(q[0, 0, 5].double()) * float(np.float32(p.scale))
+        assert torch.all((out[b * n:b * n + n].double() - v).abs() <= 2.0 ** -8 * v.abs())
+        assert torch.all((lse[b * n:b * n + n].double() - s).abs() <= 2.0 ** -21 * abs(s))
