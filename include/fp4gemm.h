@@ -405,8 +405,8 @@ int fp4_attention_workspace_size(const fp4_kv_cache* cache, const fp4_attention_
  *   BF16 activations: blocks written from infinities act as if their scale
  *   were at most 2^125, blocks below 2^-124 as if it were at least 2^-127, and
  *   values above 2^112 / keys can overflow the FP32 sums.
- * A query row that sees no key gives out 0 and lse -Inf (or the
- * sink's logarithm, out 0).  Rows of q that belong to no sequence leave out
+ * A query row that sees no key gives out 0 and lse -Inf (with sinks: its
+ * head's sink).  Rows of q that belong to no sequence leave out
  * and lse as they were.  All sizes that depend on the data (seq_lens,
  * q_offsets, page_table) stay on the device: a call captured in a HIP graph
  * follows their contents on replay.  Deterministic.

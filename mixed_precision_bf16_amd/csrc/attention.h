@@ -432,8 +432,8 @@ __device__ __forceinline__ float finish_row(float m, float l, bool has_sink, flo
     const float f = exp2_(m - top - kBias);
     float sum = l * f;
     if (has_sink) sum += exp2_(sink * kLog2e - top);
-    if (sum == 0.0f) {
-        lse = -__builtin_inff();
+    if (sum == 0.0f) {  // no key is seen, and the sink, if any, is below the range of base 2
+        lse = has_sink ? sink : -__builtin_inff();
         return 0.0f;
     }
     lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;

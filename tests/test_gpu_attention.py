@@ -754,3 +754,21 @@ def test_scores_far_from_zero(fmt, n, size):
         s = float(p.k[at, 0, 5][0]) * float(q[0, 0, 5].double()) * float(np.float32(p.scale))
         assert torch.all((out[b * n:b * n + n].double() - v).abs() <= 2.0 ** -8 * v.abs())
         assert torch.all((lse[b * n:b * n + n].double() - s).abs() <= 2.0 ** -21 * abs(s))
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_sinks_of_the_lowest_values(max_q):
+    """Sinks far below every score add nothing; where no key is seen the
+    log-sum-exp is the sink itself, also at the type's lowest value."""
+    p = Problem([0, 2, 50], [1, 4, 2], 0, BF16, 128, 1, 4, 64, seed=44)
+    low = torch.finfo(torch.float32).min
+    sinks = torch.tensor([low, -2e38, -1e31, -np.inf], device="cuda")
+    plain = p.run(max_q=max_q)
+    out, lse = p.run(max_q=max_q, sinks=sinks)
+    empty = torch.isneginf(plain[1])
+    assert torch.equal(out, plain[0]) and torch.equal(lse[~empty], plain[1][~empty])
+    want = sinks.expand(lse.shape)[empty].double()
+    got = lse[empty].double()
+    assert torch.equal(torch.isinf(got), torch.isinf(want))
+    near = ~torch.isinf(want)
+    assert torch.all((got[near] - want[near]).abs() <= 2.0 ** -22 * want[near].abs())
