@@ -611,7 +611,7 @@ def _attention_shape(q, cache, page_table, seq_lens, q_offsets, max_q):
 def _pack_attention(*fields) -> bytes:
     try:
         return _PACK_ATTENTION.pack(*fields)
-    except (struct.error, OverflowError) as e:  # the latter for a scale that no float holds
+    except struct.error as e:
         raise ValueError(f"attention: {e}") from None
 
 

@@ -237,10 +237,3 @@ def test_cache_fields_are_fixed():
     d = c._desc
     assert (d.data, d.pages, d.page_size, d.kv_heads, d.head_dim, d.format, d.k_alpha, d.v_alpha) == \
         (4096, 3, 32, 2, 64, 1, 0.5, 2.0)
-
-
-@pytest.mark.parametrize("scale", [1e39, -4e38])
-def test_a_scale_past_float_is_a_value_error(scale):
-    values = list(range(1, 8)) + list(range(11, 22)) + [1, 0, scale, 31, 32]
-    with pytest.raises(ValueError):
-        F._pack_attention(*values)
