@@ -377,7 +377,8 @@ typedef struct fp4_attention_args {
     int64_t batch, q_rows, q_heads;
     int64_t max_q;             /* about the most query tokens of a sequence (0: unknown).  Only chooses
                                   the kernel: results do not depend on it beyond rounding */
-    int64_t page_columns, page_stride; /* columns of the page table and elements between its rows */
+    int64_t page_columns, page_stride; /* columns of the page table and elements between its rows (0: every
+                                          sequence has the same row) */
     int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements, multiples of 8 */
     int64_t window;            /* > 0: a query sees only the last `window` positions up to its own (causal only) */
     int32_t causal;            /* 1: keys at positions up to the query's own; 0: all keys of the sequence */

@@ -92,7 +92,7 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     if (!attn_rows_ok(x->q, x->q_token_stride, x->q_head_stride) ||
         !attn_rows_ok(x->out, x->out_token_stride, x->out_head_stride) ||
         !rows_apart(x->q_rows, x->q_heads, D, x->out_token_stride, x->out_head_stride) ||
-        x->page_stride < x->page_columns || x->page_stride > (int64_t(1) << 40) ||
+        (x->page_stride < x->page_columns && x->page_stride != 0) || x->page_stride > (int64_t(1) << 40) ||
         (!x->q_offsets && x->q_rows % x->batch) ||
         ((reinterpret_cast<uintptr_t>(x->lse) | reinterpret_cast<uintptr_t>(x->page_table) |
           reinterpret_cast<uintptr_t>(x->seq_lens) | reinterpret_cast<uintptr_t>(x->q_offsets) |

@@ -638,9 +638,10 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     """fp4_attention: softmax(scale * q . K^T) . V over the cache.
 
     q: bfloat16 or float16 CUDA [q_rows][q_heads][head_dim]; page_table: int32
-    [batch][columns]; seq_lens: int32 [batch], keys of each sequence, the query
-    tokens' own among them.  The query rows of sequence b are
-    q_offsets[b] .. q_offsets[b + 1] - 1 (int32 [batch + 1]) or, without
+    [batch][columns], its rows at least `columns` apart, or one row for all
+    (expand); seq_lens: int32 [batch], keys of each sequence, the query tokens'
+    own among them.  The query rows of sequence b are q_offsets[b] ..
+    q_offsets[b + 1] - 1 (int32 [batch + 1], never decreasing) or, without
     q_offsets, q_rows / batch each; they are its last positions.  max_q: about
     the most query tokens of a sequence (default: q_rows), for the choice of
     kernel.  window > 0: only the last `window` positions up to the query's

@@ -772,3 +772,13 @@ def test_sinks_of_the_lowest_values(max_q):
     assert torch.equal(torch.isinf(got), torch.isinf(want))
     near = ~torch.isinf(want)
     assert torch.all((got[near] - want[near]).abs() <= 2.0 ** -22 * want[near].abs())
+
+
+def test_a_page_table_that_sequences_share():
+    p = Problem([100], [1], 0, BF16, seed=46)
+    q = torch.cat([p.q] * 3).cuda()
+    table = torch.from_numpy(p.table).cuda()
+    n = torch.tensor([100, 64, 7], dtype=torch.int32, device="cuda")
+    want = F.attention(q, p.cache(), table.repeat(3, 1), n, return_lse=True)
+    got = F.attention(q, p.cache(), table.expand(3, -1), n, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -237,3 +237,11 @@ def test_cache_fields_are_fixed():
     d = c._desc
     assert (d.data, d.pages, d.page_size, d.kv_heads, d.head_dim, d.format, d.k_alpha, d.v_alpha) == \
         (4096, 3, 32, 2, 64, 1, 0.5, 2.0)
+
+
+def test_a_page_table_row_for_all_sequences_passes_the_checks():
+    # the workspace is checked after the strides, and before any HIP call
+    call = lambda **over: F.lib().fp4_attention(ctypes.byref(_cache()), ctypes.byref(_args(workspace=None, **over)),  # noqa: E731
+                                                None)
+    assert call() == 5 and call(page_stride=0) == 5 and call(page_stride=7) == 5
+    assert call(page_stride=-1) == 2 and call(page_stride=1) == 2
