@@ -60,8 +60,9 @@ struct AttnArgs {
     const int32_t* q_offsets;  // null: every sequence has q_each query tokens
     const float* sinks;
     int64_t q_ts, q_hs, o_ts, o_hs, table_stride;
-    int batch, q_rows, q_each, q_heads, group, table_cols;
-    int max_keys;              // table_cols * page_size
+    int batch, q_rows, q_each, q_heads, group;
+    int splits;                // tiled kernel: most shares of an item
+    int max_keys;              // columns of the page table * page_size
     int window, causal;
     uint64_t tpp_magic;        // ceil(2^36 / tiles_per_page): the page of tile t < 2^26 is t * magic >> 36
     int k_exp, v_exp;          // MXFP4: exponents of k_alpha and v_alpha, which the block scales take along; else 0
@@ -69,7 +70,6 @@ struct AttnArgs {
     float v_alpha;             // v_alpha / 2^v_exp
     float inv_group;           // 1 / group
     int grid;                  // workgroups; in the streaming kernel as many as the GPU holds
-    int splits;                // tiled kernel: most shares of an item
     unsigned long long tag;    // of the arrival words
     float* ws_o;               // [2 * grid][rows][D]; tiled kernel: [grid][D / 4][rows][4] and so on
     float* ws_ml;              // [2 * grid][rows][2]
@@ -915,16 +915,15 @@ __device__ __forceinline__ void unrolled(Fn&& f) {
 //   probabilities lane 32 h + . holds after S^T.
 //
 // A tile's dequantization is dealt to WPT waves by token half u (tokens 16 u ..
-// 16 u + 15) and, with four waves, by chunk, or where there is only one by the
-// halves of its octets and value elements.
+// 16 u + 15) and, with four waves (head size 256), by chunk.
 template <int FMT, int D, int WPT>
 struct TilePart {
     using L = KvTile<FMT, D>;
-    static constexpr bool kHalf = WPT == 4 && L::C == 1;       // half the elements
-    static constexpr int N = WPT == 4 ? 1 : L::C;              // chunks
-    static constexpr int SP = kHalf ? L::KD / 16 : L::KD / 8;  // octets of a lane and chunk
-    static constexpr int VP = kHalf ? L::VD / 4 : L::VD / 2;   // pairs of value elements of a chunk
-    static constexpr int VW = D == 64 ? 2 : 4;                 // dwords of a lane's value codes
+    static_assert(WPT == 2 || (WPT == 4 && L::C == 2), "two waves a tile, or two a chunk of it");
+    static constexpr int N = 2 * L::C / WPT;    // chunks
+    static constexpr int SP = L::KD / 8;        // octets of a lane and chunk
+    static constexpr int VP = L::VD / 2;        // pairs of value elements of a chunk
+    static constexpr int VW = D == 64 ? 2 : 4;  // dwords of a lane's value codes
     uint32_t k[N][SP], v[N][VW];
     uint32_t ks[N];  // the key scales of each chunk in the low bytes
     uint32_t vs[N];  // the scales of the four value tokens
@@ -943,11 +942,11 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f
 
 // Fragments of a part, chunk n: key steps, and the halves of the value
 // fragments (two dwords: tokens 0, 1 and 2, 3 of the quad).
-template <int FMT, int CT, int D, int S_, bool kHalf>
+template <int FMT, int CT, int D, int S_>
 __device__ __forceinline__ u32x4 part_key(uint32_t w, uint32_t ks, int e) {
     using L = KvTile<FMT, D>;
     const uint32_t a[1] = {ks};
-    return key_frag<FMT, CT, kHalf ? 0 : (S_ * 8 / L::G) % L::KG>(w, a, e);
+    return key_frag<FMT, CT, (S_ * 8 / L::G) % L::KG>(w, a, e);
 }
 template <int FMT, int CT, int D, int Q>
 __device__ __forceinline__ void part_value(const uint32_t* v, uint32_t vs, int e, u32x2& even, u32x2& odd) {
@@ -987,7 +986,6 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     constexpr int OB = k32 ? D / 32 : D / 16;  // blocks of the output's elements
     constexpr int NS = k32 ? 16 : 8;        // scores of a lane and tile
     using Acc = typename std::conditional<k32, f32x16, f32x4>::type;
-    static_assert(WPT == 2 || WPT == 4, "a tile is dequantized by two or four waves");
     constexpr int kTileFrags = 2 * F;  // 1 KiB fragments of a tile
     __shared__ u32x4 lds[2][TT][kTileFrags][64];
     __shared__ int lds_scan[NW], lds_found[5];
@@ -1104,8 +1102,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
     int window_pages = steps > 0 ? load_pages(t0 + s0 * TT) : 0, window_first = t0 + s0 * TT;
     using Part = TilePart<FMT, D, WPT>;
     Part raw;
-    // this wave's token half, first chunk and half of the elements
-    const int half = sub & 1, chunk0 = Part::kHalf ? 0 : sub >> 1, quarter = Part::kHalf ? sub >> 1 : 0;
+    const int half = sub & 1, chunk0 = sub >> 1;  // this wave's token half and first chunk
     int raw_bad = 0, raw_left = 0;  // tiles of the step without keys; keys that this wave's tile holds from its start
     auto fetch = [&](int step) {
         const int ts = t0 + (s0 + step) * TT;
@@ -1129,10 +1126,8 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
 #pragma unroll
         for (int n = 0; n < Part::N; ++n) {
             const int c = chunk0 + n;
-            const uint8_t* kc = tile + (D == 64 ? half * 8 : (c * 2 + half) * 1024) + lane * 16 + quarter * 4 * Part::SP;
-            if constexpr (Part::SP == 1) {
-                raw.k[n][0] = *reinterpret_cast<const uint32_t*>(kc);
-            } else if constexpr (Part::SP == 2) {
+            const uint8_t* kc = tile + (D == 64 ? half * 8 : (c * 2 + half) * 1024) + lane * 16;
+            if constexpr (Part::SP == 2) {
                 const u32x2 k = *reinterpret_cast<const u32x2*>(kc);
                 raw.k[n][0] = k.x;
                 raw.k[n][1] = k.y;
@@ -1152,8 +1147,7 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
                 for (int e = 0; e < 4; ++e) raw.v[n][e] = v[e];
             }
             const uint8_t* ks = tile + L::kKs + key_scale_lane<FMT, D>(r, j) + (c * 2 + half) * L::KG;
-            if constexpr (L::KG == 2 && Part::kHalf) raw.ks[n] = ks[quarter];
-            else if constexpr (L::KG == 2) raw.ks[n] = *reinterpret_cast<const uint16_t*>(ks);
+            if constexpr (L::KG == 2) raw.ks[n] = *reinterpret_cast<const uint16_t*>(ks);
             else raw.ks[n] = *ks;
             const int g = c * (L::CH / L::G) + r * L::VD / L::G;
             raw.vs[n] = *reinterpret_cast<const uint32_t*>(tile + L::kVs + (g * 4 + j) * 8 + half * 4);
@@ -1167,21 +1161,17 @@ __global__ __launch_bounds__(64 * NW, WAVES) void attention_tiled(AttnArgs a, Kv
         u32x4(*out)[64] = lds[buf][my_tile];
         const int c = chunk0 + n;
         if constexpr (p < Part::SP) {
-            const int x = quarter * Part::SP + p;  // octet (j, x) of token 16 half + r
-            const u32x4 f = part_key<FMT, CT, D, p, Part::kHalf>(raw.k[n][p], raw.ks[n], a.k_exp);
-            if constexpr (k32) out[c * 2 * S + (j >> 1) * S + x][32 * (j & 1) + 16 * half + r] = f;
-            else out[half * (F / 2) + c * S + x][lane] = f;
+            // octet (j, p) of token 16 half + r
+            const u32x4 f = part_key<FMT, CT, D, p>(raw.k[n][p], raw.ks[n], a.k_exp);
+            if constexpr (k32) out[c * 2 * S + (j >> 1) * S + p][32 * (j & 1) + 16 * half + r] = f;
+            else out[half * (F / 2) + c * S + p][lane] = f;
         } else {
             constexpr int q = p - Part::SP;
             const int left = raw_left - 16 * half - 4 * j;  // value tokens of the quad that exist (clear_values)
             const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            uint32_t codes[Part::VW];
-#pragma unroll
-            for (int e = 0; e < Part::VW; ++e)
-                codes[e] = Part::kHalf ? raw.v[n][e] >> (quarter * 8 * Part::VP) : raw.v[n][e];
             u32x2 even, odd;
-            part_value<FMT, CT, D, q>(codes, raw.vs[n] & keep, a.v_exp, even, odd);
-            const int block = c * (L::VD / 2) + quarter * Part::VP + q;
+            part_value<FMT, CT, D, q>(raw.v[n], raw.vs[n] & keep, a.v_exp, even, odd);
+            const int block = c * Part::VP + q;
             if constexpr (k32) {
                 u32x2* vo = reinterpret_cast<u32x2*>(&out[F + block * 2 + half][32 * (j & 1) + 2 * r]) + (j >> 1);
                 vo[0] = even;

@@ -9,7 +9,6 @@ namespace fp4 {
 int kv_check(const fp4_kv_cache* c, KvArgs* a);  // kv_cache.hip
 bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs);
 
-
 struct AttnPlan {
     bool tiled;
     int MT, grid, splits;
@@ -121,7 +120,6 @@ static int attention_impl(const fp4_kv_cache* cache, const fp4_attention_args* x
     a.q_each = (int)(x->q_rows / x->batch);
     a.q_heads = (int)x->q_heads;
     a.group = (int)(x->q_heads / c.kv_heads);
-    a.table_cols = (int)x->page_columns;
     a.max_keys = (int)(x->page_columns * c.page_size);
     a.window = (int)std::min<int64_t>(x->window, a.max_keys);
     a.causal = x->causal;
