@@ -354,8 +354,9 @@ int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, const
 /* Read rows back: k and / or v (either may be NULL) at slots[t], as
  * code * scale (exact in FP32) times alpha in FP32, rounded to nearest even.
  * Rows whose slot is outside [0, pages * page_size) are written as zeros.
- * Alignment, strides and limits as fp4_kv_append; output rows must not
- * overlap (FP4_ERR_SHAPE). */
+ * Alignment, strides and limits as fp4_kv_append; the rows of k must not
+ * overlap each other, nor those of v (FP4_ERR_SHAPE), nor k's and v's (not
+ * checked). */
 int fp4_kv_read(const fp4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                 int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                 int act_type, void* stream);
@@ -366,7 +367,8 @@ int fp4_kv_read(const fp4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  * head h / (q_heads / kv_heads). */
 typedef struct fp4_attention_args {
     const void* q;             /* device [q_rows][q_heads][head_dim], strided, 16-byte aligned rows */
-    void* out;                 /* device, same type and shape, own strides (rows apart), 16-byte aligned rows */
+    void* out;                 /* device, same type and shape, own strides (rows apart), 16-byte aligned rows;
+                                  may be q itself, with q's strides */
     float* lse;                /* device [q_rows][q_heads] contiguous, or NULL: natural log of the softmax sum */
     const int32_t* page_table; /* device [batch][page_columns]; an entry outside [0, pages) holds no keys */
     const int32_t* seq_lens;   /* device [batch]; clamped to [0, page_columns * page_size] */

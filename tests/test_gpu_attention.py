@@ -782,3 +782,88 @@ def test_a_page_table_that_sequences_share():
     want = F.attention(q, p.cache(), table.repeat(3, 1), n, return_lse=True)
     got = F.attention(q, p.cache(), table.expand(3, -1), n, return_lse=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("group", [100, 1024])
+@pytest.mark.parametrize("news,lens", [([1, 1], [40, 300]), ([3, 1], [3, 150])])
+def test_many_query_heads_a_kv_head(group, news, lens):
+    """More query heads of a KV head than a row block holds."""
+    p = Problem(lens, news, 0, FP16, 64, 1, group, seed=group)
+    got = p.run()
+    torch.cuda.synchronize()
+    _check_sampled(p, got)
+
+
+@pytest.mark.parametrize("fmt,dtype", PAIRS)
+@pytest.mark.parametrize("D,group", [(64, 8), (128, 8), (256, 16)])
+@pytest.mark.parametrize("news,lens", [([1, 2], [90, 700]), ([70, 50], [90, 600])])
+def test_windows_and_sinks_of_every_kind(news, lens, D, group, fmt, dtype):
+    """Window and sinks for each pair of types and head size, in both kernels."""
+    p = Problem(lens, news, fmt, dtype, D, 2, group, 32, seed=D + group)
+    s = _sinks(2 * group, 7)
+    got = p.run(window=45, sinks=torch.from_numpy(s).cuda())
+    torch.cuda.synchronize()
+    _check_sampled(p, got, window=45, sinks=s)
+
+
+@pytest.mark.parametrize("fmt,news", [(0, [1, 1]), (1, [70, 70])])
+def test_pages_past_4_gib(fmt, news):
+    """The same pages at the start of a small cache and at the end of a large
+    one, and in the order reversed: the same bits."""
+    H, D, page = 8, 256, 256
+    p = Problem([600, 513], news, fmt, BF16, D, H, 2, page, seed=49)
+    want = p.run()
+    size = F.kv_cache_size(1, page, H, D, fmt)
+    pages = (5 << 30) // size
+    assert (pages - p.pages) * size > 1 << 32
+    big = F.new_kv_cache(pages, page, H, D, fmt)
+    last = pages - 1 - np.arange(p.pages)
+    small = torch.from_numpy(p.data).cuda().reshape(p.pages, size)
+    big.data.reshape(pages, size)[torch.from_numpy(last).cuda()] = small
+    table = np.where(p.table >= 0, last[np.clip(p.table, 0, p.pages - 1)], -1).astype(np.int32)
+    got = F.attention(p.q.cuda(), big, torch.from_numpy(table).cuda(),
+                      torch.tensor(p.lens, dtype=torch.int32, device="cuda"), scale=p.scale, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+    ps = [Problem([4000, 50], [1, 1], 0, BF16, seed=50), Problem([900, 700], [1, 1], 1, FP16, seed=51)]
+    want = [p.run() for p in ps]
+    args = [(p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda(),
+             torch.tensor(p.lens, dtype=torch.int32, device="cuda")) for p in ps]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                got[i].append(F.attention(*args[i], scale=ps[i].scale, stream=s, return_lse=True))
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(2):
+        assert len(got[i]) == 20
+        for o in got[i]:
+            assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
+
+
+@pytest.mark.parametrize("news,lens", [([1, 1], [4000, 70]), ([70, 64], [1500, 300])])
+def test_out_in_place_of_q(news, lens):
+    """Every workgroup has read its query rows before any of them is written."""
+    p = Problem(lens, news, 0, BF16, 128, 1, 8, seed=52)
+    want = p.run()
+    q = p.q.cuda()
+    got = p.run(q=q, out=q)
+    assert got[0].data_ptr() == q.data_ptr()
+    assert torch.equal(q, want[0]) and torch.equal(got[1], want[1])
