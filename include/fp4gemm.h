@@ -377,7 +377,8 @@ typedef struct fp4_attention_args {
                                   decrease anywhere, nothing is written */
     const float* sinks;        /* device [q_heads] or NULL: exp(sink) is added to the softmax sum */
     int64_t batch, q_rows, q_heads;
-    int64_t max_q;             /* about the most query tokens of a sequence (0: unknown).  Only chooses
+    int64_t max_q;             /* about the most query tokens of a sequence (0: unknown, all rows are taken
+                                  for one sequence's, which is slow for single tokens).  Only chooses
                                   the kernel: results do not depend on it beyond rounding */
     int64_t page_columns, page_stride; /* columns of the page table and elements between its rows (0: every
                                           sequence has the same row) */

@@ -346,16 +346,18 @@ __device__ __forceinline__ RowRange row_range(int i, int n, int len, int causal,
 // item that falls into several workgroups is joined by the one that arrives
 // last, from the FP32 partial sums of all, in their order.
 //
-// Bound by HBM while it streams: 12 waves a CU, each with the next tile's 4.6 KB
-// under way, read 7 TB/s; around that a workgroup spends 1.3 us on the scan of
+// Bound by HBM while it streams: up to 12 waves a CU, each with the next tile's
+// 4.6 KB under way (64 sequences of 4000 keys of head size 256, 590 MB: 6.0 TB/s
+// over the whole kernel); around that a workgroup spends 1.3 us on the scan of
 // the sequences, 1.5 us to its first tile, 1 us to join its waves and 2 us to
 // keep a partial sum and arrive.  Measured (MI355X, kernel time, 64 query and 8
-// KV heads of 128): 64 sequences of 16 .. 8192 keys, NVFP4, 59 us (304 MB, 5.1
+// KV heads of 128): 64 sequences of 16 .. 8192 keys, NVFP4, 60 us (304 MB, 5.1
 // TB/s); one sequence of 131071 keys, MXFP4, 35 us (143 MB, 4.1 TB/s; its 94
 // partial sums a head are joined in two stages of sixteen, which costs 6 us
 // against 11 us in one); one of 1000 keys 9 us, latency; four query tokens each
-// over 16 sequences of 1000 .. 5000 keys 28 us, where two row tiles bring the
-// vector work of a tile above its load time.  Tried: shares of equal length
+// over 16 sequences of 1000 .. 5000 keys 29 us, latency: two row tiles leave
+// registers for two waves a SIMD, 1.3 are resident in the mean, the vector units
+// are busy 34 % of the time and the matrix cores 9 %.  Tried: shares of equal length
 // dispatched one a workgroup (77 us for the first case, where this took 75) and
 // drawn from an atomic counter (115 us and more: all workgroups queue at it).
 struct Seq {
@@ -902,8 +904,8 @@ __device__ __forceinline__ void unrolled(Fn&& f) {
 // waves a SIMD (six prompts: 253 us with one wave, 207 with spills, 180 so).
 //
 // Bound by power: a chunk of 2048 tokens over 8192 keys (NVFP4, 64 and 8 heads
-// of 128) takes 452 us in a row of calls, 1065 TFLOP/s against 1311 of a large
-// library product, with the clock down to 1.75 GHz; the matrix cores are busy 51 %
+// of 128) takes 435 .. 465 us in a row of calls, 1030 .. 1106 TFLOP/s against 1311
+// of a large library product, with the clock down to 1.75 GHz; the matrix cores are busy 51 %
 // of the cycles, the vector units as long.  So what saves work counts more than what
 // overlaps it: 256 rows a workgroup instead of 128 (570 -> 537 us, half the
 // dequantization) and steps of four tiles instead of two (-> 490 us).

@@ -28,11 +28,14 @@ static int attn_plan(const KvArgs& c, int64_t D, const fp4_attention_args& x, At
     const int64_t rows = each * group;
     p->MT = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
     // The tiled kernel, its items cut into shares where they do not fill the
-    // GPU.  Measured (us, streaming / tiled; 64 query and 8 KV heads of 128, 8192
-    // keys): 32 query tokens 49 / 60, 64 (512 rows) 62 / 62, 128 95 / 75, 512
-    // 279 / 147; head size 256 (16, 4): 128 (512 rows) 63 / 74, 256 94 / 78.  With
-    // many sequences its partly filled blocks pay earlier: 32 sequences of 16
-    // tokens (128 rows), 4000 keys 133 / 118.
+    // GPU.  Measured (us, streaming / tiled; 64 query and 8 KV heads, 8192 keys):
+    // head size 128: 32 query tokens 40 / 43, 64 (512 rows) 60 / 53, 128 103 / 67,
+    // 512 361 / 138; head size 64: 32 25 / 33, 64 35 / 35, 128 60 / 46, 512 184 / 88;
+    // head size 256 (16, 4): 64 (256 rows) 46 / 43, 128 64 / 55, 192 (768 rows)
+    // 84 / 86, 256 104 / 72, uneven as the numbers of shares are.  With many
+    // sequences its partly filled blocks pay earlier: 32 sequences of 16 tokens (128
+    // rows), 4000 keys 207 / 120 (head size 64: 106 / 83); but 16 of 8 tokens (64
+    // rows) 61 / 70.
     const int64_t tiled = tiled_rows((int)D);
     const int64_t tiled_items = (x.q_rows * group / tiled + x.batch) * c.kv_heads;
     p->tiled = rows >= (D == 256 ? 768 : 512) || (rows >= 128 && x.batch * c.kv_heads >= 128);
