@@ -1303,9 +1303,17 @@ template <int FMT>
 __device__ __forceinline__ uint32_t quantize_block(const float (&x)[FMT == 0 ? 16 : 32], float alpha,
                                                    uint32_t (&out)[FMT == 0 ? 2 : 4]) {
     constexpr int G = FMT == 0 ? 16 : 32;
+    // The maximum that keeps NaNs tells of one at the end; fmaxf drops quiet NaNs,
+    // but what came before a signalling one with it.
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < G; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf drops NaN operands
+    for (int i = 0; i < G; ++i) amax = __builtin_elementwise_maximum(amax, fabsf(x[i]));
+    const bool nan_any = __builtin_isnan(amax);
+    if (nan_any) {
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) amax = fmaxf(amax, __builtin_isnan(x[i]) ? 0.0f : fabsf(x[i]));
+    }
     uint32_t sb;
     float sval;
     if constexpr (FMT == 0) {
@@ -1336,9 +1344,6 @@ __device__ __forceinline__ uint32_t quantize_block(const float (&x)[FMT == 0 ? 1
         if ((ab & 0x007FFFFFu) == 0u && ((ab >> 23) & 0xFF) != 0u && ((Sb >> 23) & 0xFF) != 0u) {
             const float sc = __uint_as_float(Sb & 0x7F800000u);  // 2^es (S is normal: >= 2^-109)
             const float r = __builtin_amdgcn_rcpf(__uint_as_float((Sb & 0x007FFFFFu) | 0x3F800000u));
-            bool nan_any = false;
-#pragma unroll
-            for (int i = 0; i < G / 2; ++i) nan_any |= __builtin_isunordered(x[2 * i], x[2 * i + 1]);
             float y[G];
 #pragma unroll
             for (int i = 0; i < G; ++i) {
@@ -1375,9 +1380,6 @@ __device__ __forceinline__ uint32_t quantize_block(const float (&x)[FMT == 0 ? 1
         const int es = int((ab >> 23) & 0xFF) - 127 + int(sb) - 127;  // log2 S when alpha = 2^(exp)
         if ((ab & 0x007FFFFFu) == 0u && ((ab >> 23) & 0xFF) != 0u && es >= -127 && es <= 127) {
             const float sc = __uint_as_float((uint32_t)(es + 127) << 23);
-            bool nan_any = false;
-#pragma unroll
-            for (int i = 0; i < G / 2; ++i) nan_any |= __builtin_isunordered(x[2 * i], x[2 * i + 1]);
 #pragma unroll
             for (int w = 0; w < G / 8; ++w) {
                 // FP32 operands (the BF16 values, exact): a bit cast of single

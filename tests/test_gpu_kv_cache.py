@@ -222,3 +222,22 @@ def test_more_tokens_than_one_launch_covers():
     F.kv_append(small, x[pick, :1], x[pick, 1:], torch.arange(6, device="cuda"))
     ks, vs = F.kv_read(small, torch.arange(6, device="cuda"))
     assert torch.equal(k[pick], ks) and torch.equal(v[pick], vs)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("ka,va", [(1.0, 0.37), (2.0 ** -20, 3000.0), (2.0 ** 60, 1e-30)])
+def test_append_every_bf16_value(fmt, ka, va):
+    """Every BF16 bit pattern, among its neighbours and mixed: all NaNs, the
+    signalling ones too, become 0 and leave the rest of their block alone."""
+    bits = np.arange(65536, dtype=np.uint16)
+    mixed = np.random.Generator(np.random.PCG64(9)).permutation(bits)
+    x = torch.from_numpy(np.concatenate([bits, mixed]).view(np.int16)).view(BF16).reshape(-1, 1, 128)
+    n = x.shape[0]
+    cache = F.new_kv_cache(n // 64, 64, 1, 128, fmt, ka, va)
+    cache.data.zero_()
+    F.kv_append(cache, x.cuda(), x.flip(0).contiguous().cuda(), torch.arange(n, device="cuda"))
+    want = np.zeros(cache.data.numel(), np.uint8)
+    f = x.float().numpy()
+    with np.errstate(all="ignore"):
+        oracle.kv_write_reference(want, np.arange(n), f, f[::-1].copy(), 64, fmt, ka, va)
+    assert np.array_equal(cache.data.cpu().numpy(), want)

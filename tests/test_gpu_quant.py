@@ -273,3 +273,16 @@ def test_native_tiny_activation_blocks():
     assert np.all(np.abs(y_ref).max(axis=1) > 0), "every row keeps non-zero quantized activations"
     assert oracle.check_tolerance(yb, y_ref, bound).all()
 
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("alpha", [1.0, 0.37])
+def test_quantize_every_bf16_value(fmt, alpha):
+    """Every BF16 bit pattern, in order and mixed: a signalling NaN is 0 like
+    every other and does not hide the block's largest element."""
+    bits = np.arange(65536, dtype=np.uint16)
+    w = np.concatenate([bits, np.random.Generator(np.random.PCG64(9)).permutation(bits)]).reshape(-1, 256)
+    codes, scales = F.quantize(torch.from_numpy(w.view(np.int16)).view(torch.bfloat16).cuda(), fmt, alpha)
+    with np.errstate(all="ignore"):
+        want = oracle.quantize_reference(w, fmt, alpha)
+    assert np.array_equal(codes.cpu().numpy(), want[0]) and np.array_equal(scales.cpu().numpy(), want[1])
