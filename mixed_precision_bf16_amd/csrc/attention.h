@@ -357,9 +357,9 @@ __device__ __forceinline__ RowRange row_range(int i, int n, int len, int causal,
 // against 11 us in one); one of 1000 keys 9 us, latency; four query tokens each
 // over 16 sequences of 1000 .. 5000 keys 29 us, latency: two row tiles leave
 // registers for two waves a SIMD, 1.3 are resident in the mean, the vector units
-// are busy 34 % of the time and the matrix cores 9 %.  Tried: shares of equal length
-// dispatched one a workgroup (77 us for the first case, where this took 75) and
-// drawn from an atomic counter (115 us and more: all workgroups queue at it).
+// are busy 34 % of the time and the matrix cores 9 %.  Tried: shares of equal
+// length dispatched one a workgroup (77 us for the first case, where this took
+// 75) and drawn from an atomic counter (115 us and more: all workgroups queue at it).
 struct Seq {
     int q0, n;       // first query row, query tokens
     int len;         // keys
@@ -620,7 +620,8 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, MT)) void attention_str
 #pragma unroll
                 for (int u = 0; u < 2; ++u) sc[mt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
             auto keys = [&](auto uc, auto cc, auto stc) {
-                const u32x4 kf = key_step<FMT, CT, D, decltype(uc)::value, decltype(cc)::value, decltype(stc)::value>(x, a.k_exp);
+                const u32x4 kf =
+                    key_step<FMT, CT, D, decltype(uc)::value, decltype(cc)::value, decltype(stc)::value>(x, a.k_exp);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     sc[mt][decltype(uc)::value] =
@@ -905,10 +906,10 @@ __device__ __forceinline__ void unrolled(Fn&& f) {
 //
 // Bound by power: a chunk of 2048 tokens over 8192 keys (NVFP4, 64 and 8 heads
 // of 128) takes 435 .. 465 us in a row of calls, 1030 .. 1106 TFLOP/s against 1311
-// of a large library product, with the clock down to 1.75 GHz; the matrix cores are busy 51 %
-// of the cycles, the vector units as long.  So what saves work counts more than what
-// overlaps it: 256 rows a workgroup instead of 128 (570 -> 537 us, half the
-// dequantization) and steps of four tiles instead of two (-> 490 us).
+// of a large library product, with the clock down to 1.75 GHz; the matrix cores
+// are busy 51 % of the cycles, the vector units as long.  So what saves work
+// counts more than what overlaps it: 256 rows a workgroup instead of 128 (570 ->
+// 537 us, half the dequantization) and steps of four tiles instead of two (-> 490 us).
 //   S^T = K Q^T: with lane = 32 h + t, step i of a chunk takes the eight
 //   elements of octet (j, s) of token t, j = 2 (i / S) + h, s = i mod S, where
 //   octet (j, s) is dword s of the codes of lane (t mod 16, j);
