@@ -502,6 +502,19 @@ def _on_stream(device, stream):
     return _Guard(device, stream)
 
 
+def _keep(device, stream, used, made=()):
+    """After a launch on a given stream: the memory of the caller's tensors
+    (`used`) is not handed out again before that stream has passed the launch,
+    nor that of the tensors made on it (`made`) before the caller's stream has
+    passed what it does with them until it drops them."""
+    import torch
+    for t in used:
+        if t is not None:
+            t.record_stream(stream)
+    for t in made:
+        t.record_stream(torch.cuda.current_stream(device))
+
+
 def _act_type(dtype, what: str) -> int:
     import torch
     if dtype == torch.bfloat16:
@@ -546,6 +559,8 @@ def kv_append(cache: KVCache, k, v, slots, stream=None) -> None:
         st = lib().fp4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), sp, n, kt, kh, vt, vh, act, s)
     if st:
         _check(st, "fp4_kv_append")
+    if stream is not None:
+        _keep(dev, stream, (cache._data, k, v, slots))
 
 
 def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=None):
@@ -566,17 +581,20 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
         shape = (n, cache._kv_heads, cache._head_dim)
         kt = vt = cache._kv_heads * cache._head_dim  # strides of what is allocated here
         kh = vh = cache._head_dim
+        made = []
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=dev)
+            made.append(k_out := torch.empty(shape, dtype=dtype, device=dev))
         else:
             kt, kh = _rows(k_out, "k_out", *shape, dev)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=dev)
+            made.append(v_out := torch.empty(shape, dtype=dtype, device=dev))
         else:
             vt, vh = _rows(v_out, "v_out", *shape, dev)
         st = lib().fp4_kv_read(cache._ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), kt, kh, vt, vh, act, s)
     if st:
         _check(st, "fp4_kv_read")
+    if stream is not None:
+        _keep(dev, stream, (cache._data, slots, k_out, v_out), made)
     return k_out, v_out
 
 
@@ -656,8 +674,10 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     rows, heads, dim = q.shape
     sink = _vector(sinks, "sinks", heads, torch.float32, dev) if sinks is not None else 0
     with _on_stream(dev, stream) as s:
+        made = []
         if out is None:
             out = torch.empty_like(q) if q.is_contiguous() else torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+            made.append(out)
             ot, oh = heads * dim, dim
         elif out.dtype != q.dtype:
             raise ValueError("out must have q's type")
@@ -667,7 +687,7 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
             if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.device != dev or not lse.is_contiguous():
                 raise ValueError(f"lse must be a contiguous float32 tensor [{rows}][{heads}] on {dev}")
         elif return_lse:
-            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+            made.append(lse := torch.empty((rows, heads), dtype=torch.float32, device=dev))
         if workspace is None:
             need = _attention_workspace(cache._kv_heads, cache._page_size, dim, cache._fmt, *sizes[:5],
                                         q_offsets is not None)
@@ -681,4 +701,6 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
         st = lib().fp4_attention(cache._ref, args, s)
     if st:
         _check(st, "fp4_attention")
+    if stream is not None:
+        _keep(dev, stream, (q, cache._data, page_table, seq_lens, q_offsets, sinks, out, lse, workspace), made)
     return (out, lse) if return_lse else out

@@ -867,3 +867,45 @@ def test_out_in_place_of_q(news, lens):
     got = p.run(q=q, out=q)
     assert got[0].data_ptr() == q.data_ptr()
     assert torch.equal(q, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_temporaries_of_calls_on_another_stream():
+    """Inputs that the caller drops right after a call on a busy stream keep
+    their memory until that stream has read them, and so do outputs dropped
+    while the caller's stream still reads them."""
+    p = Problem([300, 200], [1, 1], 0, BF16, seed=53)
+    want = p.run()
+    q, table = p.q.cuda(), torch.from_numpy(p.table).cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32, device="cuda")
+    slots = torch.from_numpy(p.slots(0, np.arange(300))).cuda()
+    cache = p.cache()
+    rows = F.kv_read(cache, slots)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        inputs = [q.clone(), table.clone(), lens.clone(), slots.clone()]
+        sizes = [(t.shape, t.dtype) for t in inputs]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = F.attention(inputs[0], cache, inputs[1], inputs[2], scale=p.scale, stream=side, return_lse=True)
+        back = F.kv_read(cache, inputs[3], stream=side)
+        held = [t.data_ptr() for t in inputs]
+        del inputs
+        reused = [torch.zeros(shape, dtype=dtype, device="cuda") for shape, dtype in sizes]
+        assert not set(held) & {t.data_ptr() for t in reused}
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip((*got, *back), (*want, *rows)):
+            assert torch.equal(a, b)
+        # the other way round: the caller's stream is late
+        torch.cuda._sleep(20_000_000)
+        copies = [t.clone() for t in got]
+        held = [t.data_ptr() for t in got]
+        shapes = [(t.shape, t.dtype) for t in got]
+        del got, a, b
+        with torch.cuda.stream(side):
+            reused = [torch.zeros(shape, dtype=dtype, device="cuda") for shape, dtype in shapes]
+        assert not set(held) & {t.data_ptr() for t in reused}
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b)
+        del copies, reused, back, a, b
