@@ -909,3 +909,27 @@ def test_temporaries_of_calls_on_another_stream():
         for a, b in zip(copies, want):
             assert torch.equal(a, b)
         del copies, reused, back, a, b
+
+
+def test_capture_that_forks_to_another_stream():
+    """A captured step whose attention runs on a second stream, with
+    temporaries of both; replayed over other queries, eager work in between."""
+    p = Problem([2000, 300], [1, 1], 0, BF16, seed=54)
+    q, cache, table = p.q.cuda(), p.cache(), torch.from_numpy(p.table).cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    F.attention(q, cache, table, lens, return_lse=True)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        got = F.attention(q * 1.0, cache, table + 0, lens, stream=side, return_lse=True)
+        main.wait_stream(side)
+        got = [t.clone() for t in got]
+    for seed in range(4):
+        q.copy_(torch.randn(q.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)))
+        want = F.attention(q, cache, table, lens, return_lse=True)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
