@@ -1,8 +1,10 @@
 /*
  * fp4gemm.h -- C ABI of the BF16 / FP16 x FP4 block-scaled GEMM for AMD MI355X (gfx950),
  * with its grouped mixture-of-experts variant, the offline repack and the
- * offline quantizer, and of a key/value cache in the same FP4 formats with the
- * attention that reads it.
+ * offline quantizer, of a key/value cache in the same FP4 formats with the
+ * attention that reads it, and of what a decoder layer has between these: the
+ * norm with the residual's addition, rotary positions, and products of 8-bit
+ * activations (plain and gated).
  *
  *   Y[m][N] = A[m][K] . dequant(W)[N][K]^T,   dequant(W)[n][k] = e2m1(code[n][k]) * scale[n][k / G]
  *
@@ -37,7 +39,8 @@
  *     leaves every output untouched.
  *   - The caller owns every buffer.  The library never allocates, frees or
  *     synchronizes in any device entry (fp4_gemm*, fp4_moe_gemm,
- *     fp4_quantize, fp4_dequant*, fp4_kv_append, fp4_kv_read, fp4_attention): they only queue kernels on `stream`.
+ *     fp4_quantize, fp4_dequant*, fp4_kv_append, fp4_kv_read, fp4_attention, fp4_rms_norm, fp4_quantize_mx8,
+ *     fp4_gemm_mx8, fp4_rope, fp4_kv_append_rope): they only queue kernels on `stream`.
  *   - "device" pointers must be HIP device memory on the current device;
  *     "host" pointers must be ordinary host memory.
  *   - Functions are reentrant and thread-safe; the only global state is a
@@ -241,8 +244,13 @@ int fp4_quantize(const void* W, void* codes, void* scales, int64_t N, int64_t K,
 int fp4_native_repack_size(int64_t N, int64_t K, size_t* wq_bytes, size_t* sq_bytes);
 
 /* Offline, host to host: canonical MXFP4 codes [N][K/2] and scales [N][K/32]
- * -> the native packed layout (a pure permutation plus zero padding; scale
- * byte 0xFF rejected with FP4_ERR_VALUE, nothing written then). */
+ * -> the native packed layout (a pure permutation plus zero padding to N a
+ * multiple of 16 and K of 512; scale byte 0xFF rejected with FP4_ERR_VALUE,
+ * nothing written then).  Codes: for every tile of 16 rows and chunk of 128 k
+ * (tile-major) 1 KiB, whose 16 bytes at (16 j + r) * 16 are the canonical bytes
+ * 64 chunk + 16 j .. + 15 of row 16 tile + r.  Scales: for every tile and 512 k
+ * (q) 256 bytes, byte (16 j + r) * 4 + s being the scale of block 16 q + 4 s + j
+ * of row 16 tile + r. */
 int fp4_native_repack(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K, uint8_t* wq,
                       uint8_t* sq);
 
@@ -420,6 +428,130 @@ int fp4_attention_workspace_size(const fp4_kv_cache* cache, const fp4_attention_
  * or a scale outside its range, is FP4_ERR_VALUE.  batch == 0 or q_rows == 0
  * is a no-op. */
 int fp4_attention(const fp4_kv_cache* cache, const fp4_attention_args* args, void* stream);
+
+/* ---- 8-bit activations ------------------------------------------------------
+ * Activations in 8 bits (MX8): rows of E4M3 codes (OCP FP8) with one E8M0 scale
+ * (2^(byte - 127)) for each 32 of them.
+ *   codes  device, uint8 [rows][Kp], Kp = K rounded up to 128; 16-byte aligned
+ *   scales device, uint8 [rows][Kp / 32]; 4-byte aligned
+ * K is a multiple of 32; what lies behind K has to be zero, and every entry that
+ * writes such rows writes those zeros.  Rule: a block's scale is the least
+ * power of two, 2^-127 at least, with (largest finite magnitude) / scale <= 448;
+ * code = nearest E4M3 value of element / scale, ties to the even code; a NaN or
+ * infinite element gives a NaN code (0x7F or 0xFF). */
+
+/* Bytes of `rows` rows of K elements (either pointer may be NULL).  rows <=
+ * 2^24, K <= 2^20. */
+int fp4_mx8_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
+
+/* BF16 (act_type 0) or FP16 (1) rows to 8 bits on `stream`: element k of row i at
+ * i * x_stride + k; x 16-byte aligned, x_stride >= 0, below 2^40 and a multiple
+ * of 8.  rows == 0 is a no-op. */
+int fp4_quantize_mx8(const void* x, int64_t rows, int64_t K, int64_t x_stride, int act_type, void* codes,
+                     void* scales, void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition before it:
+ *   h = x + residual                     (FP32; sum = h rounded to the type)
+ *   out = h / sqrt(mean(h^2) + eps) * weight
+ * The norm is taken of the unrounded h.  The squares are summed in FP64; the
+ * root, its product with h and that with the weight are each rounded to FP32,
+ * then the result to its type: the same bits whatever the kernel. */
+typedef struct fp4_rms_norm_args {
+    const void* x;        /* device, BF16 or FP16 [rows][width], strided */
+    const void* residual; /* the same, or NULL: h = x */
+    const void* weight;   /* device [width], or NULL: 1 */
+    void* out;            /* out_type 0: x's type, strided, rows apart; may be x or residual.  1: MX8 codes */
+    void* out_scales;     /* MX8 scales */
+    void* sum;            /* x's type, strided, rows apart, or NULL; may be x or residual, not out */
+    int64_t rows, width;  /* width a multiple of 8 (MX8: 32), 8 .. 2^20; rows <= 2^24 */
+    int64_t x_stride, residual_stride, out_stride, sum_stride; /* elements between rows: multiples of 8, >= 0 */
+    float eps;            /* in (0, 1], else FP4_ERR_VALUE */
+    int32_t act_type;     /* 0 BF16, 1 FP16 */
+    int32_t out_type;     /* 0 as x, 1 MX8 (out_stride is not used) */
+} fp4_rms_norm_args;
+
+/* All 16-bit arrays 16-byte aligned.  An array that is both read and written is
+ * given with the same pointer and stride, or does not overlap.  rows == 0 is a
+ * no-op. */
+int fp4_rms_norm(const fp4_rms_norm_args* args, void* stream);
+
+/* Products of 8-bit activations with MXFP4 weights in the native packed layout
+ * (fp4_native_repack), on the scaled matrix cores, accumulated in FP32:
+ *   gate 0:  Y = alpha * (A . dequant(W)^T), N columns
+ *   gate 1:  Y = silu(alpha * G) * (alpha * U), gate 2: gelu(alpha * G) * (alpha * U)
+ *            (tanh form), with G and U the products with rows 0 .. N/2 - 1 and
+ *            N/2 .. N - 1 of W: N/2 columns (the first half of a gated
+ *            feed-forward layer, its two projections stacked)
+ * out_type 0 / 1: BF16 / FP16 [m][columns], contiguous; 2: MX8, quantized from
+ * FP32 (the input of the layer's next product). */
+typedef struct fp4_gemm_mx8_args {
+    const void* codes;   /* device MX8 [m] rows of K */
+    const void* scales;
+    const void* wq;      /* device, fp4_native_repack_size(N, K) bytes, 16-byte aligned */
+    const void* sq;
+    void* out;           /* 16-byte aligned; every element is written */
+    void* out_scales;    /* out_type 2 */
+    void* workspace;     /* device, 256-byte aligned, fp4_gemm_mx8_workspace_size bytes (NULL when 0) */
+    size_t workspace_bytes;
+    int64_t m, N, K;
+    int32_t out_type;    /* 0, 1, 2; FP4_ERR_FORMAT otherwise */
+    int32_t gate;        /* 0, 1, 2; FP4_ERR_FORMAT otherwise */
+    float alpha;         /* as fp4_gemm_ex */
+} fp4_gemm_mx8_args;
+
+/* Workspace of fp4_gemm_mx8: a function of its arguments (no device is queried;
+ * 0 for many shapes).  Its contents need no initialization and are not
+ * preserved; calls that may run at the same time need separate workspaces. */
+int fp4_gemm_mx8_workspace_size(int64_t m, int64_t N, int64_t K, int out_type, int gate, size_t* bytes);
+
+/* K % 32 == 0, K <= 2^20, N <= 2^24, m <= 2^20; with a gate N % 32 == 0; with
+ * MX8 output the columns % 32 == 0; with m rounded up to 256, m * Kp bytes of A
+ * and the bytes of Y below 2^31 (else FP4_ERR_SHAPE).  m == 0 is a no-op.
+ * Deterministic. */
+int fp4_gemm_mx8(const fp4_gemm_mx8_args* args, void* stream);
+
+/* ---- Rotary positions --------------------------------------------------------
+ * Pair i of a head (i < rotary / 2) at position p is turned by p * frequency[i]:
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * with (a, b) elements i and i + rotary / 2 (halves) or 2 i and 2 i + 1
+ * (interleaved) of the head; elements from rotary on stay as they are.  The angle
+ * is formed and its cosine and sine, times the amplitude, are taken in FP64 and
+ * rounded to FP32; products and sums are rounded to FP32 one by one, the result
+ * to the row's type.  Angles beyond 2^31 lose accuracy.  Scalings for long
+ * contexts are other frequencies (and an amplitude). */
+typedef struct fp4_rope_args {
+    const int64_t* positions; /* device [tokens] */
+    const float* frequencies; /* device [rotary / 2] */
+    int64_t rotary;           /* even, 2 .. head_dim */
+    double amplitude;         /* in [2^-20, 2^20], else FP4_ERR_VALUE */
+    int32_t interleaved;
+} fp4_rope_args;
+
+/* out = x turned, on `stream`: element e of head h of token t at t *
+ * token_stride + h * head_stride + e; BF16 (act_type 0) or FP16 (1).  out may be
+ * x (same strides), else they do not overlap; its rows are apart.  head_dim a
+ * multiple of 8, 8 .. 1024; heads <= 65536, tokens <= 2^24; alignment and strides
+ * as fp4_kv_append.  tokens == 0 or heads == 0 is a no-op. */
+int fp4_rope(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens, int64_t heads, int64_t head_dim,
+             int64_t x_token_stride, int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride,
+             int act_type, void* stream);
+
+/* fp4_rope of queries and keys and fp4_kv_append of the turned keys and the
+ * values in one launch: the same bits as those calls one after another. */
+typedef struct fp4_append_rope_args {
+    const void* q;        /* device [tokens][q_heads][head_dim]; NULL with q_heads == 0 */
+    void* q_out;          /* may be q, with q's strides; else overlaps none of q, k, v */
+    const void* k;        /* device [tokens][kv_heads][head_dim]; not written */
+    const void* v;
+    const int64_t* slots; /* device [tokens]; outside the cache: key and value are skipped, queries turned all the same */
+    int64_t tokens, q_heads;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int32_t act_type;     /* 0 BF16, 1 FP16 */
+} fp4_append_rope_args;
+
+int fp4_kv_append_rope(const fp4_kv_cache* cache, const fp4_rope_args* rope, const fp4_append_rope_args* args,
+                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -37,21 +37,6 @@ __device__ __forceinline__ void widen2(uint32_t p, float& lo, float& hi) {
     }
 }
 
-// Tile that slot `slot` lies in, head h.
-__device__ __forceinline__ uint8_t* kv_tile_of(const KvArgs& c, int64_t slot, int h, int tile_bytes, int& t) {
-    int64_t page;
-    int off;
-    if (c.slots <= 0xFFFFFFFFll) {  // 32-bit division
-        page = (uint32_t)slot / (uint32_t)c.page_size;
-        off = (int)((uint32_t)slot - (uint32_t)page * (uint32_t)c.page_size);
-    } else {
-        page = slot / c.page_size;
-        off = (int)(slot - page * c.page_size);
-    }
-    t = off % kKvTile;
-    return c.data + ((page * c.kv_heads + h) * c.tiles_per_page + off / kKvTile) * (int64_t)tile_bytes;
-}
-
 // One thread quantizes one block of G elements of a key or value row
 // (quantize_block, the rule of fp4_quantize) and scatters its codes and scale
 // into the tile.  Four neighbouring lanes take four consecutive tokens, whose
@@ -65,8 +50,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs c, const uint16_t
                                                         const uint16_t* __restrict__ v,
                                                         const int64_t* __restrict__ slots, int tokens,
                                                         int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs) {
-    using L = KvTile<FMT, D>;
-    constexpr int G = L::G, GP = D / G;
+    constexpr int G = KvTile<FMT, D>::G, GP = D / G;
     const uint32_t n = blockIdx.x * 256u + threadIdx.x;
     const int token = (int)(n / (4 * GP) * 4 + n % 4), g = (int)(n / 4 % GP);
     const int h = blockIdx.y >> 1;
@@ -82,31 +66,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs c, const uint16_t
     float x[G];
 #pragma unroll
     for (int i = 0; i < G / 2; ++i) widen2<ACT>(raw[i / 4][i % 4], x[2 * i], x[2 * i + 1]);
-    uint32_t out[G / 8];
-    const uint32_t sb = quantize_block<FMT>(x, is_v ? c.v_alpha : c.k_alpha, out);
-    int t;
-    uint8_t* tile = kv_tile_of(c, slot, h, L::kBytes, t);
-    if (!is_v) {
-        if constexpr (FMT == 1 && D != 64) {
-            *reinterpret_cast<u32x4*>(tile + L::k_code(t, g * G)) = u32x4{out[0], out[1], out[2], out[3]};
-        } else {
-#pragma unroll
-            for (int w = 0; w < G / 16; ++w)
-                *reinterpret_cast<u32x2*>(tile + L::k_code(t, g * G + 16 * w)) = u32x2{out[2 * w], out[2 * w + 1]};
-        }
-        tile[L::k_scale(t, g)] = (uint8_t)sb;
-    } else {
-#pragma unroll
-        for (int w = 0; w < G / 8; ++w) {
-            if constexpr (D == 64) {
-                *reinterpret_cast<uint16_t*>(tile + L::v_code(t, g * G + 8 * w)) = (uint16_t)out[w];
-                *reinterpret_cast<uint16_t*>(tile + L::v_code(t, g * G + 8 * w + 4)) = (uint16_t)(out[w] >> 16);
-            } else {
-                *reinterpret_cast<uint32_t*>(tile + L::v_code(t, g * G + 8 * w)) = out[w];
-            }
-        }
-        tile[L::v_scale(t, g)] = (uint8_t)sb;
-    }
+    kv_store_block<FMT, D>(c, slot, h, g, is_v, x);
 }
 
 // Eight codes times their scale and alpha, rounded to the output type.
@@ -170,7 +130,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, const int64_t* _
 }
 
 // Row strides (elements) of a [tokens][heads][D] array: 16-byte aligned rows.
-static bool rows_ok(const void* p, int64_t ts, int64_t hs) {
+bool rows_ok(const void* p, int64_t ts, int64_t hs) {
     const int64_t most = int64_t(1) << 40;
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ts >= 0 && hs >= 0 && ts < most && hs < most && ts % 8 == 0 &&
            hs % 8 == 0;
@@ -209,26 +169,6 @@ static void read_t(const KvArgs& c, const int64_t* slots, int tokens, uint16_t* 
     else
         kv_read_kernel<FMT, ACT, D, false><<<grid, block, 0, s>>>(c, slots, tokens, k, v, k_ts, k_hs, v_ts, v_hs);
 }
-
-// Calls F<FMT, ACT, D>(args...) for the run-time format, type and head size.
-#define FP4_KV_DISPATCH(F, fmt, act, dim, ...)                                       \
-    do {                                                                             \
-        const int key_ = (int)(dim) * 4 + (fmt) * 2 + (act);                         \
-        switch (key_) {                                                              \
-            case 64 * 4 + 0: F<0, 0, 64>(__VA_ARGS__); break;                        \
-            case 64 * 4 + 1: F<0, 1, 64>(__VA_ARGS__); break;                        \
-            case 64 * 4 + 2: F<1, 0, 64>(__VA_ARGS__); break;                        \
-            case 64 * 4 + 3: F<1, 1, 64>(__VA_ARGS__); break;                        \
-            case 128 * 4 + 0: F<0, 0, 128>(__VA_ARGS__); break;                      \
-            case 128 * 4 + 1: F<0, 1, 128>(__VA_ARGS__); break;                      \
-            case 128 * 4 + 2: F<1, 0, 128>(__VA_ARGS__); break;                      \
-            case 128 * 4 + 3: F<1, 1, 128>(__VA_ARGS__); break;                      \
-            case 256 * 4 + 0: F<0, 0, 256>(__VA_ARGS__); break;                      \
-            case 256 * 4 + 1: F<0, 1, 256>(__VA_ARGS__); break;                      \
-            case 256 * 4 + 2: F<1, 0, 256>(__VA_ARGS__); break;                      \
-            case 256 * 4 + 3: F<1, 1, 256>(__VA_ARGS__); break;                      \
-        }                                                                            \
-    } while (0)
 
 static int append_impl(const fp4_kv_cache* cache, const void* k, const void* v, const int64_t* slots, int64_t tokens,
                        int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, int act_type, void* stream) {

@@ -76,4 +76,73 @@ struct KvArgs {
     float k_alpha, v_alpha;
 };
 
+// Tile that slot `slot` lies in, head h.
+__device__ __forceinline__ uint8_t* kv_tile_of(const KvArgs& c, int64_t slot, int h, int tile_bytes, int& t) {
+    int64_t page;
+    int off;
+    if (c.slots <= 0xFFFFFFFFll) {  // 32-bit division
+        page = (uint32_t)slot / (uint32_t)c.page_size;
+        off = (int)((uint32_t)slot - (uint32_t)page * (uint32_t)c.page_size);
+    } else {
+        page = slot / c.page_size;
+        off = (int)(slot - page * c.page_size);
+    }
+    t = off % kKvTile;
+    return c.data + ((page * c.kv_heads + h) * c.tiles_per_page + off / kKvTile) * (int64_t)tile_bytes;
+}
+
+// Quantizes one block of G elements x of a key or value row (quantize_block, the
+// rule of fp4_quantize) and scatters its codes and scale into its tile.
+template <int FMT, int D>
+__device__ __forceinline__ void kv_store_block(const KvArgs& c, int64_t slot, int h, int g, bool is_v,
+                                               const float (&x)[KvTile<FMT, D>::G]) {
+    using L = KvTile<FMT, D>;
+    constexpr int G = L::G;
+    uint32_t out[G / 8];
+    const uint32_t sb = quantize_block<FMT>(x, is_v ? c.v_alpha : c.k_alpha, out);
+    int t;
+    uint8_t* tile = kv_tile_of(c, slot, h, L::kBytes, t);
+    if (!is_v) {
+        if constexpr (FMT == 1 && D != 64) {
+            *reinterpret_cast<u32x4*>(tile + L::k_code(t, g * G)) = u32x4{out[0], out[1], out[2], out[3]};
+        } else {
+#pragma unroll
+            for (int w = 0; w < G / 16; ++w)
+                *reinterpret_cast<u32x2*>(tile + L::k_code(t, g * G + 16 * w)) = u32x2{out[2 * w], out[2 * w + 1]};
+        }
+        tile[L::k_scale(t, g)] = (uint8_t)sb;
+    } else {
+#pragma unroll
+        for (int w = 0; w < G / 8; ++w) {
+            if constexpr (D == 64) {
+                *reinterpret_cast<uint16_t*>(tile + L::v_code(t, g * G + 8 * w)) = (uint16_t)out[w];
+                *reinterpret_cast<uint16_t*>(tile + L::v_code(t, g * G + 8 * w + 4)) = (uint16_t)(out[w] >> 16);
+            } else {
+                *reinterpret_cast<uint32_t*>(tile + L::v_code(t, g * G + 8 * w)) = out[w];
+            }
+        }
+        tile[L::v_scale(t, g)] = (uint8_t)sb;
+    }
+}
+
+// Calls F<FMT, ACT, D>(args...) for the run-time format, type and head size.
+#define FP4_KV_DISPATCH(F, fmt, act, dim, ...)                                       \
+    do {                                                                             \
+        const int key_ = (int)(dim) * 4 + (fmt) * 2 + (act);                         \
+        switch (key_) {                                                              \
+            case 64 * 4 + 0: F<0, 0, 64>(__VA_ARGS__); break;                        \
+            case 64 * 4 + 1: F<0, 1, 64>(__VA_ARGS__); break;                        \
+            case 64 * 4 + 2: F<1, 0, 64>(__VA_ARGS__); break;                        \
+            case 64 * 4 + 3: F<1, 1, 64>(__VA_ARGS__); break;                        \
+            case 128 * 4 + 0: F<0, 0, 128>(__VA_ARGS__); break;                      \
+            case 128 * 4 + 1: F<0, 1, 128>(__VA_ARGS__); break;                      \
+            case 128 * 4 + 2: F<1, 0, 128>(__VA_ARGS__); break;                      \
+            case 128 * 4 + 3: F<1, 1, 128>(__VA_ARGS__); break;                      \
+            case 256 * 4 + 0: F<0, 0, 256>(__VA_ARGS__); break;                      \
+            case 256 * 4 + 1: F<0, 1, 256>(__VA_ARGS__); break;                      \
+            case 256 * 4 + 2: F<1, 0, 256>(__VA_ARGS__); break;                      \
+            case 256 * 4 + 3: F<1, 1, 256>(__VA_ARGS__); break;                      \
+        }                                                                            \
+    } while (0)
+
 }  // namespace fp4

@@ -47,6 +47,11 @@ class _AttentionArgs(ctypes.Structure):
 
 # the same structure as bytes, which is quicker to fill
 _PACK_ATTENTION = struct.Struct("@7Q11q2if4x2Q")
+# fp4_rms_norm_args, fp4_gemm_mx8_args, fp4_rope_args, fp4_append_rope_args
+_PACK_NORM = struct.Struct("@6Q6qf2i4x")
+_PACK_MX8 = struct.Struct("@8Q3q2if4x")
+_PACK_ROPE = struct.Struct("@2Qqdi4x")
+_PACK_APPEND_ROPE = struct.Struct("@5Q10qi4x")
 
 
 # name -> (restype, argtypes); mirrors include/fp4gemm.h
@@ -82,6 +87,14 @@ _SIGNATURES = {
                                    _c_i64, _c_i64, ctypes.c_int, _c_vp]),
     "fp4_attention_workspace_size": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, ctypes.POINTER(_c_sz)]),
     "fp4_attention": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_vp]),
+    "fp4_mx8_size": (ctypes.c_int, [_c_i64, _c_i64, ctypes.POINTER(_c_sz), ctypes.POINTER(_c_sz)]),
+    "fp4_quantize_mx8": (ctypes.c_int, [_c_vp, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_vp, _c_vp, _c_vp]),
+    "fp4_rms_norm": (ctypes.c_int, [_c_vp, _c_vp]),
+    "fp4_gemm_mx8_workspace_size": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int,
+                                                   ctypes.POINTER(_c_sz)]),
+    "fp4_gemm_mx8": (ctypes.c_int, [_c_vp, _c_vp]),
+    "fp4_rope": (ctypes.c_int, [_c_vp, _c_vp, _c_vp] + [_c_i64] * 7 + [ctypes.c_int, _c_vp]),
+    "fp4_kv_append_rope": (ctypes.c_int, [ctypes.POINTER(_KVCacheDesc), _c_vp, _c_vp, _c_vp]),
 }
 
 STATUS = {0: "FP4_OK", 1: "FP4_ERR_NULL", 2: "FP4_ERR_SHAPE", 3: "FP4_ERR_FORMAT", 4: "FP4_ERR_VALUE",
@@ -704,3 +717,343 @@ def attention(q, cache: KVCache, page_table, seq_lens, q_offsets=None, max_q=Non
     if stream is not None:
         _keep(dev, stream, (q, cache._data, page_table, seq_lens, q_offsets, sinks, out, lse, workspace), made)
     return (out, lse) if return_lse else out
+
+
+# ------------------------------------------- 8-bit activations: norm, products
+def mx8_padded(K: int) -> int:
+    """Columns that K elements of a row take in 8 bits: K rounded up to 128."""
+    return (K + 127) // 128 * 128
+
+
+class MX8:
+    """Activations in 8 bits: `codes` (float8_e4m3fn CUDA [rows][mx8_padded(K)])
+    and `scales` (float8_e8m0fnu CUDA [rows][mx8_padded(K) / 32]), contiguous; the
+    value of element k is codes[i, k] * scales[i, k // 32].  What lies behind K has
+    to be zero."""
+
+    __slots__ = ("codes", "scales", "K")
+
+    def __init__(self, codes, scales, K: int):
+        import torch
+        if K < 32 or K % 32:
+            raise ValueError("K must be a multiple of 32")
+        Kp = mx8_padded(K)
+        if codes.dtype != torch.float8_e4m3fn or codes.dim() != 2 or codes.shape[1] != Kp or not codes.is_cuda:
+            raise ValueError(f"codes must be a float8_e4m3fn CUDA tensor [rows][{Kp}]")
+        if (scales.dtype != torch.float8_e8m0fnu or scales.shape != (codes.shape[0], Kp // 32)
+                or scales.device != codes.device):
+            raise ValueError(f"scales must be a float8_e8m0fnu tensor [rows][{Kp // 32}] on the codes' device")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        self.codes, self.scales, self.K = codes, scales, K
+
+
+def new_mx8(rows: int, K: int, device="cuda") -> MX8:
+    """Uninitialized 8-bit rows, for an entry to write."""
+    import torch
+    Kp = mx8_padded(K)
+    a = MX8.__new__(MX8)
+    a.codes = torch.empty((rows, Kp), dtype=torch.float8_e4m3fn, device=device)
+    a.scales = torch.empty((rows, Kp // 32), dtype=torch.float8_e8m0fnu, device=device)
+    a.K = K
+    return a
+
+
+def _matrix(t, what: str, rows: int, width: int, dtype, device):
+    """Row stride of a [rows][width] matrix with contiguous, 16-byte aligned rows."""
+    if t.dtype != dtype or t.shape != (rows, width) or t.device != device:
+        raise ValueError(f"{what} must be a {dtype} tensor [{rows}][{width}] on {device}")
+    a, b = t.stride()
+    a = a if rows > 1 else width  # the stride of a single row means nothing
+    if b != 1 or a % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{what} must have contiguous, 16-byte aligned rows")
+    return a
+
+
+def _mx8_out(out, rows: int, K: int, device):
+    if not isinstance(out, MX8) or out.codes.shape[0] != rows or out.K != K or out.codes.device != device:
+        raise ValueError(f"out must be an MX8 of {rows} rows of {K} on {device}")
+    return out
+
+
+def _pack(packer, what: str, *fields) -> bytes:
+    try:
+        return packer.pack(*fields)
+    except struct.error as e:
+        raise ValueError(f"{what}: {e}") from None
+
+
+def quantize_mx8(x, out: MX8 | None = None, stream=None) -> MX8:
+    """fp4_quantize_mx8: bfloat16 or float16 CUDA rows [rows][K] (K a multiple of
+    32; any row stride that is a multiple of 8) in 8 bits."""
+    act = _act_type(x.dtype, "x")
+    if x.dim() != 2 or not x.is_cuda or x.shape[1] < 32 or x.shape[1] % 32:
+        raise ValueError("x must be a CUDA matrix [rows][K], K a multiple of 32")
+    rows, K = x.shape
+    dev = x.device
+    xs = _matrix(x, "x", rows, K, x.dtype, dev)
+    with _on_stream(dev, stream) as s:
+        made = ()
+        if out is None:
+            out = new_mx8(rows, K, dev)
+            made = (out.codes, out.scales)
+        else:
+            _mx8_out(out, rows, K, dev)
+        st = lib().fp4_quantize_mx8(x.data_ptr(), rows, K, xs, act, out.codes.data_ptr(), out.scales.data_ptr(), s)
+    if st:
+        _check(st, "fp4_quantize_mx8")
+    if stream is not None:
+        _keep(dev, stream, (x, out.codes, out.scales), made)
+    return out
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False, out=None, sum_out=None, stream=None):
+    """fp4_rms_norm: y = h / sqrt(mean(h^2) + eps) * weight with h = x + residual.
+
+    x, residual: bfloat16 or float16 CUDA [rows][width] with any row strides that
+    are multiples of 8; weight: [width] of the same type, or None.  The width is a
+    multiple of 8 (with mx8: 32).  Returns y, of x's type or (mx8) an MX8; with a
+    residual (y, h), h rounded to x's type: the next layer's residual.  out and
+    sum_out are filled if given; sum_out may be x or residual, and out (16-bit)
+    the other one."""
+    import torch
+    act = _act_type(x.dtype, "x")
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a CUDA matrix [rows][width]")
+    rows, width = x.shape
+    dev, dtype = x.device, x.dtype
+    if width < 8 or width % (32 if mx8 else 8):
+        raise ValueError(f"the width must be a multiple of {32 if mx8 else 8}")
+    xs = _matrix(x, "x", rows, width, dtype, dev)
+    rs = _matrix(residual, "residual", rows, width, dtype, dev) if residual is not None else 0
+    if weight is not None:
+        _vector(weight, "weight", width, dtype, dev)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out goes with a residual")
+    with _on_stream(dev, stream) as s:
+        made, os, scales = [], width, 0
+        if mx8:
+            if out is None:
+                out = new_mx8(rows, width, dev)
+                made += (out.codes, out.scales)
+            else:
+                _mx8_out(out, rows, width, dev)
+            to, scales = out.codes.data_ptr(), out.scales.data_ptr()
+        else:
+            if out is None:
+                made.append(out := torch.empty((rows, width), dtype=dtype, device=dev))
+            else:
+                os = _matrix(out, "out", rows, width, dtype, dev)
+            to = out.data_ptr()
+        ss = width
+        if residual is not None:
+            if sum_out is None:
+                made.append(sum_out := torch.empty((rows, width), dtype=dtype, device=dev))
+            else:
+                ss = _matrix(sum_out, "sum_out", rows, width, dtype, dev)
+        args = _pack(_PACK_NORM, "rms_norm", x.data_ptr(), residual.data_ptr() if residual is not None else 0,
+                     weight.data_ptr() if weight is not None else 0, to, scales,
+                     sum_out.data_ptr() if residual is not None else 0, rows, width, xs, rs, os, ss, eps, act,
+                     1 if mx8 else 0)
+        st = lib().fp4_rms_norm(args, s)
+    if st:
+        _check(st, "fp4_rms_norm")
+    if stream is not None:
+        used = (x, residual, weight, sum_out) + ((out.codes, out.scales) if mx8 else (out,))
+        _keep(dev, stream, used, made)
+    return (out, sum_out) if residual is not None else out
+
+
+_GATES = {None: 0, "silu": 1, "gelu": 2}
+
+
+@functools.lru_cache(maxsize=1024)
+def gemm_mx8_workspace_size(m: int, N: int, K: int, out_type: int = 0, gate: int = 0) -> int:
+    """Bytes of workspace of a product (out_type 0 BF16, 1 FP16, 2 MX8; gate 0 none, 1 SiLU, 2 GELU)."""
+    b = _c_sz()
+    _check(lib().fp4_gemm_mx8_workspace_size(m, N, K, out_type, gate, ctypes.byref(b)), "fp4_gemm_mx8_workspace_size")
+    return b.value
+
+
+@functools.lru_cache(maxsize=256)
+def _native_sizes(N: int, K: int):
+    return native_repack_size(N, K)
+
+
+def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0, dtype=None, mx8: bool = False,
+             out=None, workspace=None, stream=None):
+    """fp4_gemm_mx8: alpha * A . dequant(W)^T of 8-bit rows with MXFP4 weights
+    [N][a.K] in the native layout (native_repack; uint8 CUDA tensors).  gate
+    "silu" or "gelu": act(G) * U of the products G and U with the first and the
+    second half of the weight's rows, N / 2 columns.  Returns (or fills) a
+    tensor [m][columns] of `dtype` (bfloat16 by default, or float16) or, with
+    mx8, an MX8."""
+    import torch
+    if gate not in _GATES:
+        raise ValueError("gate must be None, 'silu' or 'gelu'")
+    g = _GATES[gate]
+    if mx8:
+        if dtype is not None:
+            raise ValueError("dtype does not go with mx8")
+        kind = 2
+    else:
+        if dtype is None:
+            dtype = out.dtype if out is not None else torch.bfloat16
+        kind = _act_type(dtype, "dtype")
+    m, K, dev = a.codes.shape[0], a.K, a.codes.device
+    for t, n in zip((wq, sq), _native_sizes(N, K)):
+        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"wq / sq must be contiguous uint8 tensors of native_repack_size(N, K) bytes on {dev}")
+    cols = N // 2 if g else N
+    need = gemm_mx8_workspace_size(m, N, K, kind, g)
+    with _on_stream(dev, stream) as s:
+        made = []
+        if mx8:
+            if out is None:
+                out = new_mx8(m, cols, dev)
+                made += (out.codes, out.scales)
+            else:
+                _mx8_out(out, m, cols, dev)
+            to, scales = out.codes.data_ptr(), out.scales.data_ptr()
+        else:
+            if out is None:
+                made.append(out := torch.empty((m, cols), dtype=dtype, device=dev))
+            elif out.dtype != dtype or out.shape != (m, cols) or out.device != dev or not out.is_contiguous():
+                raise ValueError(f"out must be a contiguous {dtype} tensor [{m}][{cols}] on {dev}")
+            to, scales = out.data_ptr(), 0
+        if workspace is None:
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        wp, wn = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
+        args = _pack(_PACK_MX8, "gemm_mx8", a.codes.data_ptr(), a.scales.data_ptr(), wq.data_ptr(), sq.data_ptr(), to,
+                     scales, wp, wn, m, N, K, kind, g, alpha)
+        st = lib().fp4_gemm_mx8(args, s)
+    if st:
+        _check(st, "fp4_gemm_mx8")
+    if stream is not None:
+        used = (a.codes, a.scales, wq, sq, workspace) + ((out.codes, out.scales) if mx8 else (out,))
+        _keep(dev, stream, used, made)
+    return out
+
+
+# ------------------------------------------------------------ rotary positions
+def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 8192, low: float = 1.0, high: float = 4.0, fast: float = 32.0, slow: float = 1.0,
+                     device="cuda"):
+    """(frequencies float32 [rotary / 2], amplitude) for rope().  Pair i turns by
+    f = base^(-2 i / rotary) a position.  Scalings to `factor` times the
+    `original` context:
+      linear  f / factor (positions interpolated)
+      ntk     base * factor^(rotary / (rotary - 2)): the slowest pair as linear, the fastest kept
+      bands   by the turns n = original f / 2 pi that a pair makes in the original
+              context: n > high kept, n < low as linear, between them blended by n
+      yarn    the same blend by pair number, between the pairs that make `fast`
+              and `slow` turns; amplitude 1 + 0.1 ln factor"""
+    import math
+
+    import torch
+    if rotary < 2 or rotary % 2:
+        raise ValueError("rotary must be even, 2 at least")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be over 1 and factor 1 at least")
+    i = np.arange(rotary // 2, dtype=np.float64)
+    f = base ** (-2.0 * i / rotary)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ntk":
+        if rotary > 2:
+            f = (base * factor ** (rotary / (rotary - 2.0))) ** (-2.0 * i / rotary)
+    elif scaling == "bands":
+        keep = np.clip((original * f / (2 * math.pi) - low) / (high - low), 0.0, 1.0)
+        f = f / factor * (1.0 - keep) + f * keep
+    elif scaling == "yarn":
+        at = [rotary * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary - 1)
+        spread = np.clip((i - first) / max(last - first, 1e-3), 0.0, 1.0)
+        f = f / factor * spread + f * (1.0 - spread)
+        amplitude = 1.0 + 0.1 * math.log(factor)
+    elif scaling is not None:
+        raise ValueError("scaling must be None, 'linear', 'ntk', 'bands' or 'yarn'")
+    return torch.from_numpy(f.astype(np.float32)).to(device), amplitude
+
+
+def _rope_args(positions, frequencies, interleaved, amplitude, tokens, head_dim, device) -> bytes:
+    import torch
+    n = frequencies.shape[0] if frequencies.dim() == 1 else 0
+    if not 1 <= n <= head_dim // 2:
+        raise ValueError(f"frequencies must be a vector of 1 to {head_dim // 2} entries (half of the rotated elements)")
+    return _pack(_PACK_ROPE, "rope", _vector(positions, "positions", tokens, torch.int64, device),
+                 _vector(frequencies, "frequencies", n, torch.float32, device), 2 * n, amplitude, 1 if interleaved else 0)
+
+
+def rope(x, positions, frequencies, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """fp4_rope: x (bfloat16 or float16 CUDA [tokens][heads][head_dim], any token
+    and head strides that are multiples of 8) turned by its positions (int64
+    CUDA [tokens]).  frequencies: float32 CUDA [rotary / 2] (rope_frequencies);
+    the first `rotary` elements of a head are turned, in halves or, interleaved,
+    in neighbouring pairs.  Returns (or fills) out, which may be x."""
+    import torch
+    act = _act_type(x.dtype, "x")
+    if x.dim() != 3 or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor [tokens][heads][head_dim]")
+    tokens, heads, dim = x.shape
+    dev = x.device
+    xt, xh = _rows(x, "x", tokens, heads, dim, dev)
+    r = _rope_args(positions, frequencies, interleaved, amplitude, tokens, dim, dev)
+    with _on_stream(dev, stream) as s:
+        made = ()
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=dev)
+            made = (out,)
+            ot, oh = heads * dim, dim
+        elif out.dtype != x.dtype:
+            raise ValueError("out must have x's type")
+        else:
+            ot, oh = _rows(out, "out", tokens, heads, dim, dev)
+        st = lib().fp4_rope(r, x.data_ptr(), out.data_ptr(), tokens, heads, dim, xt, xh, ot, oh, act, s)
+    if st:
+        _check(st, "fp4_rope")
+    if stream is not None:
+        _keep(dev, stream, (x, positions, frequencies, out), made)
+    return out
+
+
+def kv_append_rope(cache: KVCache, q, k, v, slots, positions, frequencies, interleaved: bool = False,
+                   amplitude: float = 1.0, q_out=None, stream=None):
+    """fp4_kv_append_rope: rope() of q and k and kv_append() of the turned keys and
+    the values, in one launch.  q: [tokens][q_heads][head_dim]; k, v:
+    [tokens][kv_heads][head_dim] (not written); slots, positions: int64 CUDA
+    [tokens].  Returns (or fills) q_out, which may be q.  A token whose slot is
+    outside the cache is turned but not written."""
+    import torch
+    act = _act_type(k.dtype, "k")
+    dev, dim = cache._data.device, cache._head_dim
+    if v.dtype != k.dtype or q.dtype != k.dtype or q.dim() != 3:
+        raise ValueError("q, k and v must be tensors [tokens][heads][head_dim] of the same type")
+    n, heads = k.shape[0], q.shape[1]
+    strides = _rows(q, "q", n, heads, dim, dev)
+    ks = _rows(k, "k", n, cache._kv_heads, dim, dev)
+    vs = _rows(v, "v", n, cache._kv_heads, dim, dev)
+    sp = _vector(slots, "slots", n, torch.int64, dev)
+    r = _rope_args(positions, frequencies, interleaved, amplitude, n, dim, dev)
+    with _on_stream(dev, stream) as s:
+        made = ()
+        if q_out is None:
+            q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+            made = (q_out,)
+            os = heads * dim, dim
+        elif q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's type")
+        else:
+            os = _rows(q_out, "q_out", n, heads, dim, dev)
+        args = _pack(_PACK_APPEND_ROPE, "kv_append_rope", q.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(),
+                     sp, n, heads, *strides, *os, *ks, *vs, act)
+        st = lib().fp4_kv_append_rope(cache._ref, r, args, s)
+    if st:
+        _check(st, "fp4_kv_append_rope")
+    if stream is not None:
+        _keep(dev, stream, (q, k, v, slots, positions, frequencies, cache._data, q_out), made)
+    return q_out

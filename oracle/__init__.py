@@ -32,3 +32,13 @@ from .fp4_oracle import (  # noqa: F401
 from .moe_oracle import moe_reference  # noqa: F401,E402
 from .quant_oracle import native_reference, quantize_reference, quantize_values, scaled_gemm_reference  # noqa: F401,E402
 from .kv_oracle import attention_reference, kv_offsets, kv_read_reference, kv_write_reference  # noqa: F401,E402
+from . import layer_oracle  # noqa: F401,E402
+from .layer_oracle import (  # noqa: F401,E402
+    gate_reference,
+    gemm_mx8_reference,
+    mx8_padded,
+    mx8_quantize_reference,
+    mx8_value,
+    rms_norm_reference,
+    rope_reference,
+)

@@ -1,0 +1,93 @@
+"""Oracle of the operators around the FP4 products of a decoder layer: 8-bit
+activations (MX8), the root-mean-square norm, rotary positions, and the products
+of 8-bit activations with MXFP4 weights.  Plain NumPy in float64, written from the
+definitions in include/fp4gemm.h.
+
+Where the definition takes its decisions on FP32 values, the float64 result is
+rounded to FP32: sums, products, quotients and square roots of FP32 numbers formed
+in float64 and rounded once more are the correctly rounded ones (float64 has over
+twice FP32's bits plus two).
+"""
+
+import numpy as np
+
+from .fp4_oracle import dequant_weights, e4m3_value
+
+E4M3 = e4m3_value(np.arange(127))          # non-negative finite values, codes 0 .. 126
+
+
+def f32(x):
+    with np.errstate(over="ignore", invalid="ignore"):
+        return np.asarray(x, dtype=np.float64).astype(np.float32).astype(np.float64)
+
+
+def mx8_padded(K: int) -> int:
+    return -(-K // 128) * 128
+
+
+def mx8_quantize_reference(x: np.ndarray):
+    """FP32-valued rows [m][K] -> (codes u8 [m][Kp], scale bytes u8 [m][Kp / 32])."""
+    x = np.asarray(x, dtype=np.float64)
+    m, K = x.shape
+    Kp = mx8_padded(K)
+    b = np.zeros((m, Kp))
+    b[:, :K] = x
+    b = b.reshape(m, Kp // 32, 32)
+    finite = np.isfinite(b)
+    top = np.where(finite, np.abs(b), 0.0).max(-1)
+    mant, e = np.frexp(top)                                     # top = mant 2^e, mant in [0.5, 1)
+    e = np.where(top == 0, -127, np.maximum(e - 9 + (mant > 0.875), -127))
+    q = np.where(finite, np.abs(b), 0.0) / np.exp2(e.astype(np.float64))[..., None]
+    hi = np.clip(np.searchsorted(E4M3, q, side="left"), 1, 126)
+    lo = hi - 1
+    dlo, dhi = np.abs(q - E4M3[lo]), np.abs(E4M3[hi] - q)
+    code = np.where(dlo < dhi, lo, np.where(dhi < dlo, hi, np.where(lo % 2 == 0, lo, hi)))
+    code = np.where(finite, code | np.where(np.signbit(b), 128, 0), 0x7F)
+    return code.reshape(m, Kp).astype(np.uint8), (e + 127).astype(np.uint8)
+
+
+def mx8_value(codes: np.ndarray, scales: np.ndarray, K: int) -> np.ndarray:
+    codes = np.asarray(codes)
+    v = np.where((codes & 127) == 127, np.nan, E4M3[np.minimum(codes & 127, 126)]) * np.where(codes & 128, -1.0, 1.0)
+    return (v.reshape(len(codes), -1, 32) * np.exp2(scales.astype(np.float64) - 127)[..., None]).reshape(
+        len(codes), -1)[:, :K]
+
+
+def rms_norm_reference(x, weight, eps, residual=None):
+    """(y, h): the FP32 values of the definition before their last rounding, as float64."""
+    h = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        h = f32(h + residual)
+    eps = float(np.float32(eps))
+    with np.errstate(over="ignore", invalid="ignore"):
+        root = f32(1.0 / np.sqrt((h * h).sum(-1, keepdims=True) / h.shape[1] + eps))
+        y = f32(h * root)
+        return (f32(y * weight) if weight is not None else y), h
+
+
+def rope_reference(x, positions, frequencies, interleaved=False, amplitude=1.0):
+    """x [tokens][heads][D] -> the FP32 values before the rounding to the row's type."""
+    x = np.asarray(x, dtype=np.float64)
+    angle = np.asarray(positions, dtype=np.float64)[:, None] * np.asarray(frequencies, dtype=np.float64)
+    c, s = f32(np.cos(angle) * amplitude)[:, None], f32(np.sin(angle) * amplitude)[:, None]
+    n = angle.shape[1]
+    i = np.arange(n)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+    y = x.copy()
+    y[..., a] = f32(f32(x[..., a] * c) - f32(x[..., b] * s))
+    y[..., b] = f32(f32(x[..., b] * c) + f32(x[..., a] * s))
+    return y
+
+
+def gate_reference(g, u, gate):
+    with np.errstate(over="ignore"):
+        z = g if gate == "silu" else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+        return g / (1 + np.exp(-z)) * u
+
+
+def gemm_mx8_reference(a_codes, a_scales, w_codes, w_scales, K, alpha=1.0):
+    """(alpha A . dequant(W)^T, alpha |A| . |dequant(W)|^T) with canonical MXFP4 weights."""
+    a = mx8_value(a_codes, a_scales, K)
+    w = dequant_weights(w_codes, w_scales, K, 1)
+    al = float(np.float32(alpha))
+    return al * (a @ w.T), abs(al) * (np.abs(a) @ np.abs(w).T)
