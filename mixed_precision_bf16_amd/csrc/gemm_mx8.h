@@ -47,9 +47,10 @@ __device__ __forceinline__ i32x8 fp4_operand(const u32x4& w) {
 __device__ __forceinline__ i32x8 fp8_operand(const u32x4& lo, const u32x4& hi) {
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
-__device__ __forceinline__ f32x4 mfma_fp4_fp8(const i32x8& w, const i32x8& a, const f32x4& c, uint32_t ws,
-                                              uint32_t as) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 0, 0, (int)ws, 0, (int)as);
+// Weight scale: byte T of its dword (chunk T of the 512 k); activation scale: the low byte.
+template <int T>
+__device__ __forceinline__ f32x4 mfma_fp4_fp8(const u32x4& w, const i32x8& a, const f32x4& c, uint32_t ws, uint32_t as) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(w), a, c, 4, 0, T, (int)ws, 0, (int)as);
 }
 
 // Output tile `t` (columns 16 t ..) of row m: the lane's four columns.
@@ -79,114 +80,392 @@ __device__ __forceinline__ void mx8_store8(const Mx8Gemm& p, f32x4 v0, f32x4 v1,
     }
 }
 
-// Small m.  A workgroup of NWK waves takes TN weight tiles (gated: TN / 2 gate
-// tiles and the TN / 2 up tiles of the same columns) and 16 MB rows of A; each
-// wave streams its share of K straight into registers, PD chunks ahead; the waves'
-// sums meet in LDS, in the order of the waves.
-template <int MB, int TN, int NWK, int PD>
-__global__ __launch_bounds__(64 * NWK) void gemm_mx8_stream(Mx8Gemm p) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds_raw[];
-    f32x4* lds = reinterpret_cast<f32x4*>(lds_raw);
+// The result of output tiles t (and with 8-bit output t + 1) from their sums.
+// `sum(x)`: FP32 sums of weight tile x of the caller's group: output tiles first,
+// gated: then the up tiles, `half` further on.
+template <class Sum>
+__device__ __forceinline__ void mx8_finish(const Mx8Gemm& p, Sum sum, int x, int half, int m, int t, int j) {
+    auto result = [&](int y) {
+        f32x4 v = sum(y) * p.alpha;
+        if (p.up) {
+            const f32x4 u = sum(y + half) * p.alpha;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = gated(v[e], u[e], p.gate);
+        }
+        return v;
+    };
+    if (p.out_type == 2) mx8_store8(p, result(x), result(x + 1), m, t, j);
+    else mx8_store16(p, result(x), m, t, j);
+}
+
+// Small m: bound by the weights' bytes.  A workgroup takes 16 MB rows and BT = NWN TN
+// weight tiles (gated: BT / 2 gate tiles, then the up tiles of the same columns), as
+// NWK groups of NWN waves; a group takes its share of K, a wave TN of the tiles.
+// Weights go straight to registers, 512 k ahead (a wave load is 1 KiB in a row).  The
+// activations of 512 k go to LDS by DMA, one buffer ahead, once for the NWN waves of a
+// group and in whole lines: read straight into fragments (64-byte pieces of 16
+// rows) they cost 1.4 times a weight tile's load, and 16 x 57344 x 8192 took 46 us
+// instead of 41.  The columns of a row (16 bytes) are XOR-swizzled by row: fragment
+// reads without bank conflicts.  The groups' sums meet in LDS, in their order.
+template <int MB, int TN, int NWN, int NWK>
+__global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
+    constexpr int BM = 16 * MB, BT = NWN * TN;
+    constexpr int kBuf = BM * 512 + BM * 16;            // codes and scales of a group of 512 k
+    constexpr int kStage = BM * 32 / (64 * NWN);        // 16-byte code pieces a lane brings per group
+    static_assert(kStage >= 1 && kStage * 64 * NWN == BM * 32, "whole pieces");
+    constexpr int kSums = NWK * BT * MB * 1024;
+    constexpr int kLds = 2 * NWK * kBuf > kSums ? 2 * NWK * kBuf : kSums;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = blockIdx.y * 16 * MB;
-    const int tiles = p.up ? TN / 2 : TN;  // output tiles of the workgroup
-    const int t0 = blockIdx.x * tiles;
-    const int c0 = (int)((int64_t)p.chunks * wave / NWK), c1 = (int)((int64_t)p.chunks * (wave + 1) / NWK);
+    const int wn = wave % NWN, kw = wave / NWN;
+    const int half = p.up ? BT / 2 : BT;
+    const int m0 = blockIdx.y * BM, t0 = blockIdx.x * half;
+    const int Q = (p.chunks + 3) / 4, per = (Q + NWK - 1) / NWK;
+    const int q0 = min(kw * per, Q), q1 = min(q0 + per, Q);   // every K group makes `per` turns
 
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a, (uint32_t)p.M * (uint32_t)p.KA);
     const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.as, (uint32_t)p.M * (uint32_t)(p.KA / 32));
     __amdgpu_buffer_rsrc_t rw[TN], rs[TN];
 #pragma unroll
     for (int tt = 0; tt < TN; ++tt) {
-        int t = t0 + tt;
-        if (p.up) t = tt < TN / 2 ? min(t, p.up - 1) : p.up + t0 + tt - TN / 2;
+        const int y = wn * TN + tt;                     // weight tile of the workgroup: [gate | up]
+        int t = t0 + y;
+        if (p.up) t = y < BT / 2 ? min(t, p.up - 1) : p.up + t0 + y - BT / 2;
         t = min(t, p.NT - 1);
         rw[tt] = make_rsrc(p.wq + (size_t)t * p.KB * 1024, (uint32_t)p.KB * 1024u);
         rs[tt] = make_rsrc(p.sq + (size_t)t * p.KB * 64, (uint32_t)p.KB * 64u);
     }
-    uint32_t aoff[MB], soff[MB];
+    uint8_t* mine = lds + kw * 2 * kBuf;
+    // piece n of a group: row n / 32, physical column n % 32 = column ^ (row % 8)
+    uint32_t aoff[kStage];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        aoff[mb] = (uint32_t)(m0 + mb * 16 + r) * (uint32_t)p.KA + 16 * j;
-        soff[mb] = (uint32_t)(m0 + mb * 16 + r) * (uint32_t)(p.KA / 32);
+    for (int i = 0; i < kStage; ++i) {
+        const int n = (i * NWN + wn) * 64 + lane, row = n >> 5, col = (n & 31) ^ (row & 7);
+        aoff[i] = (uint32_t)(m0 + row) * (uint32_t)p.KA + col * 16;
     }
-    u32x4 w[PD][TN], alo[PD][MB], ahi[PD][MB];
-    uint32_t ws[PD][TN], as[PD][MB];
-    auto issue = [&](int s, int c) {
+    const uint32_t soff = (uint32_t)(m0 + lane) * (uint32_t)(p.KA / 32);
+    auto a_dma = [&](int q, int buf) {
+        q = max(min(q, q1 - 1), 0);
 #pragma unroll
-        for (int tt = 0; tt < TN; ++tt) {
-            w[s][tt] = __builtin_amdgcn_raw_buffer_load_b128(rw[tt], lane * 16, c * 1024, kLoadStream);
-            ws[s][tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, (c >> 2) * 256, kLoadReused);
-        }
+        for (int i = 0; i < kStage; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (__attribute__((address_space(3))) void*)(mine + buf * kBuf + (i * NWN + wn) * 1024), 16,
+                (int)(aoff[i] + (uint32_t)q * 512), 0, 0, 0);
+        if (wn == 0 && lane < BM)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsa, (__attribute__((address_space(3))) void*)(mine + buf * kBuf + BM * 512), 16,
+                (int)(soff + (uint32_t)q * 16), 0, 0, 0);
+    };
+    u32x4 w[4][TN];
+    uint32_t sc[2][TN];
+    auto w_issue = [&](auto t_c, int q) {
+        constexpr int T = decltype(t_c)::value;
+        const int c = max(min(4 * q + T, 4 * q1 - 1), 0);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            alo[s][mb] = __builtin_amdgcn_raw_buffer_load_b128(ra, aoff[mb] + c * 128, 0, kLoadReused);
-            ahi[s][mb] = __builtin_amdgcn_raw_buffer_load_b128(ra, aoff[mb] + c * 128 + 64, 0, kLoadReused);
-            as[s][mb] = __builtin_amdgcn_raw_buffer_load_b32(rsa, soff[mb] + c * 4, 0, kLoadReused);
-        }
+        for (int tt = 0; tt < TN; ++tt)
+            w[T][tt] = __builtin_amdgcn_raw_buffer_load_b128(rw[tt], lane * 16, c * 1024, kLoadStream);
+    };
+    auto s_issue = [&](int q, uint32_t (&s)[TN]) {
+#pragma unroll
+        for (int tt = 0; tt < TN; ++tt)
+            s[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, max(min(q, q1 - 1), 0) * 256, kLoadStream);
     };
     f32x4 acc[TN][MB];
 #pragma unroll
     for (int tt = 0; tt < TN; ++tt)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) acc[tt][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto compute = [&](int s, int c) {
-        const int shift = 8 * (c & 3);
+    const int frow = r * 512;
+    auto compute = [&](auto t_c, int buf, const uint32_t (&s)[TN]) {
+        constexpr int T = decltype(t_c)::value;
+        const uint8_t* b = mine + buf * kBuf;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            const i32x8 a = fp8_operand(alo[s][mb], ahi[s][mb]);
-            const uint32_t sc = as[s][mb] >> (8 * j);
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + j) ^ (r & 7)) << 4));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + 4 + j) ^ (r & 7)) << 4));
+            const uint32_t as = b[BM * 512 + (mb * 16 + r) * 16 + T * 4 + j];
+            const i32x8 a = fp8_operand(lo, hi);
 #pragma unroll
             for (int tt = 0; tt < TN; ++tt)
-                acc[tt][mb] = mfma_fp4_fp8(fp4_operand(w[s][tt]), a, acc[tt][mb], ws[s][tt] >> shift, sc);
+                acc[tt][mb] = mfma_fp4_fp8<T>(w[T][tt], a, acc[tt][mb], s[tt], as);
         }
     };
-#pragma unroll
-    for (int s = 0; s < PD; ++s)
-        if (c0 + s < c1) issue(s, c0 + s);
-    int c = c0;
-    for (; c + 2 * PD <= c1; c += PD) {
-#pragma unroll
-        for (int s = 0; s < PD; ++s) {
-            compute(s, c + s);
-            issue(s, c + s + PD);
-        }
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    a_dma(q0, 0);
+    s_issue(q0, sc[0]);
+    w_issue(I0{}, q0);
+    w_issue(I1{}, q0);
+    w_issue(I2{}, q0);
+    w_issue(I3{}, q0);
+    auto turn = [&](int i, const uint32_t (&cur)[TN], uint32_t (&nxt)[TN]) {
+        const int q = q0 + i;
+        // the DMA of this group is complete: after it came its weights alone
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * TN) : "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        a_dma(q + 1, (i + 1) & 1);
+        s_issue(q + 1, nxt);
+        auto one = [&](auto t_c) {
+            constexpr int T = decltype(t_c)::value;
+            if (4 * q + T < min(p.chunks, 4 * q1)) compute(t_c, i & 1, cur);
+            w_issue(t_c, q + 1);
+        };
+        one(I0{});
+        one(I1{});
+        one(I2{});
+        one(I3{});
+    };
+    int i = 0;
+    for (; i + 1 < per; i += 2) {
+        turn(i, sc[0], sc[1]);
+        turn(i + 1, sc[1], sc[0]);
     }
-#pragma unroll
-    for (int s = 0; s < 2 * PD - 1; ++s) {
-        if (c + s < c1) compute(s % PD, c + s);
-        if (c + s + PD < c1 && s < PD) issue(s % PD, c + s + PD);
-    }
-
-    // the waves' sums
+    if (i < per) turn(i, sc[0], sc[1]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
     for (int tt = 0; tt < TN; ++tt)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) lds[((wave * TN + tt) * MB + mb) * 64 + lane] = acc[tt][mb];
+        for (int mb = 0; mb < MB; ++mb) sums[((kw * BT + wn * TN + tt) * MB + mb) * 64 + lane] = acc[tt][mb];
     __syncthreads();
-    auto total = [&](int tt, int mb) {
-        f32x4 v = lds[(tt * MB + mb) * 64 + lane];
+    const int unit = p.out_type == 2 ? 2 : 1, items = half / unit * MB;
+    for (int it = wave; it < items; it += NWN * NWK) {
+        const int y0 = it / MB * unit, mb = it % MB;
+        auto sum = [&](int y) {
+            f32x4 v = sums[(y * MB + mb) * 64 + lane];
 #pragma unroll
-        for (int k = 1; k < NWK; ++k) v += lds[((k * TN + tt) * MB + mb) * 64 + lane];
-        return v * p.alpha;
+            for (int k = 1; k < NWK; ++k) v += sums[((k * BT + y) * MB + mb) * 64 + lane];
+            return v;
+        };
+        mx8_finish(p, sum, y0, BT / 2, m0 + mb * 16 + r, t0 + y0, j);
+    }
+}
+
+// Larger m: a workgroup of WM x WN waves takes BM = 16 WM MBW rows and WN TNW
+// weight tiles (gated: a wave's first TNW / 2 are gate tiles, the others the up
+// tiles of the same columns), over groups of 512 k [ks Q / S, (ks + 1) Q / S).
+// A goes to LDS by DMA, three chunks of 128 k in rotation, the 16-byte columns of a
+// row XOR-swizzled by row / 2 (conflict-free fragment reads); its scales, 16 bytes a
+// row and group, one group ahead in two buffers.  Weights go straight to registers,
+// two chunks ahead.  Per chunk c: the fragments of each 16 rows are read one step
+// ahead of their products; before the last products: wait for this wave's DMA of
+// chunk c + 1, barrier (every wave has read chunk c, and chunk c + 1 is whole), DMA of
+// chunk c + 3 into c's buffer.
+// S > 1: FP32 partial sums in fragment order to P, for reduce_mx8.
+template <int WM, int WN, int MBW, int TNW>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4* __restrict__ P, int S) {
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int BM = WM * MBW * 16;
+    constexpr int kBuf = BM * 128;
+    constexpr int kStage = BM * 8 / kThreads;  // 16-byte pieces a thread brings per chunk
+    static_assert(kStage * kThreads == BM * 8 && BM % 64 == 0 && BM <= kThreads, "whole pieces, whole waves");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuf + 2 * BM * 16];
+    constexpr int kScales = 3 * kBuf;
+
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, j = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    // work item: K share innermost, then m tiles, then weight tiles, in one band
+    // for each XCD: the workgroups of an XCD share weights and rows in its L2
+    const int out_tiles = p.out_type == 2 ? p.cols_pad / 16 : (p.cols + 15) / 16;
+    const int half = p.up ? TNW / 2 : TNW;         // output tiles of a wave
+    const int MT = (p.M + BM - 1) / BM, NG = (out_tiles + WN * half - 1) / (WN * half);
+    const int total = MT * NG * S, xcd = blockIdx.x % kXcdCount, each = total / kXcdCount, more = total % kXcdCount;
+    const int item = xcd * each + min(xcd, more) + blockIdx.x / kXcdCount;
+    const int ks = item % S, mt = item / S % MT, ng = item / S / MT;
+    const int m0 = mt * BM, t0 = (ng * WN + wn) * half;
+    const int Q = (p.chunks + 3) / 4;
+    const int q0 = (int)((int64_t)Q * ks / S), q1 = (int)((int64_t)Q * (ks + 1) / S);
+    const int clast = min(4 * q1, p.chunks) - 1;
+
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a, (uint32_t)p.M * (uint32_t)p.KA);
+    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.as, (uint32_t)p.M * (uint32_t)(p.KA / 32));
+    __amdgpu_buffer_rsrc_t rw[TNW], rs[TNW];
+#pragma unroll
+    for (int tt = 0; tt < TNW; ++tt) {
+        int t = t0 + tt;
+        if (p.up) t = tt < TNW / 2 ? min(t, p.up - 1) : p.up + t0 + tt - TNW / 2;
+        t = min(t, p.NT - 1);
+        rw[tt] = make_rsrc(p.wq + (size_t)t * p.KB * 1024, (uint32_t)p.KB * 1024u);
+        rs[tt] = make_rsrc(p.sq + (size_t)t * p.KB * 64, (uint32_t)p.KB * 64u);
+    }
+
+    // LDS slot n = row n / 8, physical column n % 8
+    uint32_t aoff[kStage];
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+        const int n = tid + kThreads * i, row = n >> 3, col = (n & 7) ^ ((row >> 1) & 7);
+        aoff[i] = (uint32_t)(m0 + row) * (uint32_t)p.KA + col * 16;
+    }
+    auto a_dma = [&](int c, int buf) {
+        c = min(c, clast);  // a prefetch past the range goes into a buffer nobody reads again
+#pragma unroll
+        for (int i = 0; i < kStage; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (__attribute__((address_space(3))) void*)(lds + buf + (i * kThreads + 64 * wave) * 16), 16,
+                (int)(aoff[i] + (uint32_t)c * 128), 0, 0, 0);
     };
-    auto result = [&](int tt, int mb) {
-        f32x4 v = total(tt, mb);
-        if (p.up) {
-            const f32x4 u = total(tt + TN / 2, mb);
+    // scales of group q, 16 bytes a row (behind the row's last chunk: bytes that no
+    // product takes)
+    const uint32_t soff = (uint32_t)(m0 + tid) * (uint32_t)(p.KA / 32);
+    auto s_dma = [&](int q) {
+        if (wave < BM / 64)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsa, (__attribute__((address_space(3))) void*)(lds + kScales + (q & 1) * BM * 16 + 64 * wave * 16), 16,
+                (int)(soff + (uint32_t)min(q, q1 - 1) * 16), 0, 0, 0);
+    };
+    u32x4 w[4][TNW];
+    auto w_issue = [&](auto slot_c, int c) {
+        constexpr int SL = decltype(slot_c)::value;
+        c = min(c, clast);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = gated(v[e], u[e], p.gate);
+        for (int tt = 0; tt < TNW; ++tt)
+            w[SL][tt] = __builtin_amdgcn_raw_buffer_load_b128(rw[tt], lane * 16, c * 1024, kLoadReused);
+    };
+    // no fence: it would also wait for the newest DMA
+    auto lds_barrier = [] {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    struct Frag {
+        u32x4 lo, hi;
+        uint32_t s;
+    };
+    const int frow = (wm * MBW * 16 + r) * 128, swz = (r >> 1) & 7;
+    const int flo = frow + ((j ^ swz) << 4), fhi = frow + (((4 + j) ^ swz) << 4);
+    const int fs = kScales + (wm * MBW * 16 + r) * 16 + j;
+    auto read = [&](int buf, int mb, int t, int q, Frag& f) {
+        f.lo = *reinterpret_cast<const u32x4*>(lds + buf + flo + mb * 2048);
+        f.hi = *reinterpret_cast<const u32x4*>(lds + buf + fhi + mb * 2048);
+        f.s = lds[fs + (q & 1) * BM * 16 + mb * 256 + t * 4];
+    };
+    f32x4 acc[TNW][MBW];
+#pragma unroll
+    for (int tt = 0; tt < TNW; ++tt)
+#pragma unroll
+        for (int mb = 0; mb < MBW; ++mb) acc[tt][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    int b_cur = 0, b_nxt = kBuf, b_far = 2 * kBuf;
+    Frag fa, fb;
+    uint32_t wsc[TNW], wsn[TNW];
+    // chunk c = 4 q + T; fa holds its first fragment on entry
+    auto step = [&](auto t_c, int q, const uint32_t (&sc)[TNW]) {
+        constexpr int T = decltype(t_c)::value;
+        constexpr int kYounger = T == 2 ? kStage + TNW : kStage + 2 * TNW;
+        const int c = 4 * q + T;
+        w_issue(std::integral_constant<int, (T + 2) % 4>{}, c + 2);
+        auto mma = [&](const Frag& f, int mb) {
+            const i32x8 a = fp8_operand(f.lo, f.hi);
+#pragma unroll
+            for (int tt = 0; tt < TNW; ++tt)
+                acc[tt][mb] = mfma_fp4_fp8<T>(w[T][tt], a, acc[tt][mb], sc[tt], f.s);
+        };
+#pragma unroll
+        for (int mb = 0; mb + 1 < MBW; ++mb) {
+            read(b_cur, mb + 1, T, q, mb % 2 ? fa : fb);
+            mma(mb % 2 ? fb : fa, mb);
         }
+        // Loads complete in issue order, and after the DMA of chunk c + 1 came the
+        // weights of c + 1, the DMA of c + 2 and the weights of c + 2.  (The last are
+        // deleted by the compiler at T = 2 of a last group, where nothing takes them.)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kYounger) : "memory");
+        lds_barrier();
+        a_dma(c + 3, b_cur);
+        const int b_free = b_cur;
+        b_cur = b_nxt;
+        b_nxt = b_far;
+        b_far = b_free;
+        read(b_cur, 0, (T + 1) % 4, T == 3 ? q + 1 : q, fa);
+        mma(fb, MBW - 1);
+    };
+    static_assert(MBW % 2 == 0, "fragments alternate");
+    auto group = [&](int q, const uint32_t (&cur)[TNW], uint32_t (&nxt)[TNW]) {
+#pragma unroll
+        for (int tt = 0; tt < TNW; ++tt)
+            nxt[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, min(q + 1, q1 - 1) * 256, kLoadReused);
+        s_dma(q + 1);
+        step(std::integral_constant<int, 0>{}, q, cur);
+        if (4 * q + 1 > clast) return;
+        step(std::integral_constant<int, 1>{}, q, cur);
+        if (4 * q + 2 > clast) return;
+        step(std::integral_constant<int, 2>{}, q, cur);
+        if (4 * q + 3 > clast) return;
+        step(std::integral_constant<int, 3>{}, q, cur);
+    };
+    s_dma(q0);
+#pragma unroll
+    for (int tt = 0; tt < TNW; ++tt) wsc[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, q0 * 256, kLoadReused);
+    w_issue(std::integral_constant<int, 0>{}, 4 * q0);
+    a_dma(4 * q0, 0);
+    w_issue(std::integral_constant<int, 1>{}, 4 * q0 + 1);
+    a_dma(4 * q0 + 1, kBuf);
+    a_dma(4 * q0 + 2, 2 * kBuf);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage) : "memory");
+    lds_barrier();
+    read(b_cur, 0, 0, q0, fa);
+    int q = q0;
+    for (; q + 1 < q1; q += 2) {
+        group(q, wsc, wsn);
+        group(q + 1, wsn, wsc);
+    }
+    if (q < q1) group(q, wsc, wsn);
+    // no DMA may still write this workgroup's LDS after it exits
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if (P) {
+        const int MB16 = (p.M + 15) / 16;
+#pragma unroll
+        for (int mb = 0; mb < MBW; ++mb) {
+            const int b = m0 / 16 + wm * MBW + mb;
+            if (b >= MB16) continue;
+#pragma unroll
+            for (int tt = 0; tt < TNW; ++tt) {
+                // weight tiles in the order [output tile][gate, up]
+                const int o = t0 + (p.up ? tt % (TNW / 2) : tt), ot = p.up ? 2 * out_tiles : out_tiles;
+                const int at = p.up ? 2 * o + tt / (TNW / 2) : o;
+                if (o < out_tiles) P[(((int64_t)ks * MB16 + b) * ot + at) * 64 + lane] = acc[tt][mb];
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int mb = 0; mb < MBW; ++mb) {
+        const int m = m0 + (wm * MBW + mb) * 16 + r;
+#pragma unroll
+        for (int tt = 0; tt < TNW; ++tt) {
+            if (p.out_type == 2 && tt % 2) continue;
+            if (p.up && tt >= TNW / 2) continue;
+            mx8_finish(p, [&](int y) { return acc[y < TNW ? y : 0][mb]; }, tt, TNW / 2, m, t0 + tt, j);
+        }
+    }
+}
+
+// The partial sums of S shares of K, added in the order of the shares; one wave for
+// 16 rows and one output tile (8-bit output: two).
+__global__ __launch_bounds__(256) void reduce_mx8(Mx8Gemm p, const f32x4* __restrict__ P, int S) {
+    const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;
+    const int unit = p.out_type == 2 ? 2 : 1;
+    const int out_tiles = p.out_type == 2 ? p.cols_pad / 16 : (p.cols + 15) / 16;
+    const int MB16 = (p.M + 15) / 16, ot = p.up ? 2 * out_tiles : out_tiles;
+    const int t = (blockIdx.x * 4 + threadIdx.x / 64) * unit, b = blockIdx.y;
+    if (t >= out_tiles) return;
+    const int64_t plane = (int64_t)MB16 * ot * 64;
+    auto sum = [&](int y) {  // y = tile, or gated: tile + (up ? half : 0) with half = 2
+        const int at = p.up ? 2 * (t + y % 2) + y / 2 : t + y;
+        const f32x4* src = P + ((int64_t)b * ot + at) * 64 + lane;
+        f32x4 v = src[0];
+        for (int k = 1; k < S; ++k) v += src[k * plane];
         return v;
     };
-    const int unit = p.out_type == 2 ? 2 : 1, items = tiles / unit * MB;
-    for (int i = wave; i < items; i += NWK) {
-        const int tt = i / MB * unit, mb = i % MB, m = m0 + mb * 16 + r;
-        const f32x4 v = result(tt, mb);
-        if (unit == 1) mx8_store16(p, v, m, t0 + tt, j);
-        else mx8_store8(p, v, result(tt + 1, mb), m, t0 + tt, j);
-    }
+    mx8_finish(p, sum, 0, 2, b * 16 + r, t, j);
 }
 
 }  // namespace fp4

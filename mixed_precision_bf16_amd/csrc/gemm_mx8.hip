@@ -1,16 +1,115 @@
 // C ABI and launches of the products of 8-bit activations (gemm_mx8.h).
+#include <utility>
+
 #include "gemm_mx8.h"
 
 int fp4_check_weight_shape(int64_t N, int64_t K, int format);  // repack.cpp
 
 namespace fp4 {
 
-template <int MB, int TN, int NWK, int PD>
-static void stream_t(const Mx8Gemm& p, hipStream_t s) {
-    const int tiles = p.up ? TN / 2 : TN;
-    const int out_tiles = p.out_type == 2 ? p.cols_pad / 16 : (p.cols + 15) / 16;
-    const dim3 grid((unsigned)((out_tiles + tiles - 1) / tiles), (unsigned)((p.M + 16 * MB - 1) / (16 * MB)));
-    gemm_mx8_stream<MB, TN, NWK, PD><<<grid, dim3(64 * NWK), (size_t)NWK * TN * MB * 1024, s>>>(p);
+static int64_t out_tiles_of(int64_t cols, int out_type) {
+    return out_type == 2 ? mx8_padded(cols) / 16 : (cols + 15) / 16;
+}
+
+// Kernels of a product, in the order of Mx8Plan::shape: small m (16 mb rows, nwn x tn
+// weight tiles, nwk shares of K a workgroup) and larger m (wm x wn waves of 16 mbw
+// rows by 64 weight rows).
+struct DecodeMx8 {
+    int mb, tn, nwn, nwk;
+};
+constexpr int kCus = 256;  // compute units of an MI355X
+constexpr DecodeMx8 kDecode[] = {{1, 1, 1, 4}, {1, 2, 1, 4}, {1, 3, 1, 4}, {1, 2, 2, 2}, {1, 2, 4, 1}, {2, 1, 1, 4},
+                                 {2, 2, 1, 4}, {2, 3, 1, 4}, {2, 2, 2, 2}, {2, 2, 4, 1}, {4, 2, 2, 2}, {4, 2, 4, 1}};
+constexpr int kDecodes = sizeof(kDecode) / sizeof(kDecode[0]);
+struct TiledMx8 {
+    int wm, wn, mbw;
+    double alone_us, share_us;  // 128 k of a tile: one tile a compute unit; each of several
+};
+constexpr TiledMx8 kTiled[] = {{1, 4, 4, 0.55, 0.48}, {2, 4, 4, 0.82, 0.80}, {2, 4, 8, 1.50, 1.48}};
+constexpr int kTiles = sizeof(kTiled) / sizeof(kTiled[0]);
+
+struct Mx8Plan {
+    int shape, S;
+    size_t workspace;
+};
+
+// The kernel and split with the least modelled time (us).  Measured on MI355X, N x K of
+// 57344 x 8192, 10240 x 8192, 8192 x 28672, 8192 x 8192, 4096 x 14336, 5760 x 2880 and
+// 1024 x 8192, m = 1 .. 2048, all shapes forced: the choice is within 10 % of the best.
+//   Small m: launch and first loads 3.5, then 128 k of a workgroup's tiles cost 0.03 a
+//   tile (the weights of all 256 compute units arrive at 6.2 TB/s) and 0.02 + 0.015 for
+//   16 rows of activations.  16 x 10240 x 8192 takes 11.3 us with 3 tiles a workgroup (214
+//   workgroups), 14.2 with 2 (320: two rounds), 13.1 with 4 and 16.2 with 8; 16 x 57344
+//   x 8192 47, 43 and 41 us with 2, 4 and 8.
+//   Larger m: 3.0, then the tile's time; a split of K adds its partial sums' round trip
+//   through the caches at 8 TB/s and the second launch, 4.0.  256 x 8192 x 28672: 59 us
+//   as 128 x 256 tiles split four ways, 118 unsplit; 2048 x 57344 x 8192: 663 us as 256 x
+//   256, 752 as 128 x 256, 791 as 64 x 256 tiles.
+static Mx8Plan mx8_plan(int64_t m, int64_t N, int64_t K, int out_type, int gate) {
+    const int64_t out = out_tiles_of(gate ? N / 2 : N, out_type), chunks = mx8_padded(K) / kChunkK;
+    const double bytes = (double)N * (double)K * 0.53125;
+    Mx8Plan best{0, 1, 0};
+    double best_us = 1e30;
+    auto offer = [&](int shape, int S, double us) {
+        if (us < best_us) {
+            best_us = us;
+            best = Mx8Plan{shape, S, 0};
+        }
+    };
+    for (int i = 0; i < kDecodes && m <= 64; ++i) {
+        const DecodeMx8& d = kDecode[i];
+        const int tiles = d.tn * d.nwn, cols = gate ? tiles / 2 : tiles;
+        if (d.mb != (m <= 16 ? 1 : m <= 32 ? 2 : 4) || (gate && tiles % 2) || (out_type == 2 && cols % 2)) continue;
+        const int64_t groups = (out + cols - 1) / cols, rounds = (groups + kCus - 1) / kCus;
+        offer(i, 1, 3.5 + std::max((double)(rounds * chunks) * (0.02 + 0.015 * d.mb + 0.03 * tiles),
+                                   bytes / 6.2e6 * (1.0 + 0.3 / tiles)));
+    }
+    for (int i = 0; i < kTiles && m > 16; ++i) {
+        const TiledMx8& t = kTiled[i];
+        const int64_t cols = t.wn * (gate ? 2 : 4), rows = 16 * t.wm * t.mbw;
+        const int64_t tiles = ((out + cols - 1) / cols) * ((m + rows - 1) / rows), groups = (chunks + 3) / 4;
+        for (int S : {1, 2, 3, 4, 6, 8}) {
+            if (S > groups) break;
+            const int64_t rounds = (tiles * S + kCus - 1) / kCus, each = 4 * ((groups + S - 1) / S);
+            double us = 3.0 + std::max((double)each * (rounds == 1 ? t.alone_us : (double)rounds * t.share_us), bytes / 5.2e6);
+            if (S > 1) us += 4.0 + (double)S * (double)m * (double)N * 8.0 / 8e6;
+            offer(kDecodes + i, S, us);
+        }
+    }
+    if (best.S > 1)
+        best.workspace = (size_t)best.S * (size_t)((m + 15) / 16) * (size_t)out * (gate ? 2 : 1) * 1024;
+    return best;
+}
+
+template <int I>
+static void decode_t(const Mx8Gemm& p, hipStream_t s) {
+    constexpr DecodeMx8 d = kDecode[I];
+    const int64_t tiles = d.tn * d.nwn / (p.up ? 2 : 1), out = out_tiles_of(p.cols, p.out_type);
+    const dim3 grid((unsigned)((out + tiles - 1) / tiles), (unsigned)((p.M + 16 * d.mb - 1) / (16 * d.mb)));
+    gemm_mx8_decode<d.mb, d.tn, d.nwn, d.nwk><<<grid, dim3(64 * d.nwn * d.nwk), 0, s>>>(p);
+}
+
+template <int I>
+static void tiled_t(const Mx8Gemm& p, int S, void* workspace, hipStream_t s) {
+    constexpr TiledMx8 t = kTiled[I];
+    constexpr int TNW = 4, BM = 16 * t.wm * t.mbw;
+    const int64_t tiles = t.wn * TNW / (p.up ? 2 : 1), out = out_tiles_of(p.cols, p.out_type);
+    const int64_t groups = (out + tiles - 1) / tiles, rows = (p.M + BM - 1) / BM;
+    f32x4* P = S > 1 ? static_cast<f32x4*>(workspace) : nullptr;
+    gemm_mx8_tiled<t.wm, t.wn, t.mbw, TNW><<<dim3((unsigned)(groups * rows * S)), dim3(64 * t.wm * t.wn), 0, s>>>(p, P, S);
+    if (P) {
+        const int64_t units = out / (p.out_type == 2 ? 2 : 1);
+        reduce_mx8<<<dim3((unsigned)((units + 3) / 4), (unsigned)((p.M + 15) / 16)), dim3(256), 0, s>>>(p, P, S);
+    }
+}
+
+template <int... I>
+static void launch_decode(int shape, const Mx8Gemm& p, hipStream_t s, std::integer_sequence<int, I...>) {
+    (void)((shape == I && (decode_t<I>(p, s), true)) || ...);
+}
+template <int... I>
+static void launch_tiled(int shape, const Mx8Gemm& p, int S, void* ws, hipStream_t s, std::integer_sequence<int, I...>) {
+    (void)((shape == I && (tiled_t<I>(p, S, ws, s), true)) || ...);
 }
 
 static int gemm_mx8_check(int64_t m, int64_t N, int64_t K, int out_type, int gate) {
@@ -38,6 +137,10 @@ static int gemm_mx8_impl(const fp4_gemm_mx8_args* q, void* stream) {
          reinterpret_cast<uintptr_t>(q->sq) | reinterpret_cast<uintptr_t>(q->out)) & 15 ||
         (reinterpret_cast<uintptr_t>(q->scales) | reinterpret_cast<uintptr_t>(q->out_scales)) & 3)
         return FP4_ERR_SHAPE;
+    const Mx8Plan plan = mx8_plan(q->m, q->N, q->K, q->out_type, q->gate);
+    if (plan.workspace && (!q->workspace || q->workspace_bytes < plan.workspace ||
+                           (reinterpret_cast<uintptr_t>(q->workspace) & 255)))
+        return FP4_ERR_WORKSPACE;
     st = check_device();
     if (st != FP4_OK) return st;
     Mx8Gemm p{};
@@ -61,9 +164,10 @@ static int gemm_mx8_impl(const fp4_gemm_mx8_args* q, void* stream) {
     p.alpha = q->alpha;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    if (p.M <= 16) stream_t<1, 4, 8, 2>(p, s);
-    else if (p.M <= 32) stream_t<2, 4, 8, 2>(p, s);
-    else stream_t<4, 4, 4, 2>(p, s);
+    if (plan.shape < kDecodes)
+        launch_decode(plan.shape, p, s, std::make_integer_sequence<int, kDecodes>{});
+    else
+        launch_tiled(plan.shape - kDecodes, p, plan.S, q->workspace, s, std::make_integer_sequence<int, kTiles>{});
     return launch_status();
 }
 
@@ -73,7 +177,7 @@ extern "C" int fp4_gemm_mx8_workspace_size(int64_t m, int64_t N, int64_t K, int 
     int st = fp4::gemm_mx8_check(m, N, K, out_type, gate);
     if (st != FP4_OK) return st;
     if (!bytes) return FP4_ERR_NULL;
-    *bytes = 0;
+    *bytes = m == 0 ? 0 : fp4::mx8_plan(m, N, K, out_type, gate).workspace;
     return FP4_OK;
 }
 
