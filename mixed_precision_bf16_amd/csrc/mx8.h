@@ -48,6 +48,11 @@ __device__ __forceinline__ float mx8_amax(const float (&x)[8]) {
     return a;
 }
 
+// Eight 16-bit elements that are read once: the nontemporal hint.
+__device__ __forceinline__ u32x4 load_once(const uint16_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
 // Two 16-bit elements to FP32.
 template <int ACT>
 __device__ __forceinline__ void widen2(uint32_t p, float& lo, float& hi) {
