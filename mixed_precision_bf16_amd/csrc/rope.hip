@@ -9,6 +9,12 @@ int kv_check(const fp4_kv_cache* c, KvArgs* a);                                 
 bool rows_ok(const void* p, int64_t ts, int64_t hs);
 bool rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs);
 
+// Tokens of a workgroup (whole quads: the value codes of four tokens are neighbours),
+// and its shares of the heads: enough workgroups for the GPU, each with 256 items at
+// least.  8191 tokens of 64 + 8 heads of 128: 65.6 us with 4 tokens, 70 with 8, 73 with 16;
+// with 4 tokens and twice the workgroups 71 us.
+constexpr int kRopeTile = 4;
+
 struct RopeArgs {
     const int64_t* positions;
     const float* frequencies;
@@ -106,11 +112,18 @@ __device__ __forceinline__ int rope_items(int head_dim, int rotary) {
     return rotary / 2 + (head_dim - rotary);
 }
 
-template <int ACT, int KIND>
+// kFar: outputs too large for the caches go past them.
+template <bool kFar>
+__device__ __forceinline__ void store16(uint16_t* p, const u32x4& v) {
+    if constexpr (kFar) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+    else *reinterpret_cast<u32x4*>(p) = v;
+}
+
+template <int ACT, int KIND, bool kFar>
 __device__ __forceinline__ void rope_item(const uint16_t* x, uint16_t* y, int p, const RopeArgs& r,
                                           const f32x2* cs) {
     if constexpr (KIND == kPairs) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(x + 8 * p);
+        u32x4 v = load_once(x + 8 * p);
         if (8 * p < r.rotary) {
             float f[8];
             widen8<ACT>(v, f);
@@ -121,20 +134,20 @@ __device__ __forceinline__ void rope_item(const uint16_t* x, uint16_t* y, int p,
                     v[i] = pack_out<ACT>(f[2 * i], f[2 * i + 1]);
                 }
         }
-        *reinterpret_cast<u32x4*>(y + 8 * p) = v;
+        store16<kFar>(y + 8 * p, v);
     } else if constexpr (KIND == kHalves) {
         const int n = r.pairs / 8;
         if (p < n) {
             float a[8], b[8];
-            widen8<ACT>(*reinterpret_cast<const u32x4*>(x + 8 * p), a);
-            widen8<ACT>(*reinterpret_cast<const u32x4*>(x + r.pairs + 8 * p), b);
+            widen8<ACT>(load_once(x + 8 * p), a);
+            widen8<ACT>(load_once(x + r.pairs + 8 * p), b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) rotate(a[i], b[i], cs[8 * p + i], a[i], b[i]);
-            *reinterpret_cast<u32x4*>(y + 8 * p) = narrow8<ACT>(a);
-            *reinterpret_cast<u32x4*>(y + r.pairs + 8 * p) = narrow8<ACT>(b);
+            store16<kFar>(y + 8 * p, narrow8<ACT>(a));
+            store16<kFar>(y + r.pairs + 8 * p, narrow8<ACT>(b));
         } else {
             const int d = r.rotary + 8 * (p - n);
-            *reinterpret_cast<u32x4*>(y + d) = *reinterpret_cast<const u32x4*>(x + d);
+            store16<kFar>(y + d, load_once(x + d));
         }
     } else {
         if (p < r.pairs) {
@@ -148,120 +161,137 @@ __device__ __forceinline__ void rope_item(const uint16_t* x, uint16_t* y, int p,
     }
 }
 
-// Heads [h0, h1) of `tokens` tokens.
-template <int ACT, int KIND>
+// Heads [h0, h1) of `tokens` tokens: a thread keeps its item of a head and goes
+// through the heads of all tokens.
+template <int ACT, int KIND, bool kFar>
 __device__ __forceinline__ void rope_heads(const Rows& x, const RowsOut& y, int head_dim, int token0, int tokens,
                                            int h0, int h1, const RopeArgs& r, const f32x2* table) {
-    const uint32_t per = (uint32_t)rope_items<KIND>(head_dim, r.rotary), heads = (uint32_t)(h1 - h0);
-    for (uint32_t i = threadIdx.x; i < tokens * heads * per; i += 256) {
-        const uint32_t th = i / per, t = th / heads;
-        const int h = h0 + (int)(th - t * heads), p = (int)(i - th * per);
-        rope_item<ACT, KIND>(x.p + (token0 + t) * x.ts + h * x.hs, y.p + (token0 + t) * y.ts + h * y.hs, p, r,
-                             table + t * r.pairs);
+    const int per = rope_items<KIND>(head_dim, r.rotary), heads = h1 - h0;
+    const int side = min(per, 256), step = 256 / side;  // threads on a head, heads at a time
+    if ((int)threadIdx.x >= side * step) return;
+    const int row = threadIdx.x / side;
+    int t = row / heads, h = row - t * heads;
+    while (t < tokens) {
+        for (int p = threadIdx.x - row * side; p < per; p += side)
+            rope_item<ACT, KIND, kFar>(x.p + (token0 + t) * x.ts + (h0 + h) * x.hs,
+                                       y.p + (token0 + t) * y.ts + (h0 + h) * y.hs, p, r, table + t * r.pairs);
+        for (h += step; h >= heads; h -= heads) ++t;
     }
 }
 
-// Elements d .. d + 7 of a rotated key row, rounded to the row's type: what
+// What turns the block of G elements from d0 on of one token's keys: element e
+// becomes own c[e] + other s[e], other being its pair's other element and s signed
+// (a - b s and a + b (-s) round alike).
+template <int G, int KIND>
+struct BlockTurn {
+    float c[G], s[G];
+    __device__ __forceinline__ void load(const RopeArgs& r, const f32x2* cs, int d0) {
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+            const int d = d0 + e;
+            const bool first = KIND == kPairs ? d % 2 == 0 : d < r.pairs;
+            const f32x2 v = cs[min(KIND == kPairs ? d / 2 : first ? d : d - r.pairs, r.pairs - 1)];
+            c[e] = v.x;
+            s[e] = first ? -v.y : v.y;
+        }
+    }
+};
+
+// Elements d0 .. d0 + G - 1 of a key row, turned and rounded to the row's type: what
 // rope_item writes.
-template <int ACT, int KIND>
-__device__ __forceinline__ void rope_eight(const uint16_t* x, int d, const RopeArgs& r, const f32x2* cs,
-                                           float (&f)[8]) {
-    const u32x4 own = *reinterpret_cast<const u32x4*>(x + d);
-    widen8<ACT>(own, f);
-    if (d >= r.rotary) return;
-    if constexpr (KIND == kPairs) {
+template <int ACT, int KIND, int G>
+__device__ __forceinline__ void turned_block(const uint16_t* x, int d0, const RopeArgs& r, const BlockTurn<G, KIND>& turn,
+                                             float (&out)[G]) {
+#pragma clang fp contract(off)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (d / 2 + i < r.pairs) rotate(f[2 * i], f[2 * i + 1], cs[d / 2 + i], f[2 * i], f[2 * i + 1]);
-    } else if constexpr (KIND == kHalves) {
-        const bool first = d < r.pairs;
-        const int other = first ? d + r.pairs : d - r.pairs, p = first ? d : other;
-        float g[8];
-        widen8<ACT>(*reinterpret_cast<const u32x4*>(x + other), g);
+    for (int w = 0; w < G; w += 8) {
+        const int d = d0 + w;
+        float own[8], other[8];
+        widen8<ACT>(*reinterpret_cast<const u32x4*>(x + d), own);
+        if constexpr (KIND == kHalves) {
+            if (d < r.rotary)
+                widen8<ACT>(*reinterpret_cast<const u32x4*>(d < r.pairs ? x + d + r.pairs : x + d - r.pairs), other);
+        } else if constexpr (KIND == kPairs) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (d + i < r.rotary) other[i] = widen1<ACT>(d + i < r.pairs ? x[d + i + r.pairs] : x[d + i - r.pairs]);
+        }
+        float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float u, v;
-            rotate(first ? f[i] : g[i], first ? g[i] : f[i], cs[p + i], u, v);
-            f[i] = first ? u : v;
+            const float oc = own[i] * turn.c[w + i], ts = other[i] * turn.s[w + i];
+            y[i] = d + i < r.rotary ? oc + ts : own[i];
         }
-    } else {
+        widen8<ACT>(narrow8<ACT>(y), y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = d + i;
-            if (e < r.rotary) {
-                const bool first = e < r.pairs;
-                const int p = first ? e : e - r.pairs;
-                float u, v;
-                rotate(widen1<ACT>(x[p]), widen1<ACT>(x[p + r.pairs]), cs[p], u, v);
-                f[i] = first ? u : v;
-            }
-        }
+        for (int i = 0; i < 8; ++i) out[w + i] = y[i];
     }
-    widen8<ACT>(narrow8<ACT>(f), f);
 }
 
-// A workgroup takes `tile` tokens and the heads of its share (blockIdx.y).
-template <int ACT, int KIND>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs r, Rows x, RowsOut y, int tokens, int tile, int heads,
+// A workgroup takes kRopeTile tokens and the heads of its share (blockIdx.y).
+template <int ACT, int KIND, bool kFar>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs r, Rows x, RowsOut y, int tokens, int heads,
                                                    int head_dim) {
     extern __shared__ f32x2 table[];
-    const int token0 = blockIdx.x * tile, n = min(tile, tokens - token0);
+    const int token0 = blockIdx.x * kRopeTile, n = min(kRopeTile, tokens - token0);
     rope_table(r, token0, n, table);
     __syncthreads();
     const int h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y);
     const int h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
-    rope_heads<ACT, KIND>(x, y, head_dim, token0, n, h0, h1, r, table);
+    rope_heads<ACT, KIND, kFar>(x, y, head_dim, token0, n, h0, h1, r, table);
 }
 
-// One block of G elements of one token and head, keys rotated first, quantized
-// and scattered as kv_append does.
-template <int FMT, int ACT, int D, int KIND>
-__device__ __forceinline__ void append_block(const KvArgs& c, const RopeArgs& r, const Rows& x, bool is_v, int token,
-                                             int64_t slot, int h, int g, const f32x2* cs) {
-    constexpr int G = KvTile<FMT, D>::G;
-    const uint16_t* row = x.p + token * x.ts + h * x.hs;
-    float f[G];
-#pragma unroll
-    for (int w = 0; w < G / 8; ++w) {
-        float e[8];
-        if (is_v) widen8<ACT>(*reinterpret_cast<const u32x4*>(row + g * G + 8 * w), e);
-        else rope_eight<ACT, KIND>(row, g * G + 8 * w, r, cs, e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[8 * w + i] = e[i];
-    }
-    kv_store_block<FMT, D>(c, slot, h, g, is_v, f);
-}
-
-// Shares of blockIdx.y: first the query heads' (q_parts), then the KV heads'.
-// The 4 GP threads of four tokens and one head lie together (kv_append_kernel).
-template <int FMT, int ACT, int D, int KIND>
+// Shares of blockIdx.y: first the KV heads' (kv_parts; their scattered stores take
+// longest), then the query heads'.  The 4 GP threads of four tokens and one head lie
+// together (kv_append_kernel).
+template <int FMT, int ACT, int D, int KIND, bool kFar>
 __global__ __launch_bounds__(256) void append_rope_kernel(KvArgs c, RopeArgs r, Rows q, RowsOut qo, Rows k, Rows v,
-                                                          const int64_t* __restrict__ slots, int tokens, int tile,
-                                                          int q_heads, int q_parts) {
+                                                          const int64_t* __restrict__ slots, int tokens,
+                                                          int q_heads, int kv_parts) {
     extern __shared__ f32x2 table[];
     constexpr int GP = D / KvTile<FMT, D>::G;
-    const int token0 = blockIdx.x * tile, n = min(tile, tokens - token0);
+    const int token0 = blockIdx.x * kRopeTile, n = min(kRopeTile, tokens - token0);
     rope_table(r, token0, n, table);
     __syncthreads();
     int part = blockIdx.y;
-    if (part < q_parts) {
-        const int h0 = (int)((int64_t)q_heads * part / q_parts), h1 = (int)((int64_t)q_heads * (part + 1) / q_parts);
-        rope_heads<ACT, KIND>(q, qo, D, token0, n, h0, h1, r, table);
+    if (part >= kv_parts) {
+        part -= kv_parts;
+        const int parts = gridDim.y - kv_parts;
+        const int h0 = (int)((int64_t)q_heads * part / parts), h1 = (int)((int64_t)q_heads * (part + 1) / parts);
+        rope_heads<ACT, KIND, kFar>(q, qo, D, token0, n, h0, h1, r, table);
         return;
     }
-    part -= q_parts;
-    const int parts = gridDim.y - q_parts;
-    const int b0 = (int)((int64_t)2 * c.kv_heads * part / parts), b1 = (int)((int64_t)2 * c.kv_heads * (part + 1) / parts);
-    const int per = (n + 3) / 4 * 4 * GP;
-    for (int i = threadIdx.x; i < (b1 - b0) * per; i += 256) {
-        const int hv = i / per, m = i - hv * per;  // keys of all heads, then values
-        const int t = m / (4 * GP) * 4 + m % 4, g = m / 4 % GP;
-        if (t >= n) continue;
-        const int64_t slot = slots[token0 + t];
-        if (slot < 0 || slot >= c.slots) continue;
-        const bool is_v = b0 + hv >= c.kv_heads;
-        append_block<FMT, ACT, D, KIND>(c, r, is_v ? v : k, is_v, token0 + t, slot,
-                                        is_v ? b0 + hv - c.kv_heads : b0 + hv, g, table + t * r.pairs);
+    // a thread keeps its token and block, and goes through the heads: keys, then values
+    constexpr int G = KvTile<FMT, D>::G;
+    const int b0 = 2 * c.kv_heads * part / kv_parts, b1 = 2 * c.kv_heads * (part + 1) / kv_parts;
+    const int per = (n + 3) / 4 * 4 * GP, step = 256 / per;
+    const int row = threadIdx.x / per, m = threadIdx.x - row * per;
+    const int t = m / (4 * GP) * 4 + m % 4, g = m / 4 % GP;
+    if (row >= step || t >= n) return;
+    const int64_t slot = slots[token0 + t];
+    if (slot < 0 || slot >= c.slots) return;
+    BlockTurn<G, KIND> turn;
+    turn.load(r, table + t * r.pairs, g * G);
+    for (int b = b0 + row; b < b1; b += step) {
+        const bool is_v = b >= c.kv_heads;
+        const int h = is_v ? b - c.kv_heads : b;
+        float f[G];
+        if (is_v) {
+            const uint16_t* x = v.p + (token0 + t) * v.ts + h * v.hs + g * G;
+#pragma unroll
+            for (int w = 0; w < G; w += 8) {
+                float e[8];
+                widen8<ACT>(*reinterpret_cast<const u32x4*>(x + w), e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[w + i] = e[i];
+            }
+        } else {
+            turned_block<ACT, KIND, G>(k.p + (token0 + t) * k.ts + h * k.hs, g * G, r, turn, f);
+        }
+        kv_store_block<FMT, D>(c, slot, h, g, is_v, f);
     }
 }
 
@@ -291,26 +321,27 @@ static int rope_pointers(const RopeArgs& a) {
 // Tokens a launch covers: its work-items are counted in 32 bits.
 constexpr int64_t kRopeSliceTokens = int64_t(1) << 20;
 
-// Tokens of a workgroup and shares of the heads.
-static int rope_tile(int64_t tokens) { return tokens >= 2048 ? 8 : 4; }
-
-static int rope_parts(int64_t tokens, int tile, int64_t items) {
-    // enough workgroups for the GPU, each with 256 items at least
-    const int64_t groups = (tokens + tile - 1) / tile, want = (2048 + groups - 1) / groups;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, items * tile / 256));
+static int rope_parts(int64_t tokens, int64_t items) {
+    const int64_t groups = (tokens + kRopeTile - 1) / kRopeTile, want = (2048 + groups - 1) / groups;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, items * kRopeTile / 256));
 }
+
+// Outputs above this many bytes are stored past the caches.
+constexpr int64_t kRopeFar = int64_t(64) << 20;
 
 template <int ACT>
 static void rope_t(int kind, const RopeArgs& r, const Rows& x, const RowsOut& y, int tokens, int heads, int head_dim,
                    hipStream_t s) {
-    const int tile = rope_tile(tokens);
-    const dim3 grid((unsigned)((tokens + tile - 1) / tile),
-                    (unsigned)std::min(heads, rope_parts(tokens, tile, (int64_t)heads * (head_dim / 8)))),
+    const dim3 grid((unsigned)((tokens + kRopeTile - 1) / kRopeTile),
+                    (unsigned)std::min(heads, rope_parts(tokens, (int64_t)heads * (head_dim / 8)))),
         block(256);
-    const size_t lds = (size_t)tile * r.pairs * sizeof(f32x2);
-    if (kind == kPairs) rope_kernel<ACT, kPairs><<<grid, block, lds, s>>>(r, x, y, tokens, tile, heads, head_dim);
-    else if (kind == kHalves) rope_kernel<ACT, kHalves><<<grid, block, lds, s>>>(r, x, y, tokens, tile, heads, head_dim);
-    else rope_kernel<ACT, kHalvesAny><<<grid, block, lds, s>>>(r, x, y, tokens, tile, heads, head_dim);
+    const size_t lds = (size_t)kRopeTile * r.pairs * sizeof(f32x2);
+    const bool far = (int64_t)tokens * heads * head_dim * 2 > kRopeFar;
+    if (kind == kHalvesAny) rope_kernel<ACT, kHalvesAny, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
+    else if (kind == kPairs && far) rope_kernel<ACT, kPairs, true><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
+    else if (kind == kPairs) rope_kernel<ACT, kPairs, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
+    else if (far) rope_kernel<ACT, kHalves, true><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
+    else rope_kernel<ACT, kHalves, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
 }
 
 static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens, int64_t heads,
@@ -353,23 +384,24 @@ struct AppendRope {
     int tokens, q_heads, kind;
 };
 
+template <int FMT, int ACT, int D, int KIND, bool kFar>
+static void launch_append_rope(const AppendRope& a, hipStream_t s) {
+    constexpr int GP = D / KvTile<FMT, D>::G;
+    const int qp = a.q_heads ? std::min(a.q_heads, rope_parts(a.tokens, (int64_t)a.q_heads * (D / 8))) : 0;
+    const int kp = std::min(2 * a.c.kv_heads, rope_parts(a.tokens, (int64_t)2 * a.c.kv_heads * GP));
+    const dim3 grid((unsigned)((a.tokens + kRopeTile - 1) / kRopeTile), (unsigned)(qp + kp)), block(256);
+    append_rope_kernel<FMT, ACT, D, KIND, kFar><<<grid, block, (size_t)kRopeTile * a.r.pairs * sizeof(f32x2), s>>>(
+        a.c, a.r, a.q, a.qo, a.k, a.v, a.slots, a.tokens, a.q_heads, kp);
+}
+
 template <int FMT, int ACT, int D>
 static void append_rope_t(const AppendRope& a, hipStream_t s) {
-    constexpr int GP = D / KvTile<FMT, D>::G;
-    const int tile = rope_tile(a.tokens);
-    const int qp = a.q_heads ? std::min(a.q_heads, rope_parts(a.tokens, tile, (int64_t)a.q_heads * (D / 8))) : 0;
-    const int kp = std::min(2 * a.c.kv_heads, rope_parts(a.tokens, tile, (int64_t)2 * a.c.kv_heads * GP));
-    const dim3 grid((unsigned)((a.tokens + tile - 1) / tile), (unsigned)(qp + kp)), block(256);
-    const size_t lds = (size_t)tile * a.r.pairs * sizeof(f32x2);
-    if (a.kind == kPairs)
-        append_rope_kernel<FMT, ACT, D, kPairs><<<grid, block, lds, s>>>(a.c, a.r, a.q, a.qo, a.k, a.v, a.slots,
-                                                                         a.tokens, tile, a.q_heads, qp);
-    else if (a.kind == kHalves)
-        append_rope_kernel<FMT, ACT, D, kHalves><<<grid, block, lds, s>>>(a.c, a.r, a.q, a.qo, a.k, a.v, a.slots,
-                                                                          a.tokens, tile, a.q_heads, qp);
-    else
-        append_rope_kernel<FMT, ACT, D, kHalvesAny><<<grid, block, lds, s>>>(a.c, a.r, a.q, a.qo, a.k, a.v, a.slots,
-                                                                             a.tokens, tile, a.q_heads, qp);
+    const bool far = (int64_t)a.tokens * a.q_heads * D * 2 > kRopeFar;
+    if (a.kind == kHalvesAny) launch_append_rope<FMT, ACT, D, kHalvesAny, false>(a, s);
+    else if (a.kind == kPairs && far) launch_append_rope<FMT, ACT, D, kPairs, true>(a, s);
+    else if (a.kind == kPairs) launch_append_rope<FMT, ACT, D, kPairs, false>(a, s);
+    else if (far) launch_append_rope<FMT, ACT, D, kHalves, true>(a, s);
+    else launch_append_rope<FMT, ACT, D, kHalves, false>(a, s);
 }
 
 static int append_rope_impl(const fp4_kv_cache* cache, const fp4_rope_args* rope, const fp4_append_rope_args* p,
