@@ -504,7 +504,7 @@ class _Current:
     def __enter__(self):
         return self.handle
 
-    def __exit__(self, *exc):
+    def __exit__(self, kind, value, trace):
         return None
 
 
@@ -596,11 +596,11 @@ def kv_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=No
         kh = vh = cache._head_dim
         made = []
         if k_out is None:
-            made.append(k_out := torch.empty(shape, dtype=dtype, device=dev))
+            made.append(k_out := torch.empty(*shape, dtype=dtype, device=dev))
         else:
             kt, kh = _rows(k_out, "k_out", *shape, dev)
         if v_out is None:
-            made.append(v_out := torch.empty(shape, dtype=dtype, device=dev))
+            made.append(v_out := torch.empty(*shape, dtype=dtype, device=dev))
         else:
             vt, vh = _rows(v_out, "v_out", *shape, dev)
         st = lib().fp4_kv_read(cache._ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), kt, kh, vt, vh, act, s)
@@ -753,8 +753,8 @@ def new_mx8(rows: int, K: int, device="cuda") -> MX8:
     import torch
     Kp = mx8_padded(K)
     a = MX8.__new__(MX8)
-    a.codes = torch.empty((rows, Kp), dtype=torch.float8_e4m3fn, device=device)
-    a.scales = torch.empty((rows, Kp // 32), dtype=torch.float8_e8m0fnu, device=device)
+    a.codes = torch.empty(rows, Kp, dtype=torch.float8_e4m3fn, device=device)  # sizes one by one: quicker than a tuple
+    a.scales = torch.empty(rows, Kp // 32, dtype=torch.float8_e8m0fnu, device=device)
     a.K = K
     return a
 
@@ -763,8 +763,13 @@ def _matrix(t, what: str, rows: int, width: int, dtype, device):
     """Row stride of a [rows][width] matrix with contiguous, 16-byte aligned rows."""
     if t.dtype != dtype or t.shape != (rows, width) or t.device != device:
         raise ValueError(f"{what} must be a {dtype} tensor [{rows}][{width}] on {device}")
+    return _row_stride(t, what, rows, width)
+
+
+def _row_stride(t, what: str, rows: int, width: int):
     a, b = t.stride()
-    a = a if rows > 1 else width  # the stride of a single row means nothing
+    if rows < 2:
+        a = width  # the stride of a single row means nothing
     if b != 1 or a % 8 or t.data_ptr() % 16:
         raise ValueError(f"{what} must have contiguous, 16-byte aligned rows")
     return a
@@ -817,21 +822,24 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
     sum_out are filled if given; sum_out may be x or residual, and out (16-bit)
     the other one."""
     import torch
-    act = _act_type(x.dtype, "x")
+    dtype, dev = x.dtype, x.device
+    act = _act_type(dtype, "x")
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError("x must be a CUDA matrix [rows][width]")
     rows, width = x.shape
-    dev, dtype = x.device, x.dtype
     if width < 8 or width % (32 if mx8 else 8):
         raise ValueError(f"the width must be a multiple of {32 if mx8 else 8}")
-    xs = _matrix(x, "x", rows, width, dtype, dev)
-    rs = _matrix(residual, "residual", rows, width, dtype, dev) if residual is not None else 0
-    if weight is not None:
-        _vector(weight, "weight", width, dtype, dev)
-    if sum_out is not None and residual is None:
+    xs, xp = _row_stride(x, "x", rows, width), x.data_ptr()
+    rs = rp = wp = scales = total = 0
+    if residual is not None:
+        rs, rp = _matrix(residual, "residual", rows, width, dtype, dev), residual.data_ptr()
+    elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
+    if weight is not None:
+        wp = _vector(weight, "weight", width, dtype, dev)
+    os = ss = width
     with _on_stream(dev, stream) as s:
-        made, os, scales = [], width, 0
+        made = []
         if mx8:
             if out is None:
                 out = new_mx8(rows, width, dev)
@@ -841,19 +849,17 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
             to, scales = out.codes.data_ptr(), out.scales.data_ptr()
         else:
             if out is None:
-                made.append(out := torch.empty((rows, width), dtype=dtype, device=dev))
+                made.append(out := torch.empty(rows, width, dtype=dtype, device=dev))
             else:
                 os = _matrix(out, "out", rows, width, dtype, dev)
             to = out.data_ptr()
-        ss = width
         if residual is not None:
             if sum_out is None:
-                made.append(sum_out := torch.empty((rows, width), dtype=dtype, device=dev))
+                made.append(sum_out := torch.empty(rows, width, dtype=dtype, device=dev))
             else:
                 ss = _matrix(sum_out, "sum_out", rows, width, dtype, dev)
-        args = _pack(_PACK_NORM, "rms_norm", x.data_ptr(), residual.data_ptr() if residual is not None else 0,
-                     weight.data_ptr() if weight is not None else 0, to, scales,
-                     sum_out.data_ptr() if residual is not None else 0, rows, width, xs, rs, os, ss, eps, act,
+            total = sum_out.data_ptr()
+        args = _pack(_PACK_NORM, "rms_norm", xp, rp, wp, to, scales, total, rows, width, xs, rs, os, ss, eps, act,
                      1 if mx8 else 0)
         st = lib().fp4_rms_norm(args, s)
     if st:
@@ -917,7 +923,7 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
             to, scales = out.codes.data_ptr(), out.scales.data_ptr()
         else:
             if out is None:
-                made.append(out := torch.empty((m, cols), dtype=dtype, device=dev))
+                made.append(out := torch.empty(m, cols, dtype=dtype, device=dev))
             elif out.dtype != dtype or out.shape != (m, cols) or out.device != dev or not out.is_contiguous():
                 raise ValueError(f"out must be a contiguous {dtype} tensor [{m}][{cols}] on {dev}")
             to, scales = out.data_ptr(), 0
@@ -1006,7 +1012,7 @@ def rope(x, positions, frequencies, interleaved: bool = False, amplitude: float 
     with _on_stream(dev, stream) as s:
         made = ()
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=dev)
+            out = torch.empty(tokens, heads, dim, dtype=x.dtype, device=dev)
             made = (out,)
             ot, oh = heads * dim, dim
         elif out.dtype != x.dtype:
@@ -1042,7 +1048,7 @@ def kv_append_rope(cache: KVCache, q, k, v, slots, positions, frequencies, inter
     with _on_stream(dev, stream) as s:
         made = ()
         if q_out is None:
-            q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+            q_out = torch.empty(n, heads, dim, dtype=q.dtype, device=dev)
             made = (q_out,)
             os = heads * dim, dim
         elif q_out.dtype != q.dtype:
