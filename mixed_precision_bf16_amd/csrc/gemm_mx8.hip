@@ -13,19 +13,20 @@ static int64_t out_tiles_of(int64_t cols, int out_type) {
 
 // Kernels of a product, in the order of Mx8Plan::shape: small m (16 mb rows, nwn x tn
 // weight tiles, nwk shares of K a workgroup) and larger m (wm x wn waves of 16 mbw
-// rows by 64 weight rows).
+// rows by 16 tnw weight rows).
 struct DecodeMx8 {
     int mb, tn, nwn, nwk;
 };
 constexpr int kCus = 256;  // compute units of an MI355X
-constexpr DecodeMx8 kDecode[] = {{1, 1, 1, 4}, {1, 2, 1, 4}, {1, 3, 1, 4}, {1, 2, 2, 2}, {1, 2, 4, 1}, {2, 1, 1, 4},
-                                 {2, 2, 1, 4}, {2, 3, 1, 4}, {2, 2, 2, 2}, {2, 2, 4, 1}, {4, 2, 2, 2}, {4, 2, 4, 1}};
+constexpr DecodeMx8 kDecode[] = {{1, 1, 1, 4}, {1, 2, 1, 4}, {1, 3, 1, 4}, {1, 2, 2, 2}, {1, 2, 4, 1}, {2, 1, 1, 4}, {2, 2, 1, 4},
+                                 {2, 3, 1, 4}, {2, 2, 2, 2}, {2, 2, 4, 1}, {2, 2, 8, 1}, {4, 1, 2, 2}, {4, 2, 2, 2}, {4, 2, 8, 1}};
 constexpr int kDecodes = sizeof(kDecode) / sizeof(kDecode[0]);
 struct TiledMx8 {
-    int wm, wn, mbw;
+    int wm, wn, mbw, tnw;
     double alone_us, share_us;  // 128 k of a tile: one tile a compute unit; each of several
 };
-constexpr TiledMx8 kTiled[] = {{1, 4, 4, 0.55, 0.48}, {2, 4, 4, 0.82, 0.80}, {2, 4, 8, 1.50, 1.48}};
+constexpr TiledMx8 kTiled[] = {{1, 4, 4, 2, 0.33, 0.28}, {1, 4, 4, 4, 0.55, 0.48}, {2, 4, 4, 4, 0.82, 0.80},
+                               {2, 4, 8, 4, 1.50, 1.48}};
 constexpr int kTiles = sizeof(kTiled) / sizeof(kTiled[0]);
 
 struct Mx8Plan {
@@ -33,18 +34,22 @@ struct Mx8Plan {
     size_t workspace;
 };
 
-// The kernel and split with the least modelled time (us).  Measured on MI355X, N x K of
-// 57344 x 8192, 10240 x 8192, 8192 x 28672, 8192 x 8192, 4096 x 14336, 5760 x 2880 and
-// 1024 x 8192, m = 1 .. 2048, all shapes forced: the choice is within 10 % of the best.
+// The kernel and split with the least modelled time (us).  Measured on MI355X with every
+// shape forced, N x K of 57344 x 8192, 10240 x 8192, 8192 x 28672, 8192 x 8192, 4096 x
+// 14336, 1024 x 8192, 2880 x 2880, gated 57344 x 8192, 20480 x 4096 and 5760 x 2880, m = 1,
+// 16, 24, 48, 64, 80, 160, 256, 700, 2048: the choice is 1.6 % off the best on average,
+// 18 % at most (700 x 5760 x 2880 and the narrowest below 15 us).
 //   Small m: launch and first loads 3.5, then 128 k of a workgroup's tiles cost 0.03 a
-//   tile (the weights of all 256 compute units arrive at 6.2 TB/s) and 0.02 + 0.015 for
-//   16 rows of activations.  16 x 10240 x 8192 takes 11.3 us with 3 tiles a workgroup (214
-//   workgroups), 14.2 with 2 (320: two rounds), 13.1 with 4 and 16.2 with 8; 16 x 57344
-//   x 8192 47, 43 and 41 us with 2, 4 and 8.
+//   tile (the weights of all 256 compute units arrive at 6.2 TB/s) and 0.022 for 16 rows of
+//   activations.  16 x 10240 x 8192 takes 10.7 us with 3 tiles a workgroup (214
+//   workgroups), 13.8 with 2 (320: two rounds), 11.1 with 4 and 15.6 with 8; 16 x 57344
+//   x 8192 gated 46, 43 and 40 us with 2, 4 and 8.
 //   Larger m: 3.0, then the tile's time; a split of K adds its partial sums' round trip
-//   through the caches at 8 TB/s and the second launch, 4.0.  256 x 8192 x 28672: 59 us
-//   as 128 x 256 tiles split four ways, 118 unsplit; 2048 x 57344 x 8192: 663 us as 256 x
-//   256, 752 as 128 x 256, 791 as 64 x 256 tiles.
+//   through the caches at 6 TB/s and the second launch, 4.0.  256 x 8192 x 28672: 61 us
+//   as 128 x 256 tiles split four ways, 69 as 256 x 256 split eight ways, 94 as 64 x 128
+//   unsplit; 2048 x 57344 x 8192 gated: 679 us as 256 x 256, 752 as 128 x 256, 798 as 64 x
+//   256, 1065 as 64 x 128 tiles; 256 x 8192 x 8192: 23 us as 64 x 128 tiles, 27 as 128 x 256
+//   split four ways.
 static Mx8Plan mx8_plan(int64_t m, int64_t N, int64_t K, int out_type, int gate) {
     const int64_t out = out_tiles_of(gate ? N / 2 : N, out_type), chunks = mx8_padded(K) / kChunkK;
     const double bytes = (double)N * (double)K * 0.53125;
@@ -61,18 +66,19 @@ static Mx8Plan mx8_plan(int64_t m, int64_t N, int64_t K, int out_type, int gate)
         const int tiles = d.tn * d.nwn, cols = gate ? tiles / 2 : tiles;
         if (d.mb != (m <= 16 ? 1 : m <= 32 ? 2 : 4) || (gate && tiles % 2) || (out_type == 2 && cols % 2)) continue;
         const int64_t groups = (out + cols - 1) / cols, rounds = (groups + kCus - 1) / kCus;
-        offer(i, 1, 3.5 + std::max((double)(rounds * chunks) * (0.02 + 0.015 * d.mb + 0.03 * tiles),
+        offer(i, 1, 3.5 + std::max((double)(rounds * chunks) * (0.01 + 0.022 * d.mb + 0.03 * tiles),
                                    bytes / 6.2e6 * (1.0 + 0.3 / tiles)));
     }
     for (int i = 0; i < kTiles && m > 16; ++i) {
         const TiledMx8& t = kTiled[i];
-        const int64_t cols = t.wn * (gate ? 2 : 4), rows = 16 * t.wm * t.mbw;
+        if (gate && out_type == 2 && t.tnw < 4) continue;  // a wave holds whole blocks of 32 columns
+        const int64_t cols = t.wn * t.tnw / (gate ? 2 : 1), rows = 16 * t.wm * t.mbw;
         const int64_t tiles = ((out + cols - 1) / cols) * ((m + rows - 1) / rows), groups = (chunks + 3) / 4;
         for (int S : {1, 2, 3, 4, 6, 8}) {
-            if (S > groups) break;
+            if (S > groups || (S > 1 && tiles * S > kCus)) break;  // a split fills the first round
             const int64_t rounds = (tiles * S + kCus - 1) / kCus, each = 4 * ((groups + S - 1) / S);
             double us = 3.0 + std::max((double)each * (rounds == 1 ? t.alone_us : (double)rounds * t.share_us), bytes / 5.2e6);
-            if (S > 1) us += 4.0 + (double)S * (double)m * (double)N * 8.0 / 8e6;
+            if (S > 1) us += 4.0 + (double)S * (double)m * (double)N * 8.0 / 6e6;
             offer(kDecodes + i, S, us);
         }
     }
@@ -92,14 +98,21 @@ static void decode_t(const Mx8Gemm& p, hipStream_t s) {
 template <int I>
 static void tiled_t(const Mx8Gemm& p, int S, void* workspace, hipStream_t s) {
     constexpr TiledMx8 t = kTiled[I];
-    constexpr int TNW = 4, BM = 16 * t.wm * t.mbw;
+    constexpr int TNW = t.tnw, BM = 16 * t.wm * t.mbw;
     const int64_t tiles = t.wn * TNW / (p.up ? 2 : 1), out = out_tiles_of(p.cols, p.out_type);
     const int64_t groups = (out + tiles - 1) / tiles, rows = (p.M + BM - 1) / BM;
     f32x4* P = S > 1 ? static_cast<f32x4*>(workspace) : nullptr;
     gemm_mx8_tiled<t.wm, t.wn, t.mbw, TNW><<<dim3((unsigned)(groups * rows * S)), dim3(64 * t.wm * t.wn), 0, s>>>(p, P, S);
     if (P) {
         const int64_t units = out / (p.out_type == 2 ? 2 : 1);
-        reduce_mx8<<<dim3((unsigned)((units + 3) / 4), (unsigned)((p.M + 15) / 16)), dim3(256), 0, s>>>(p, P, S);
+        const dim3 grid((unsigned)((units + 3) / 4), (unsigned)((p.M + 15) / 16));
+        switch (S) {
+            case 2: reduce_mx8<2><<<grid, dim3(256), 0, s>>>(p, P); break;
+            case 3: reduce_mx8<3><<<grid, dim3(256), 0, s>>>(p, P); break;
+            case 4: reduce_mx8<4><<<grid, dim3(256), 0, s>>>(p, P); break;
+            case 6: reduce_mx8<6><<<grid, dim3(256), 0, s>>>(p, P); break;
+            case 8: reduce_mx8<8><<<grid, dim3(256), 0, s>>>(p, P); break;
+        }
     }
 }
 
