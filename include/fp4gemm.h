@@ -476,7 +476,11 @@ typedef struct fp4_rms_norm_args {
 int fp4_rms_norm(const fp4_rms_norm_args* args, void* stream);
 
 /* Products of 8-bit activations with MXFP4 weights in the native packed layout
- * (fp4_native_repack), on the scaled matrix cores, accumulated in FP32:
+ * (fp4_native_repack), accumulated in FP32: for m <= 16 on the 16-bit matrix cores,
+ * both operands being exact in BF16 (values below 2^-126 may count as zero, those
+ * from 2^128 on overflow: no row that fp4_quantize_mx8 writes has such); for more
+ * rows on the scaled 8-bit matrix cores, which add the products of 32 k to 13 bits
+ * below the largest of them (an error of about 1e-5 of sum |a w|):
  *   gate 0:  Y = alpha * (A . dequant(W)^T), N columns
  *   gate 1:  Y = silu(alpha * G) * (alpha * U), gate 2: gelu(alpha * G) * (alpha * U)
  *            (tanh form), with G and U the products with rows 0 .. N/2 - 1 and

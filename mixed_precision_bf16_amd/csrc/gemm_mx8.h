@@ -4,12 +4,19 @@
 //   Y[m][n] = alpha * sum_k a[m][k] w[n][k]
 //   a = E4M3 code * 2^(scale - 127), one scale for 32 k; w the same with E2M1
 //
+// Up to 16 rows (bound by the weights' bytes): both operands become BF16, exactly,
+// and the 16-bit matrix cores add their products in FP32.  More rows:
 // One v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 weight rows by 16
 // activation rows over 128 k.  Operand layout (checked on the device), lane =
 // 16 j + r: row r of either operand; FP4: k = 32 j .. 32 j + 31 (the native
 // weight layout, repack.cpp); FP8: k = 16 j .. 16 j + 15 and 64 + 16 j ..
 // 64 + 16 j + 15; either scale: block j of the row's four.  The result: rows n =
-// 4 j .. 4 j + 3, column m = r.
+// 4 j .. 4 j + 3, column m = r.  With an FP8 operand this instruction aligns the products
+// of a lane group to their largest and keeps 13 bits below it (checked on the
+// device): the sums of 128 products are off by 1e-5 of sum |a w| on average (FP4 by FP4
+// and the 16-bit products: none).  For Gaussian rows of 8192 that is 1e-5 of the result's
+// size, a hundredth of a BF16 step; in 8-bit outputs it can move a code, and one
+// block's scale in 15000, that lies next to a border.
 #pragma once
 #include "mx8.h"
 
@@ -98,6 +105,16 @@ __device__ __forceinline__ void mx8_finish(const Mx8Gemm& p, Sum sum, int x, int
     else mx8_store16(p, result(x), m, t, j);
 }
 
+// Eight E4M3 codes times a power of two (the exponent of `scale`): exact BF16 values.
+__device__ __forceinline__ u32x4 bf16_of_fp8(uint32_t lo, uint32_t hi, float scale) {
+    u32x4 o;
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+    return o;
+}
+
 // Place of workgroup x of `total` in the order of work: one band for each XCD, to which
 // the workgroups are dealt in turn.
 __device__ __forceinline__ int xcd_band(int x, int total) {
@@ -114,9 +131,13 @@ __device__ __forceinline__ int xcd_band(int x, int total) {
 // rows) they cost 1.4 times a weight tile's load, and 16 x 57344 x 8192 took 46 us
 // instead of 41.  The columns of a row (16 bytes) are XOR-swizzled by row: fragment
 // reads without bank conflicts.  The groups' sums meet in LDS, in their order.
+// 16 rows: exact BF16 operands, 3 to 5 % slower than the 8-bit products (16 x 57344 x 8192
+// gated 40.5 and 42.4 us) and free of their rounding; with 32 rows the conversions cost 6
+// to 20 %, with 64 half, so those take the 8-bit products.
 template <int MB, int TN, int NWN, int NWK>
 __global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
     constexpr int BM = 16 * MB, BT = NWN * TN;
+    constexpr bool kExact = MB == 1;
     constexpr int kBuf = BM * 512 + BM * 16;            // codes and scales of a group of 512 k
     constexpr int kStage = BM * 32 / (64 * NWN);        // 16-byte code pieces a lane brings per group
     static_assert(kStage >= 1 && kStage * 64 * NWN == BM * 32, "whole pieces");
@@ -188,15 +209,28 @@ __global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
     auto compute = [&](auto t_c, int buf, const uint32_t (&s)[TN]) {
         constexpr int T = decltype(t_c)::value;
         const uint8_t* b = mine + buf * kBuf;
+        if constexpr (kExact) {
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(b + frow + (((8 * T + 2 * j) ^ (r & 7)) << 4));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(b + frow + (((8 * T + 2 * j + 1) ^ (r & 7)) << 4));
+            const float sa = __uint_as_float((uint32_t)b[BM * 512 + r * 16 + T * 4 + j] << 23);
+            const u32x4 a[4] = {bf16_of_fp8(lo.x, lo.y, sa), bf16_of_fp8(lo.z, lo.w, sa), bf16_of_fp8(hi.x, hi.y, sa),
+                                bf16_of_fp8(hi.z, hi.w, sa)};
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const u32x4 lo = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + j) ^ (r & 7)) << 4));
-            const u32x4 hi = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + 4 + j) ^ (r & 7)) << 4));
-            const uint32_t as = b[BM * 512 + (mb * 16 + r) * 16 + T * 4 + j];
-            const i32x8 a = fp8_operand(lo, hi);
+            for (int tt = 0; tt < TN; ++tt) {
+                const float sw = __uint_as_float(((s[tt] >> (8 * T)) & 0xFFu) << 23);
 #pragma unroll
-            for (int tt = 0; tt < TN; ++tt)
-                acc[tt][mb] = mfma_fp4_fp8<T>(w[T][tt], a, acc[tt][mb], s[tt], as);
+                for (int i = 0; i < 4; ++i) acc[tt][0] = mfma<0>(dequant_mxfp4(w[T][tt][i], sw), a[i], acc[tt][0]);
+            }
+        } else {
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + j) ^ (r & 7)) << 4));
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(b + mb * 8192 + frow + (((8 * T + 4 + j) ^ (r & 7)) << 4));
+                const uint32_t as = b[BM * 512 + (mb * 16 + r) * 16 + T * 4 + j];
+                const i32x8 a = fp8_operand(lo, hi);
+#pragma unroll
+                for (int tt = 0; tt < TN; ++tt) acc[tt][mb] = mfma_fp4_fp8<T>(w[T][tt], a, acc[tt][mb], s[tt], as);
+            }
         }
     };
     using I0 = std::integral_constant<int, 0>;

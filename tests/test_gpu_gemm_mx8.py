@@ -59,7 +59,8 @@ def _upload(codes, scales, N, K):
 def _expected(a, w, K, gate=None, alpha=1.0):
     """(values, bound of the FP32 result's error), float64."""
     y, total = oracle.gemm_mx8_reference(*a, *w, K, alpha)
-    err = total * (2.0 ** -9 + K / 16 * 2.0 ** -24) + np.abs(y) * 2.0 ** -23
+    group = 2.0 ** -9 + K / 16 * 2.0 ** -24
+    err = total * (min(group, K * 2.0 ** -24) if len(y) <= 16 else group) + np.abs(y) * 2.0 ** -23
     if gate is None:
         return y, err
     n = y.shape[1] // 2
@@ -159,8 +160,9 @@ def test_whole_numbers_are_exact(m):
         assert got.cpu().equal(torch.from_numpy(y).to(dtype))
 
 
-def test_nan_and_zero_rows_stay_in_their_row():
-    m, N, K = 40, 96, 512
+@pytest.mark.parametrize("m", [14, 40, 130])
+def test_nan_and_zero_rows_stay_in_their_row(m):
+    N, K = 96, 512
     a, w = _activations(m, K, 3), _weights(N, K, 4)
     a[0][5, 100] = 0x7F
     a[1][9, 3] = 0xFF
