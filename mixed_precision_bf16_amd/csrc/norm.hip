@@ -146,10 +146,10 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs a) {
 // Rows of 16-bit values to codes and scales, one vector a thread.
 template <int ACT>
 __global__ __launch_bounds__(256) void quantize_mx8_kernel(NormArgs a) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= (int64_t)a.rows * a.vecs_out) return;  // whole blocks of 32
-    const int64_t row = n / a.vecs_out;
-    const int i = (int)(n - row * a.vecs_out);
+    const uint32_t n = blockIdx.x * 256u + threadIdx.x;  // at most 2^30
+    if (n >= (uint32_t)a.rows * (uint32_t)a.vecs_out) return;  // whole blocks of 32
+    const uint32_t row = n / (uint32_t)a.vecs_out;
+    const int i = (int)(n - row * (uint32_t)a.vecs_out);
     float y[8] = {};
     if (i < a.vecs) widen8<ACT>(load_once(a.x + row * a.x_stride + i * 8), y);
 #pragma unroll

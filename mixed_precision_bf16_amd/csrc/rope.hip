@@ -206,7 +206,7 @@ __device__ __forceinline__ void turned_block(const uint16_t* x, int d0, const Ro
 #pragma unroll
     for (int w = 0; w < G; w += 8) {
         const int d = d0 + w;
-        float own[8], other[8];
+        float own[8], other[8] = {};
         widen8<ACT>(*reinterpret_cast<const u32x4*>(x + d), own);
         if constexpr (KIND == kHalves) {
             if (d < r.rotary)

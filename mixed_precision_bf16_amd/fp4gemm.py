@@ -729,33 +729,36 @@ class MX8:
     """Activations in 8 bits: `codes` (float8_e4m3fn CUDA [rows][mx8_padded(K)])
     and `scales` (float8_e8m0fnu CUDA [rows][mx8_padded(K) / 32]), contiguous; the
     value of element k is codes[i, k] * scales[i, k // 32].  What lies behind K has
-    to be zero."""
+    to be zero.  All are fixed once the object is made."""
 
-    __slots__ = ("codes", "scales", "K")
+    __slots__ = ("_codes", "_scales", "_K")
+
+    codes, scales, K = (property(operator.attrgetter(name)) for name in __slots__)
 
     def __init__(self, codes, scales, K: int):
         import torch
         if K < 32 or K % 32:
             raise ValueError("K must be a multiple of 32")
-        Kp = mx8_padded(K)
+        Kp, dev = (K + 127) // 128 * 128, codes.device
         if codes.dtype != torch.float8_e4m3fn or codes.dim() != 2 or codes.shape[1] != Kp or not codes.is_cuda:
             raise ValueError(f"codes must be a float8_e4m3fn CUDA tensor [rows][{Kp}]")
-        if (scales.dtype != torch.float8_e8m0fnu or scales.shape != (codes.shape[0], Kp // 32)
-                or scales.device != codes.device):
+        if scales.dtype != torch.float8_e8m0fnu or scales.shape != (codes.shape[0], Kp // 32) or scales.device != dev:
             raise ValueError(f"scales must be a float8_e8m0fnu tensor [rows][{Kp // 32}] on the codes' device")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous")
-        self.codes, self.scales, self.K = codes, scales, K
+        self._codes, self._scales, self._K = codes, scales, K
 
 
 def new_mx8(rows: int, K: int, device="cuda") -> MX8:
     """Uninitialized 8-bit rows, for an entry to write."""
     import torch
-    Kp = mx8_padded(K)
+    if K < 32 or K % 32:
+        raise ValueError("K must be a multiple of 32")
+    Kp = (K + 127) // 128 * 128
     a = MX8.__new__(MX8)
-    a.codes = torch.empty(rows, Kp, dtype=torch.float8_e4m3fn, device=device)  # sizes one by one: quicker than a tuple
-    a.scales = torch.empty(rows, Kp // 32, dtype=torch.float8_e8m0fnu, device=device)
-    a.K = K
+    a._codes = torch.empty(rows, Kp, dtype=torch.float8_e4m3fn, device=device)  # sizes one by one: quicker than a tuple
+    a._scales = torch.empty(rows, Kp // 32, dtype=torch.float8_e8m0fnu, device=device)
+    a._K = K
     return a
 
 
@@ -776,7 +779,7 @@ def _row_stride(t, what: str, rows: int, width: int):
 
 
 def _mx8_out(out, rows: int, K: int, device):
-    if not isinstance(out, MX8) or out.codes.shape[0] != rows or out.K != K or out.codes.device != device:
+    if not isinstance(out, MX8) or out._codes.shape[0] != rows or out._K != K or out._codes.device != device:
         raise ValueError(f"out must be an MX8 of {rows} rows of {K} on {device}")
     return out
 
@@ -801,14 +804,14 @@ def quantize_mx8(x, out: MX8 | None = None, stream=None) -> MX8:
         made = ()
         if out is None:
             out = new_mx8(rows, K, dev)
-            made = (out.codes, out.scales)
+            made = (out._codes, out._scales)
         else:
             _mx8_out(out, rows, K, dev)
-        st = lib().fp4_quantize_mx8(x.data_ptr(), rows, K, xs, act, out.codes.data_ptr(), out.scales.data_ptr(), s)
+        st = lib().fp4_quantize_mx8(x.data_ptr(), rows, K, xs, act, out._codes.data_ptr(), out._scales.data_ptr(), s)
     if st:
         _check(st, "fp4_quantize_mx8")
     if stream is not None:
-        _keep(dev, stream, (x, out.codes, out.scales), made)
+        _keep(dev, stream, (x, out._codes, out._scales), made)
     return out
 
 
@@ -843,10 +846,10 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
         if mx8:
             if out is None:
                 out = new_mx8(rows, width, dev)
-                made += (out.codes, out.scales)
+                made += (out._codes, out._scales)
             else:
                 _mx8_out(out, rows, width, dev)
-            to, scales = out.codes.data_ptr(), out.scales.data_ptr()
+            to, scales = out._codes.data_ptr(), out._scales.data_ptr()
         else:
             if out is None:
                 made.append(out := torch.empty(rows, width, dtype=dtype, device=dev))
@@ -865,7 +868,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
     if st:
         _check(st, "fp4_rms_norm")
     if stream is not None:
-        used = (x, residual, weight, sum_out) + ((out.codes, out.scales) if mx8 else (out,))
+        used = (x, residual, weight, sum_out) + ((out._codes, out._scales) if mx8 else (out,))
         _keep(dev, stream, used, made)
     return (out, sum_out) if residual is not None else out
 
@@ -895,9 +898,9 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
     tensor [m][columns] of `dtype` (bfloat16 by default, or float16) or, with
     mx8, an MX8."""
     import torch
-    if gate not in _GATES:
-        raise ValueError("gate must be None, 'silu' or 'gelu'")
-    g = _GATES[gate]
+    g = _GATES.get(gate)
+    if g is None or not isinstance(a, MX8):
+        raise ValueError("gate must be None, 'silu' or 'gelu', and a an MX8")
     if mx8:
         if dtype is not None:
             raise ValueError("dtype does not go with mx8")
@@ -906,7 +909,7 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
         if dtype is None:
             dtype = out.dtype if out is not None else torch.bfloat16
         kind = _act_type(dtype, "dtype")
-    m, K, dev = a.codes.shape[0], a.K, a.codes.device
+    m, K, dev = a._codes.shape[0], a._K, a._codes.device
     for t, n in zip((wq, sq), _native_sizes(N, K)):
         if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"wq / sq must be contiguous uint8 tensors of native_repack_size(N, K) bytes on {dev}")
@@ -917,10 +920,10 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
         if mx8:
             if out is None:
                 out = new_mx8(m, cols, dev)
-                made += (out.codes, out.scales)
+                made += (out._codes, out._scales)
             else:
                 _mx8_out(out, m, cols, dev)
-            to, scales = out.codes.data_ptr(), out.scales.data_ptr()
+            to, scales = out._codes.data_ptr(), out._scales.data_ptr()
         else:
             if out is None:
                 made.append(out := torch.empty(m, cols, dtype=dtype, device=dev))
@@ -933,13 +936,13 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
         elif not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         wp, wn = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
-        args = _pack(_PACK_MX8, "gemm_mx8", a.codes.data_ptr(), a.scales.data_ptr(), wq.data_ptr(), sq.data_ptr(), to,
+        args = _pack(_PACK_MX8, "gemm_mx8", a._codes.data_ptr(), a._scales.data_ptr(), wq.data_ptr(), sq.data_ptr(), to,
                      scales, wp, wn, m, N, K, kind, g, alpha)
         st = lib().fp4_gemm_mx8(args, s)
     if st:
         _check(st, "fp4_gemm_mx8")
     if stream is not None:
-        used = (a.codes, a.scales, wq, sq, workspace) + ((out.codes, out.scales) if mx8 else (out,))
+        used = (a._codes, a._scales, wq, sq, workspace) + ((out._codes, out._scales) if mx8 else (out,))
         _keep(dev, stream, used, made)
     return out
 

@@ -211,24 +211,27 @@ def _columns(wq, sq, N, K, tiles):
     return np.concatenate(cs), np.concatenate(ss)
 
 
-@pytest.mark.parametrize("m,N,K,gate", [(16, 57344, 8192, "silu"), (16, 10240, 8192, None), (256, 8192, 28672, None),
-                                        (100, 28672, 4096, "gelu"), (700, 20480, 2880, None),
-                                        (5, (1 << 20) + 16, 8192, None)])
-def test_large_on_sampled_columns(m, N, K, gate):
-    gen = torch.Generator(device="cuda").manual_seed(m + N)
+def _random_packed(N, K, seed):
+    """Random weights in the packed layout, made on the device, zero behind K."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
     nw, ns = F.native_repack_size(N, K)
     Np, Kp = -(-N // 16) * 16, -(-K // 512) * 512
     wq = torch.randint(0, 256, (nw,), dtype=torch.uint8, device="cuda", generator=gen)
     sq = torch.randint(120, 130, (ns,), dtype=torch.uint8, device="cuda", generator=gen)
-    if Kp != K:                                                            # zeros behind K
-        wq.view(Np // 16, Kp // 128, 4, 256)[:, K // 128:, :, :] *= (
-            (torch.arange(K // 128, Kp // 128, device="cuda")[:, None] * 4 + torch.arange(4, device="cuda")) * 32 < K
-        )[None, :, :, None].to(torch.uint8)
+    if Kp != K:
+        block = torch.arange(K // 128, Kp // 128, device="cuda")[:, None] * 4 + torch.arange(4, device="cuda")
+        wq.view(Np // 16, Kp // 128, 4, 256)[:, K // 128:, :, :] *= (block * 32 < K)[None, :, :, None].to(torch.uint8)
+    return wq, sq
+
+
+def _check_sampled(m, N, K, gate, tiles):
+    """16-bit and (where the columns allow) 8-bit results on the columns of the given output tiles."""
+    wq, sq = _random_packed(N, K, m + N)
     a = _activations(m, K, 8)
     A = _mx8(*a, K)
     cols = N // 2 if gate else N
+    tiles = sorted({min(max(t, 0), cols // 16 - 1) for t in tiles})
     got = F.gemm_mx8(A, wq, sq, N, gate=gate)
-    tiles = sorted({0, 1, cols // 48, cols // 16 - 1, cols // 32 + 1, min(cols // 16 - 1, 1 << 16)})
     pick = np.concatenate([np.arange(16 * t, 16 * t + 16) for t in tiles])
     w = _columns(wq, sq, N, K, tiles + ([t + cols // 16 for t in tiles] if gate else []))
     want, err = _expected(a, w, K, gate)
@@ -245,6 +248,27 @@ def test_large_on_sampled_columns(m, N, K, gate):
         codes[:, :len(p)] = eight.codes.view(torch.uint8)[:, torch.from_numpy(p).cuda()]
         scales[:, :len(pair)] = eight.scales.view(torch.uint8)[:, pair]
         _check8(F.MX8(codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu), len(p)), want, err)
+        assert not eight.codes.view(torch.uint8)[:, cols:].any() and not eight.scales.view(torch.uint8)[:, cols // 32:].any()
+
+
+@pytest.mark.parametrize("m,N,K,gate", [(16, 57344, 8192, "silu"), (16, 10240, 8192, None), (256, 8192, 28672, None),
+                                        (100, 28672, 4096, "gelu"), (700, 20480, 2880, None),
+                                        (5, (1 << 20) + 16, 8192, None)])
+def test_large_on_sampled_columns(m, N, K, gate):
+    cols = N // 2 if gate else N
+    _check_sampled(m, N, K, gate, [0, 1, cols // 48, cols // 16 - 1, cols // 32 + 1, min(cols // 16 - 1, 1 << 16)])
+
+
+# one size for every kernel and split of K that the choice by the time model reaches besides
+@pytest.mark.parametrize("m,N,K,gate", [
+    (17, 11200, 32, None), (21, 17440, 32, "silu"), (25, 52928, 32, "silu"), (35, 39712, 32, None), (70, 5872, 4928, None),
+    (1780, 160, 2784, "silu"), (17, 16, 14176, None), (65, 16064, 3840, "silu"), (125, 64, 1184, "silu"),
+    (157, 64, 1600, "gelu"), (73, 39200, 32, "silu"), (132, 14080, 8192, "silu"), (67, 17632, 5952, None),
+    (75, 8928, 11488, None), (2744, 64, 17888, "silu"), (320, 13152, 31648, "silu"), (1051, 3904, 12512, None),
+    (261, 7920, 30752, None)])
+def test_every_kernel_on_sampled_columns(m, N, K, gate):
+    last = (N // 2 if gate else N) // 16 - 1
+    _check_sampled(m, N, K, gate, [0, 1, last // 2, last - 1, last])
 
 
 def test_activations_near_the_size_limit():

@@ -283,3 +283,18 @@ def test_binding_refuses():
             call()
     with pytest.raises(F.Fp4Error):
         F.gemm_mx8_workspace_size(1, 0, 32)
+    for a, gate in ((x, None), (None, "silu")):
+        with pytest.raises(ValueError):
+            F.gemm_mx8(a, x, x, 32, gate=gate)
+    with pytest.raises(ValueError):
+        F.new_mx8(1, 48, "cpu")
+
+
+def test_8_bit_rows_are_fixed():
+    a = F.new_mx8(3, 160, "cpu")
+    assert a.codes.shape == (3, 256) and a.scales.shape == (3, 8) and a.K == 160
+    for name in ("codes", "scales", "K"):
+        with pytest.raises(AttributeError):
+            setattr(a, name, getattr(a, name))
+        with pytest.raises(AttributeError):
+            delattr(a, name)
