@@ -298,7 +298,13 @@ __global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
 // two chunks ahead.  Per chunk c: the fragments of each 16 rows are read one step
 // ahead of their products; before the last products: wait for this wave's DMA of
 // chunk c + 1, barrier (every wave has read chunk c, and chunk c + 1 is whole), DMA of
-// chunk c + 3 into c's buffer.
+// chunk c + 3 into c's buffer.  Six buffers with weights four chunks ahead were slower
+// on every shape (2048 x 57344 x 8192 on 128 x 256 tiles 752 -> 789 us, on 64 x 256 798 ->
+// 1112): fewer workgroups fit a compute unit.
+// Bound by the matrix cores and their operands' reads where rows are many: 2048 x 57344 x
+// 8192 gated 687 us, 2.8 PFLOP/s (a library product of 8-bit floats of 8192 cubed reaches
+// 2.7); by rounds and the latency of the first loads where they are few: 256 x 8192 x 28672
+// 61 us, 2.0 PFLOP/s.
 // S > 1: FP32 partial sums in fragment order to P, for reduce_mx8.
 template <int WM, int WN, int MBW, int TNW>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4* __restrict__ P, int S) {
@@ -415,8 +421,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
             mma(mb % 2 ? fb : fa, mb);
         }
         // Loads complete in issue order, and after the DMA of chunk c + 1 came the
-        // weights of c + 1, the DMA of c + 2 and the weights of c + 2.  (The last are
-        // deleted by the compiler at T = 2 of a last group, where nothing takes them.)
+        // weights of c + 1, the DMA of c + 2 and the weights of c + 2, before the first
+        // step too.  (Weights that nothing takes are deleted by the compiler: in the copy
+        // of a last group those of c + 2 from T = 2 on.  After T = 3 of it nothing is read.)
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kYounger) : "memory");
         lds_barrier();
         a_dma(c + 3, b_cur);
@@ -444,12 +451,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
     s_dma(q0);
 #pragma unroll
     for (int tt = 0; tt < TNW; ++tt) wsc[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, q0 * 256, kLoadReused);
-    w_issue(std::integral_constant<int, 0>{}, 4 * q0);
     a_dma(4 * q0, 0);
-    w_issue(std::integral_constant<int, 1>{}, 4 * q0 + 1);
+    w_issue(std::integral_constant<int, 0>{}, 4 * q0);
     a_dma(4 * q0 + 1, kBuf);
+    w_issue(std::integral_constant<int, 1>{}, 4 * q0 + 1);
     a_dma(4 * q0 + 2, 2 * kBuf);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage) : "memory");  // the DMA of the first chunk
     lds_barrier();
     read(b_cur, 0, 0, q0, fa);
     int q = q0;
@@ -491,7 +498,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
 
 // The partial sums of S shares of K, added in the order of the shares; one wave for
 // 16 rows and one output tile (8-bit output: two).  All loads of a wave are under way
-// at once.
+// at once.  256 x 8192 in four shares: 7.4 us, 5 TB/s; a last workgroup that adds in
+// the product itself needs the shares' tiles in turn, and took twice the product's time.
 template <int S>
 __global__ __launch_bounds__(256) void reduce_mx8(Mx8Gemm p, const f32x4* __restrict__ P) {
     const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;

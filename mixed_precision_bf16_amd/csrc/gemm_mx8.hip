@@ -35,21 +35,22 @@ struct Mx8Plan {
 };
 
 // The kernel and split with the least modelled time (us).  Measured on MI355X with every
-// shape forced, N x K of 57344 x 8192, 10240 x 8192, 8192 x 28672, 8192 x 8192, 4096 x
-// 14336, 1024 x 8192, 2880 x 2880, gated 57344 x 8192, 20480 x 4096 and 5760 x 2880, m = 1,
-// 16, 24, 48, 64, 80, 160, 256, 700, 2048: the choice is 1.6 % off the best on average,
-// 18 % at most (700 x 5760 x 2880 and the narrowest below 15 us).
+// shape forced and the weights in HBM (copies of them in turn, 700 MB and more), N x K of
+// 57344 x 8192, 10240 x 8192, 8192 x 28672, 8192 x 8192, 4096 x 14336, 1024 x 8192, 2880 x
+// 2880, gated 57344 x 8192, 20480 x 4096 and 5760 x 2880, m = 1, 16, 24, 48, 64, 80, 160,
+// 256, 700, 2048: the choice is 1.5 % off the best on average, 19 % at most (160 x 8192 x
+// 8192).
 //   Small m: launch and first loads 3.5, then 128 k of a workgroup's tiles cost 0.03 a
 //   tile (the weights of all 256 compute units arrive at 6.2 TB/s) and 0.022 for 16 rows of
-//   activations.  16 x 10240 x 8192 takes 10.7 us with 3 tiles a workgroup (214
-//   workgroups), 13.8 with 2 (320: two rounds), 11.1 with 4 and 15.6 with 8; 16 x 57344
-//   x 8192 gated 46, 43 and 40 us with 2, 4 and 8.
+//   activations.  16 x 10240 x 8192 takes 11.7 us with 3 tiles a workgroup (214
+//   workgroups), 14.7 with 2 (320: two rounds), 11.6 with 4 and 18 with 8; 16 x 57344
+//   x 8192 gated 51, 44 and 41 us with 2, 4 and 8.
 //   Larger m: 3.0, then the tile's time; a split of K adds its partial sums' round trip
 //   through the caches at 6 TB/s and the second launch, 4.0.  256 x 8192 x 28672: 61 us
-//   as 128 x 256 tiles split four ways, 69 as 256 x 256 split eight ways, 94 as 64 x 128
-//   unsplit; 2048 x 57344 x 8192 gated: 679 us as 256 x 256, 752 as 128 x 256, 798 as 64 x
-//   256, 1065 as 64 x 128 tiles; 256 x 8192 x 8192: 23 us as 64 x 128 tiles, 27 as 128 x 256
-//   split four ways.
+//   as 128 x 256 tiles split four ways, 71 as 256 x 256 split eight ways, 92 as 64 x 128
+//   unsplit; 2048 x 57344 x 8192 gated: 687 us as 256 x 256, 758 as 128 x 256, 794 as 64 x
+//   256, 1062 as 64 x 128 tiles, which are for few rows and short K: 256 x 8192 x 8192 29.4
+//   us, 32 as 128 x 256 split four ways (with the weights in the Infinity Cache 23 and 27).
 static Mx8Plan mx8_plan(int64_t m, int64_t N, int64_t K, int out_type, int gate) {
     const int64_t out = out_tiles_of(gate ? N / 2 : N, out_type), chunks = mx8_padded(K) / kChunkK;
     const double bytes = (double)N * (double)K * 0.53125;

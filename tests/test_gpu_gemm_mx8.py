@@ -124,6 +124,13 @@ def test_against_the_oracle(m, N, K):
     _run_all(m, N, K, (None, "silu", "gelu"), m * 31 + N + K)
 
 
+# more than 16 rows and at most 512 k: a workgroup's first group is its last, so the first
+# wait for a chunk meets the fewest loads behind it
+@pytest.mark.parametrize("m,N,K", [(130, 4096, 512), (300, 2048, 384), (1000, 1024, 256), (520, 1056, 480), (2000, 2048, 160)])
+def test_one_group_of_k(m, N, K):
+    _run_all(m, N, K, (None, "silu"), m + N + K)
+
+
 def test_alpha():
     _run_all(20, 192, 512, (None, "silu", "gelu"), 4, alpha=0.037)
     _run_all(3, 64, 256, (None, "silu"), 5, alpha=-8.0)
