@@ -185,6 +185,7 @@ __global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsa, (__attribute__((address_space(3))) void*)(mine + buf * kBuf + BM * 512), 16,
                 (int)(soff + (uint32_t)q * 16), 0, 0, 0);
+        asm volatile("" ::: "memory");  // the weights stay behind it: the waits count them
     };
     u32x4 w[4][TN];
     uint32_t sc[2][TN];
@@ -454,9 +455,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
     a_dma(4 * q0, 0);
     w_issue(std::integral_constant<int, 0>{}, 4 * q0);
     a_dma(4 * q0 + 1, kBuf);
+    asm volatile("" ::: "memory");  // the weights of chunk 1 stay behind its DMA: the waits count them
     w_issue(std::integral_constant<int, 1>{}, 4 * q0 + 1);
     a_dma(4 * q0 + 2, 2 * kBuf);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage) : "memory");  // the DMA of the first chunk
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage + TNW) : "memory");  // the DMA of the first chunk
     lds_barrier();
     read(b_cur, 0, 0, q0, fa);
     int q = q0;
