@@ -446,7 +446,7 @@ int fp4_mx8_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_by
 
 /* BF16 (act_type 0) or FP16 (1) rows to 8 bits on `stream`: element k of row i at
  * i * x_stride + k; x 16-byte aligned, x_stride >= 0, below 2^40 and a multiple
- * of 8.  rows == 0 is a no-op. */
+ * of 8; codes and scales do not overlap it.  rows == 0 is a no-op. */
 int fp4_quantize_mx8(const void* x, int64_t rows, int64_t K, int64_t x_stride, int act_type, void* codes,
                      void* scales, void* stream);
 
@@ -471,14 +471,14 @@ typedef struct fp4_rms_norm_args {
 } fp4_rms_norm_args;
 
 /* All 16-bit arrays 16-byte aligned.  An array that is both read and written is
- * given with the same pointer and stride, or does not overlap.  rows == 0 is a
- * no-op. */
+ * given with the same pointer and stride, or does not overlap (the same pointer with
+ * another stride, or of two outputs: FP4_ERR_SHAPE).  rows == 0 is a no-op. */
 int fp4_rms_norm(const fp4_rms_norm_args* args, void* stream);
 
 /* Products of 8-bit activations with MXFP4 weights in the native packed layout
  * (fp4_native_repack), accumulated in FP32: for m <= 16 on the 16-bit matrix cores,
- * both operands being exact in BF16 (values below 2^-126 may count as zero, those
- * from 2^128 on overflow: no row that fp4_quantize_mx8 writes has such); for more
+ * both operands being exact in BF16 (values below 2^-126 may count as zero; values
+ * from 2^128 on, which no row written here holds, overflow); for more
  * rows on the scaled 8-bit matrix cores, which add the products of 32 k to 13 bits
  * below the largest of them (an error of about 1e-5 of sum |a w|):
  *   gate 0:  Y = alpha * (A . dequant(W)^T), N columns
@@ -510,8 +510,8 @@ int fp4_gemm_mx8_workspace_size(int64_t m, int64_t N, int64_t K, int out_type, i
 
 /* K % 32 == 0, K <= 2^20, N <= 2^24, m <= 2^20; with a gate N % 32 == 0; with
  * MX8 output the columns % 32 == 0; with m rounded up to 256, m * Kp bytes of A
- * and the bytes of Y below 2^31 (else FP4_ERR_SHAPE).  m == 0 is a no-op.
- * Deterministic. */
+ * and the bytes of Y below 2^31, and what is written (out, out_scales, workspace)
+ * apart from all else (else FP4_ERR_SHAPE).  m == 0 is a no-op.  Deterministic. */
 int fp4_gemm_mx8(const fp4_gemm_mx8_args* args, void* stream);
 
 /* ---- Rotary positions --------------------------------------------------------

@@ -139,6 +139,25 @@ static int gemm_mx8_check(int64_t m, int64_t N, int64_t K, int out_type, int gat
     return FP4_OK;
 }
 
+// Whether what a call writes (output, its scales, workspace) lies apart from all else of it.
+static bool gemm_mx8_apart(const fp4_gemm_mx8_args* q, size_t workspace) {
+    const int64_t KA = mx8_padded(q->K), cols = q->gate ? q->N / 2 : q->N;
+    const int64_t out = q->out_type == 2 ? q->m * mx8_padded(cols) : q->m * cols * 2;
+    const int64_t weights = padded_n(q->N) * padded_k(q->K);
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } part[] = {{q->out, out}, {q->out_scales, q->out_type == 2 ? out / 32 : 0}, {q->workspace, (int64_t)workspace},
+                {q->codes, q->m * KA}, {q->scales, q->m * KA / 32}, {q->wq, weights / 2}, {q->sq, weights / 32}};
+    for (int i = 0; i < 3; ++i)
+        for (int k = i + 1; k < 7; ++k) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(part[i].p), b = reinterpret_cast<uintptr_t>(part[k].p);
+            if (part[i].bytes && part[k].bytes && a < b + (uintptr_t)part[k].bytes && b < a + (uintptr_t)part[i].bytes)
+                return false;
+        }
+    return true;
+}
+
 static int gemm_mx8_impl(const fp4_gemm_mx8_args* q, void* stream) {
     if (!q) return FP4_ERR_NULL;
     int st = gemm_mx8_check(q->m, q->N, q->K, q->out_type, q->gate);
@@ -155,6 +174,7 @@ static int gemm_mx8_impl(const fp4_gemm_mx8_args* q, void* stream) {
     if (plan.workspace && (!q->workspace || q->workspace_bytes < plan.workspace ||
                            (reinterpret_cast<uintptr_t>(q->workspace) & 255)))
         return FP4_ERR_WORKSPACE;
+    if (!gemm_mx8_apart(q, plan.workspace)) return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;
     Mx8Gemm p{};

@@ -199,6 +199,17 @@ static int norm_impl(const fp4_rms_norm_args* p, void* stream) {
     if (mx8 ? !mx8_out_ok(p->out, p->out_scales)
             : !matrix_ok(p->out, p->out_stride) || !rows_apart(p->rows, 1, p->width, p->out_stride, p->width))
         return FP4_ERR_SHAPE;
+    // a row is read whole before it is written, so an output may lie where an input does,
+    // row on row; no two outputs may
+    auto apart_or_same = [&](const void* to, int64_t stride, const void* from, int64_t from_stride) {
+        return to != from || (p->rows == 1 || stride == from_stride);
+    };
+    const bool apart = mx8 ? p->out != p->x && p->out != p->residual
+                           : apart_or_same(p->out, p->out_stride, p->x, p->x_stride) &&
+                                 apart_or_same(p->out, p->out_stride, p->residual, p->residual_stride);
+    if (!apart || (p->sum && (p->sum == p->out || !apart_or_same(p->sum, p->sum_stride, p->x, p->x_stride) ||
+                              !apart_or_same(p->sum, p->sum_stride, p->residual, p->residual_stride))))
+        return FP4_ERR_SHAPE;
     int st = check_device();
     if (st != FP4_OK) return st;
     NormArgs a{};
@@ -244,7 +255,7 @@ static int quantize_mx8_impl(const void* x, int64_t rows, int64_t K, int64_t x_s
     if (rows < 0 || rows > (int64_t(1) << 24) || K < 32 || K > (int64_t(1) << 20) || K % 32) return FP4_ERR_SHAPE;
     if (rows == 0) return FP4_OK;
     if (!x || !codes || !scales) return FP4_ERR_NULL;
-    if (!matrix_ok(x, x_stride) || !mx8_out_ok(codes, scales)) return FP4_ERR_SHAPE;
+    if (!matrix_ok(x, x_stride) || !mx8_out_ok(codes, scales) || codes == x) return FP4_ERR_SHAPE;
     int st = check_device();
     if (st != FP4_OK) return st;
     NormArgs a{};

@@ -344,6 +344,12 @@ static void rope_t(int kind, const RopeArgs& r, const Rows& x, const RowsOut& y,
     else rope_kernel<ACT, kHalves, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
 }
 
+// Whether rows `to` begin elsewhere than rows `from`, or lie on them one by one.
+static bool apart_or_same(const void* to, int64_t to_ts, int64_t to_hs, const void* from, int64_t ts, int64_t hs,
+                          int64_t tokens, int64_t heads) {
+    return to != from || ((tokens == 1 || to_ts == ts) && (heads == 1 || to_hs == hs));
+}
+
 static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens, int64_t heads,
                      int64_t head_dim, int64_t x_ts, int64_t x_hs, int64_t out_ts, int64_t out_hs, int act_type,
                      void* stream) {
@@ -356,7 +362,8 @@ static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_
     if (!x || !out) return FP4_ERR_NULL;
     st = rope_pointers(r);
     if (st != FP4_OK) return st;
-    if (!rows_ok(x, x_ts, x_hs) || !rows_ok(out, out_ts, out_hs) || !rows_apart(tokens, heads, head_dim, out_ts, out_hs))
+    if (!rows_ok(x, x_ts, x_hs) || !rows_ok(out, out_ts, out_hs) || !rows_apart(tokens, heads, head_dim, out_ts, out_hs) ||
+        !apart_or_same(out, out_ts, out_hs, x, x_ts, x_hs, tokens, heads))
         return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;
@@ -423,7 +430,10 @@ static int append_rope_impl(const fp4_kv_cache* cache, const fp4_rope_args* rope
         return FP4_ERR_SHAPE;
     if (p->q_heads && (!rows_ok(p->q, p->q_token_stride, p->q_head_stride) ||
                        !rows_ok(p->q_out, p->q_out_token_stride, p->q_out_head_stride) ||
-                       !rows_apart(p->tokens, p->q_heads, cache->head_dim, p->q_out_token_stride, p->q_out_head_stride)))
+                       !rows_apart(p->tokens, p->q_heads, cache->head_dim, p->q_out_token_stride, p->q_out_head_stride) ||
+                       p->q_out == p->k || p->q_out == p->v ||
+                       !apart_or_same(p->q_out, p->q_out_token_stride, p->q_out_head_stride, p->q, p->q_token_stride,
+                                      p->q_head_stride, p->tokens, p->q_heads)))
         return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;

@@ -965,8 +965,10 @@ def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str | None = N
     import torch
     if rotary < 2 or rotary % 2:
         raise ValueError("rotary must be even, 2 at least")
-    if not base > 1.0 or not factor >= 1.0:
+    if not 1.0 < base < math.inf or not 1.0 <= factor < math.inf:
         raise ValueError("base must be over 1 and factor 1 at least")
+    if not 0.0 < low < high or not 0.0 < slow < fast or original < 1:
+        raise ValueError("low < high and slow < fast must be over 0, original 1 at least")
     i = np.arange(rotary // 2, dtype=np.float64)
     f = base ** (-2.0 * i / rotary)
     amplitude = 1.0

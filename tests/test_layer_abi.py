@@ -121,7 +121,9 @@ def test_frequencies():
     same, amp = F.rope_frequencies(64, scaling="yarn", device="cpu")
     assert amp == 1.0 and torch.allclose(same, f)
     for bad in (dict(rotary=0), dict(rotary=7), dict(rotary=8, scaling="other"), dict(rotary=8, factor=0.5),
-                dict(rotary=8, base=1.0)):
+                dict(rotary=8, base=1.0), dict(rotary=8, base=math.inf), dict(rotary=8, factor=math.inf),
+                dict(rotary=8, scaling="bands", low=4.0), dict(rotary=8, scaling="yarn", slow=0.0),
+                dict(rotary=8, scaling="yarn", original=0)):
         with pytest.raises(ValueError):
             F.rope_frequencies(device="cpu", **bad)
 
@@ -259,6 +261,34 @@ def test_append_rope_argument_errors():
                  dict(kt=-8), dict(vh=4), dict(vt=1 << 40)):
         assert call(**over) == 2, over
     assert call(tokens=0, q=0, q_out=0, k=0, v=0, slots=0) == 0
+
+
+def test_outputs_on_other_arrays_are_refused():
+    """Calls right but for an output that lies on another array of theirs."""
+    far = dict(x=1 << 30, residual=2 << 30, weight=3 << 30, out=4 << 30, out_scales=5 << 30, sum=6 << 30)
+    for over in (dict(out=1 << 30, x_stride=72), dict(out=2 << 30, residual_stride=72), dict(sum=1 << 30, sum_stride=72),
+                 dict(sum=2 << 30, sum_stride=72), dict(sum=4 << 30), dict(out_type=1, out=1 << 30),
+                 dict(out_type=1, out=2 << 30), dict(out_type=1, sum=4 << 30)):
+        assert _norm(**(far | over)) == 2, over
+    assert F.lib().fp4_quantize_mx8(1 << 30, 3, 64, 64, 0, 1 << 30, 2 << 30, None) == 2
+    far = dict(codes=1 << 40, scales=2 << 40, wq=3 << 40, sq=4 << 40, out=5 << 40, out_scales=6 << 40, workspace=7 << 40)
+    m, N, K = 256, 8192, 28672
+    for name, last in (("codes", m * K), ("scales", m * K // 32), ("wq", N * K // 2), ("sq", N * K // 32)):
+        for by in (0, last - 256, 256 - m * N * 2):
+            assert _product(**(far | dict(out=far[name] + by)), m=m, N=N, K=K) == 2, (name, by)
+        assert _product(**(far | dict(workspace=far[name])), m=m, N=N, K=K) == 2
+        assert _product(**(far | dict(out_type=2, out_scales=far[name] + last - 4)), m=m, N=N, K=K) == 2
+    assert _product(**(far | dict(workspace=5 << 40)), m=m, N=N, K=K) == 2
+    assert _product(**(far | dict(out_type=2, out_scales=5 << 40)), m=m, N=N, K=K) == 2
+
+    def turn(out=1 << 30, xt=256, xh=64, ot=256, oh=64):
+        return F.lib().fp4_rope(_rope(), 1 << 30, out, 3, 4, 64, xt, xh, ot, oh, 0, None)
+    assert turn(xt=512) == 2 and turn(xh=128, xt=512, ot=512) == 2
+    c = F._KVCacheDesc(data=16, pages=4, page_size=64, kv_heads=2, head_dim=128, format=0, k_alpha=1.0, v_alpha=1.0)
+    for over in (dict(q_out=2 << 30), dict(q_out=3 << 30), dict(q_out=1 << 30, qt=1024), dict(q_out=1 << 30, qt=1024, ot=1024, qh=256)):
+        f = dict(q=1 << 30, q_out=5 << 30, k=2 << 30, v=3 << 30, slots=4 << 30, tokens=3, q_heads=4, qt=512, qh=128,
+                 ot=512, oh=128, kt=256, kh=128, vt=256, vh=128, act=0) | over
+        assert F.lib().fp4_kv_append_rope(ctypes.byref(c), _rope(), F._PACK_APPEND_ROPE.pack(*f.values()), None) == 2, over
 
 
 def test_packed_arguments_have_the_structures_sizes():
