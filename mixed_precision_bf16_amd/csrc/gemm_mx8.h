@@ -299,19 +299,27 @@ __global__ __launch_bounds__(64 * NWN * NWK) void gemm_mx8_decode(Mx8Gemm p) {
 // two chunks ahead.  Per chunk c: the fragments of each 16 rows are read one step
 // ahead of their products; before the last products: wait for this wave's DMA of
 // chunk c + 1, barrier (every wave has read chunk c, and chunk c + 1 is whole), DMA of
-// chunk c + 3 into c's buffer.  Six buffers with weights four chunks ahead were slower
-// on every shape (2048 x 57344 x 8192 on 128 x 256 tiles 752 -> 789 us, on 64 x 256 798 ->
-// 1112): fewer workgroups fit a compute unit.
-// Bound by the matrix cores and their operands' reads where rows are many: 2048 x 57344 x
-// 8192 gated 687 us, 2.8 PFLOP/s (a library product of 8-bit floats of 8192 cubed reaches
-// 2.7); by rounds and the latency of the first loads where they are few: 256 x 8192 x 28672
-// 61 us, 2.0 PFLOP/s.
+// chunk c + 3 into c's buffer.
+// kDeep, the narrow tile (64 x 128) of few rows, whose weights come from HBM: buffers
+// of two chunks, weights four chunks ahead past the caches, and a loop without a way
+// out of it (37 -> 30 us for 61 x 8192 x 28672, 29 -> 23 for 256 x 8192 x 8192).  It
+// leaves less room for other workgroups (1060 -> 1470 us for 2048 x 57344 x 8192 gated),
+// and wider tiles lose by it in one round too (128 x 256: 61 -> 67 us for 256 x 8192 x
+// 28672).
+// Bound by the matrix cores where rows are many: 2048 x 57344 x 8192 gated 660 us, 2.9
+// PFLOP/s (a library product of 8-bit floats of 8192 cubed reaches 2.7), the cores busy
+// 65 % of the time at 1.86 GHz, what the power limit leaves; where they are few by the
+// weights' way through the second-level cache: 256 x 8192 x 28672 61 us, 2.0 PFLOP/s,
+// of which 7 are the shares' sums (with weights that lie in the cache 52).
 // S > 1: FP32 partial sums in fragment order to P, for reduce_mx8.
 template <int WM, int WN, int MBW, int TNW>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4* __restrict__ P, int S) {
     constexpr int kThreads = 64 * WM * WN;
     constexpr int BM = WM * MBW * 16;
-    constexpr int kBuf = BM * 128;
+    constexpr bool kDeep = TNW == 2;
+    // chunks of a buffer, chunks the weights are ahead, and room for them
+    constexpr int kPer = kDeep ? 2 : 1, kAhead = kDeep ? 4 : 2, kSlots = kDeep ? 8 : 4;
+    constexpr int kChunk = BM * 128, kBuf = kPer * kChunk;
     constexpr int kStage = BM * 8 / kThreads;  // 16-byte pieces a thread brings per chunk
     static_assert(kStage * kThreads == BM * 8 && BM % 64 == 0 && BM <= kThreads, "whole pieces, whole waves");
     __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuf + 2 * BM * 16];
@@ -352,30 +360,33 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
         const int n = tid + kThreads * i, row = n >> 3, col = (n & 7) ^ ((row >> 1) & 7);
         aoff[i] = (uint32_t)(m0 + row) * (uint32_t)p.KA + col * 16;
     }
+    // chunks c .. c + kPer - 1 to the buffer at `buf` (past the range: into bytes nobody reads again)
     auto a_dma = [&](int c, int buf) {
-        c = min(c, clast);  // a prefetch past the range goes into a buffer nobody reads again
 #pragma unroll
-        for (int i = 0; i < kStage; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (__attribute__((address_space(3))) void*)(lds + buf + (i * kThreads + 64 * wave) * 16), 16,
-                (int)(aoff[i] + (uint32_t)c * 128), 0, 0, 0);
+        for (int u = 0; u < kPer; ++u)
+#pragma unroll
+            for (int i = 0; i < kStage; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    ra, (__attribute__((address_space(3))) void*)(lds + buf + u * kChunk + (i * kThreads + 64 * wave) * 16), 16,
+                    (int)(aoff[i] + (uint32_t)min(c + u, clast) * 128), 0, 0, 0);
+        asm volatile("" ::: "memory");  // later loads stay behind it: the waits count them
     };
     // scales of group q, 16 bytes a row (behind the row's last chunk: bytes that no
-    // product takes)
-    const uint32_t soff = (uint32_t)(m0 + tid) * (uint32_t)(p.KA / 32);
+    // product takes), 64 rows a wave
+    const uint32_t soff = (uint32_t)(m0 + 64 * (wave % (BM / 64)) + lane) * (uint32_t)(p.KA / 32);
     auto s_dma = [&](int q) {
-        if (wave < BM / 64)
+        if (kDeep || wave < BM / 64)  // kDeep: every wave the same rows, no branch in a group
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsa, (__attribute__((address_space(3))) void*)(lds + kScales + (q & 1) * BM * 16 + 64 * wave * 16), 16,
-                (int)(soff + (uint32_t)min(q, q1 - 1) * 16), 0, 0, 0);
+                rsa, (__attribute__((address_space(3))) void*)(lds + kScales + (q & 1) * BM * 16 + 64 * (wave % (BM / 64)) * 16),
+                16, (int)(soff + (uint32_t)min(q, q1 - 1) * 16), 0, 0, 0);
     };
-    u32x4 w[4][TNW];
+    u32x4 w[kSlots][TNW];
     auto w_issue = [&](auto slot_c, int c) {
-        constexpr int SL = decltype(slot_c)::value;
+        constexpr int SL = decltype(slot_c)::value % kSlots;
         c = min(c, clast);
 #pragma unroll
         for (int tt = 0; tt < TNW; ++tt)
-            w[SL][tt] = __builtin_amdgcn_raw_buffer_load_b128(rw[tt], lane * 16, c * 1024, kLoadReused);
+            w[SL][tt] = __builtin_amdgcn_raw_buffer_load_b128(rw[tt], lane * 16, c * 1024, kDeep ? kLoadStream : kLoadReused);
     };
     // no fence: it would also wait for the newest DMA
     auto lds_barrier = [] {
@@ -404,69 +415,114 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
     int b_cur = 0, b_nxt = kBuf, b_far = 2 * kBuf;
     Frag fa, fb;
     uint32_t wsc[TNW], wsn[TNW];
-    // chunk c = 4 q + T; fa holds its first fragment on entry
-    auto step = [&](auto t_c, int q, const uint32_t (&sc)[TNW]) {
-        constexpr int T = decltype(t_c)::value;
-        constexpr int kYounger = T == 2 ? kStage + TNW : kStage + 2 * TNW;
-        const int c = 4 * q + T;
-        w_issue(std::integral_constant<int, (T + 2) % 4>{}, c + 2);
+    // chunk c = 4 q + T, its weights in slot E + T; fa holds its first fragment on entry
+    auto step = [&](auto t_c, auto e_c, auto tail_c, int q, const uint32_t (&sc)[TNW]) {
+        constexpr int T = decltype(t_c)::value, SL = (decltype(e_c)::value + T) % kSlots;
+        constexpr bool kLast = T % kPer == kPer - 1;  // the last chunk of its buffer
+        constexpr bool kTail = decltype(tail_c)::value;  // nothing follows the group
+        const int c = 4 * q + T, at = b_cur + T % kPer * kChunk;
+        if constexpr (!kTail || T + kAhead < 4) w_issue(std::integral_constant<int, SL + kAhead>{}, c + kAhead);
+        if constexpr (!kLast) asm volatile("" ::: "memory");  // not put off to the next chunk
         auto mma = [&](const Frag& f, int mb) {
             const i32x8 a = fp8_operand(f.lo, f.hi);
 #pragma unroll
             for (int tt = 0; tt < TNW; ++tt)
-                acc[tt][mb] = mfma_fp4_fp8<T>(w[T][tt], a, acc[tt][mb], sc[tt], f.s);
+                acc[tt][mb] = mfma_fp4_fp8<T>(w[SL][tt], a, acc[tt][mb], sc[tt], f.s);
         };
 #pragma unroll
         for (int mb = 0; mb + 1 < MBW; ++mb) {
-            read(b_cur, mb + 1, T, q, mb % 2 ? fa : fb);
+            read(at, mb + 1, T, q, mb % 2 ? fa : fb);
             mma(mb % 2 ? fb : fa, mb);
         }
-        // Loads complete in issue order, and after the DMA of chunk c + 1 came the
-        // weights of c + 1, the DMA of c + 2 and the weights of c + 2, before the first
-        // step too.  (Weights that nothing takes are deleted by the compiler: in the copy
-        // of a last group those of c + 2 from T = 2 on.  After T = 3 of it nothing is read.)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kYounger) : "memory");
-        lds_barrier();
-        a_dma(c + 3, b_cur);
-        const int b_free = b_cur;
-        b_cur = b_nxt;
-        b_nxt = b_far;
-        b_far = b_free;
-        read(b_cur, 0, (T + 1) % 4, T == 3 ? q + 1 : q, fa);
+        if constexpr (kLast) {
+            // Loads complete in issue order.  After the DMA of the next buffer came the
+            // weights asked for in two buffers' steps, this one's included, and between
+            // them the DMA of the buffer after it (before the first step too; a last group
+            // asks for no weights behind it, and nothing is read after its T = 3).
+            constexpr int kSteps = kTail ? std::max(0, std::min(2 * kPer, 2 * kPer - (T + 1 - std::max(0, 4 - kAhead)))) : 2 * kPer;
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer * kStage + kSteps * TNW) : "memory");
+            lds_barrier();
+            a_dma(c + 1 + 2 * kPer, b_cur);
+            const int b_free = b_cur;
+            b_cur = b_nxt;
+            b_nxt = b_far;
+            b_far = b_free;
+            if constexpr (!kTail || T < 3) read(b_cur, 0, (T + 1) % 4, T == 3 ? q + 1 : q, fa);
+        } else {
+            read(at + kChunk, 0, T + 1, q, fa);
+        }
         mma(fb, MBW - 1);
+        if constexpr (kDeep) __builtin_amdgcn_sched_barrier(0);  // products stay in their step
     };
     static_assert(MBW % 2 == 0, "fragments alternate");
-    auto group = [&](int q, const uint32_t (&cur)[TNW], uint32_t (&nxt)[TNW]) {
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    using I4 = std::integral_constant<int, 4>;
+    auto next_scales = [&](int q, uint32_t (&nxt)[TNW]) {
 #pragma unroll
         for (int tt = 0; tt < TNW; ++tt)
-            nxt[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, min(q + 1, q1 - 1) * 256, kLoadReused);
-        s_dma(q + 1);
-        step(std::integral_constant<int, 0>{}, q, cur);
+            nxt[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, min(q, q1 - 1) * 256, kLoadReused);
+        s_dma(q);
+    };
+    auto group = [&](auto e_c, auto tail_c, int q, const uint32_t (&cur)[TNW]) {
+        step(I0{}, e_c, tail_c, q, cur);
         if (4 * q + 1 > clast) return;
-        step(std::integral_constant<int, 1>{}, q, cur);
+        step(I1{}, e_c, tail_c, q, cur);
         if (4 * q + 2 > clast) return;
-        step(std::integral_constant<int, 2>{}, q, cur);
+        step(I2{}, e_c, tail_c, q, cur);
         if (4 * q + 3 > clast) return;
-        step(std::integral_constant<int, 3>{}, q, cur);
+        step(I3{}, e_c, tail_c, q, cur);
+    };
+    // A group with another behind it: no way out of it, so that the compiler's own waits
+    // for weights count the loads of the one way through (else of the shortest).
+    auto whole_group = [&](auto e_c, int q, const uint32_t (&cur)[TNW]) {
+        step(I0{}, e_c, std::false_type{}, q, cur);
+        step(I1{}, e_c, std::false_type{}, q, cur);
+        step(I2{}, e_c, std::false_type{}, q, cur);
+        step(I3{}, e_c, std::false_type{}, q, cur);
     };
     s_dma(q0);
 #pragma unroll
     for (int tt = 0; tt < TNW; ++tt) wsc[tt] = __builtin_amdgcn_raw_buffer_load_b32(rs[tt], lane * 4, q0 * 256, kLoadReused);
+    // the first wait finds kAhead chunks of weights and one buffer behind the second DMA
     a_dma(4 * q0, 0);
-    w_issue(std::integral_constant<int, 0>{}, 4 * q0);
-    a_dma(4 * q0 + 1, kBuf);
-    asm volatile("" ::: "memory");  // the weights of chunk 1 stay behind its DMA: the waits count them
-    w_issue(std::integral_constant<int, 1>{}, 4 * q0 + 1);
-    a_dma(4 * q0 + 2, 2 * kBuf);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kStage + TNW) : "memory");  // the DMA of the first chunk
+    a_dma(4 * q0 + kPer, kBuf);
+    w_issue(I0{}, 4 * q0);
+    w_issue(I1{}, 4 * q0 + 1);
+    if constexpr (kAhead > 2) {
+        w_issue(I2{}, 4 * q0 + 2);
+        w_issue(I3{}, 4 * q0 + 3);
+    }
+    a_dma(4 * q0 + 2 * kPer, 2 * kBuf);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kPer * kStage + kAhead * TNW) : "memory");  // the first DMA
     lds_barrier();
     read(b_cur, 0, 0, q0, fa);
     int q = q0;
-    for (; q + 1 < q1; q += 2) {
-        group(q, wsc, wsn);
-        group(q + 1, wsn, wsc);
+    if constexpr (kDeep) {
+        for (; q + 2 < q1; q += 2) {
+            next_scales(q + 1, wsn);
+            whole_group(I0{}, q, wsc);
+            next_scales(q + 2, wsc);
+            whole_group(I4{}, q + 1, wsn);
+        }
+        if (q + 2 == q1) {
+            next_scales(q + 1, wsn);
+            whole_group(I0{}, q, wsc);
+            group(I4{}, std::true_type{}, q + 1, wsn);
+        } else {
+            group(I0{}, std::true_type{}, q, wsc);
+        }
+    } else {
+        for (; q + 1 < q1; q += 2) {
+            next_scales(q + 1, wsn);
+            group(I0{}, std::false_type{}, q, wsc);
+            next_scales(q + 2, wsc);
+            group(I0{}, std::false_type{}, q + 1, wsn);
+        }
+        if (q < q1) group(I0{}, std::true_type{}, q, wsc);
     }
-    if (q < q1) group(q, wsc, wsn);
     // no DMA may still write this workgroup's LDS after it exits
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
