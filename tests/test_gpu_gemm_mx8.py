@@ -131,6 +131,13 @@ def test_one_group_of_k(m, N, K):
     _run_all(m, N, K, (None, "silu"), m + N + K)
 
 
+# the narrow tile's loop takes groups of 512 k two by two: one to five of them, the last
+# one whole or of one to four steps of 128
+@pytest.mark.parametrize("K", [544, 896, 1024, 1056, 1152, 1312, 1536, 1568, 1760, 2048, 2080, 2560])
+def test_groups_of_k(K):
+    _run_all(70, 160, K, (None, "silu"), K)
+
+
 def test_alpha():
     _run_all(20, 192, 512, (None, "silu", "gelu"), 4, alpha=0.037)
     _run_all(3, 64, 256, (None, "silu"), 5, alpha=-8.0)
@@ -276,6 +283,13 @@ def test_large_on_sampled_columns(m, N, K, gate):
 def test_every_kernel_on_sampled_columns(m, N, K, gate):
     last = (N // 2 if gate else N) // 16 - 1
     _check_sampled(m, N, K, gate, [0, 1, last // 2, last - 1, last])
+
+
+@pytest.mark.parametrize("m,N,K,gate", [(2754, 32, 2944, "silu"), (33, 10240, 8192, None), (64, 8192, 28672, None),
+                                        (96, 10240, 8192, None), (64, 20480, 4096, "gelu")])
+def test_narrow_tiles_on_sampled_columns(m, N, K, gate):
+    last = (N // 2 if gate else N) // 16 - 1
+    _check_sampled(m, N, K, gate, sorted({0, last // 2, max(last - 1, 0), last}))
 
 
 def test_activations_near_the_size_limit():
