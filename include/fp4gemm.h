@@ -547,7 +547,7 @@ typedef struct fp4_append_rope_args {
     void* q_out;          /* may be q, with q's strides; else overlaps none of q, k, v */
     const void* k;        /* device [tokens][kv_heads][head_dim]; not written */
     const void* v;
-    const int64_t* slots; /* device [tokens]; outside the cache: key and value are skipped, queries turned all the same */
+    const int64_t* slots; /* device [tokens], none twice; outside the cache: key and value skipped, queries turned all the same */
     int64_t tokens, q_heads;
     int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
     int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;

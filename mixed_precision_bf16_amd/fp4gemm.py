@@ -1037,8 +1037,8 @@ def kv_append_rope(cache: KVCache, q, k, v, slots, positions, frequencies, inter
     """fp4_kv_append_rope: rope() of q and k and kv_append() of the turned keys and
     the values, in one launch.  q: [tokens][q_heads][head_dim]; k, v:
     [tokens][kv_heads][head_dim] (not written); slots, positions: int64 CUDA
-    [tokens].  Returns (or fills) q_out, which may be q.  A token whose slot is
-    outside the cache is turned but not written."""
+    [tokens], no slot twice.  Returns (or fills) q_out, which may be q.  A token
+    whose slot is outside the cache is turned but not written."""
     import torch
     act = _act_type(k.dtype, "k")
     dev, dim = cache._data.device, cache._head_dim

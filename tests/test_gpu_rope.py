@@ -147,3 +147,43 @@ def test_no_tokens():
     assert F.rope(x, none, freq).shape == (0, 3, 64)
     cache = F.new_kv_cache(1, 32, 3, 64, 0)
     assert F.kv_append_rope(cache, x, x, x, none, none, freq).shape == (0, 3, 64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("inter", [False, True])
+def test_large_outputs_are_those_of_their_parts(inter, dtype):
+    """Queries of more than 64 MiB (stored past the caches), alone and with the cache's write."""
+    n, QH, H, D, page = 4101, 64, 2, 128, 64
+    x = torch.randn((n, QH + 2 * H, D), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(dtype)
+    pos, freq = _positions(n, 5).cuda(), F.rope_frequencies(D, 10000.0)[0]
+    slots = torch.randperm(65 * page, generator=torch.Generator().manual_seed(1))[:n].cuda()
+    whole, parts = F.new_kv_cache(65, page, H, D, 0), F.new_kv_cache(65, page, H, D, 0)
+    whole.data.zero_(), parts.data.zero_()
+    got = F.kv_append_rope(whole, x[:, :QH], x[:, QH:QH + H], x[:, QH + H:], slots, pos, freq, interleaved=inter)
+    alone = F.rope(x[:, :QH], pos, freq, interleaved=inter)
+    for a in range(0, n, 1000):
+        y, at = x[a:a + 1000], slice(a, a + 1000)
+        q = F.kv_append_rope(parts, y[:, :QH], y[:, QH:QH + H], y[:, QH + H:], slots[at], pos[at], freq, interleaved=inter)
+        assert q.equal(got[at]) and q.equal(alone[at])
+    assert whole.data.equal(parts.data)
+    F.rope(x[:, :QH], pos, freq, interleaved=inter, out=x[:, :QH])                 # in place
+    assert x[:, :QH].equal(got)
+
+
+def test_more_tokens_than_a_launch_takes():
+    n, D, page = (1 << 20) + 6, 64, 32
+    x = torch.randn((n, 3, D), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(BF16)
+    pos = torch.arange(n, device="cuda")
+    freq, _ = F.rope_frequencies(D, 500000.0)
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    slots[:20], slots[-20:] = torch.arange(20, device="cuda"), torch.arange(64, 84, device="cuda")
+    cache, few = F.new_kv_cache(3, page, 1, D, 0), F.new_kv_cache(3, page, 1, D, 0)
+    cache.data.zero_(), few.data.zero_()
+    got = F.kv_append_rope(cache, x[:, :1], x[:, 1:2], x[:, 2:], slots, pos, freq)
+    alone = F.rope(x[:, :1], pos, freq)
+    for at in (slice(0, 20), slice(n - 20, n)):
+        y = x[at]
+        q = F.kv_append_rope(few, y[:, :1], y[:, 1:2], y[:, 2:], slots[at], pos[at], freq)
+        assert q.equal(got[at]) and q.equal(alone[at])
+        assert q.cpu().equal(_want(y[:, :1].cpu(), pos[at].cpu(), freq, False))
+    assert cache.data.equal(few.data) and got.equal(alone)
