@@ -292,6 +292,11 @@ def test_narrow_tiles_on_sampled_columns(m, N, K, gate):
     _check_sampled(m, N, K, gate, sorted({0, last // 2, max(last - 1, 0), last}))
 
 
+@pytest.mark.parametrize("m", [3, 24, 70])
+def test_longest_rows(m):
+    _run_all(m, 32, 1 << 20, (None, "silu"), m)
+
+
 def test_activations_near_the_size_limit():
     m, N, K = 130816, 32, 16384                                            # 2.14e9 bytes of codes
     few = _activations(64, K, 1)

@@ -164,6 +164,21 @@ def test_quantizer_rows(rows, K):
     _same_mx8(into, x[:, :K].double().numpy(), K)
 
 
+def test_longest_rows():
+    n = 1 << 20
+    x, r = (torch.randn((2, n), generator=torch.Generator().manual_seed(i)).to(BF16) for i in (1, 2))
+    y, h = oracle.rms_norm_reference(x.double().numpy(), None, 1e-6, r.double().numpy())
+    got, total = F.rms_norm(x.cuda(), residual=r.cuda(), mx8=True)
+    codes, scales = oracle.mx8_quantize_reference(y)
+    assert np.array_equal(got.codes.view(torch.uint8).cpu().numpy(), codes)
+    assert np.array_equal(got.scales.view(torch.uint8).cpu().numpy(), scales)
+    assert total.cpu().equal(torch.from_numpy(h.astype(np.float32)).to(BF16))
+    codes, scales = oracle.mx8_quantize_reference(x.double().numpy())
+    got = F.quantize_mx8(x.cuda())
+    assert np.array_equal(got.codes.view(torch.uint8).cpu().numpy(), codes)
+    assert np.array_equal(got.scales.view(torch.uint8).cpu().numpy(), scales)
+
+
 def test_many_rows():
     """More rows than one launch takes."""
     rows = (1 << 20) + 5
