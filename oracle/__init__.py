@@ -35,7 +35,9 @@ from .kv_oracle import attention_reference, kv_offsets, kv_read_reference, kv_wr
 from . import layer_oracle  # noqa: F401,E402
 from .layer_oracle import (  # noqa: F401,E402
     gate_reference,
+    gemm_mx8_cut_reference,
     gemm_mx8_reference,
+    mx8_group_sums,
     mx8_padded,
     mx8_quantize_reference,
     mx8_value,
