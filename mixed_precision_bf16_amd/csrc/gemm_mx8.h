@@ -387,6 +387,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsa, (__attribute__((address_space(3))) void*)(lds + kScales + (q & 1) * BM * 16 + 64 * (wave % (BM / 64)) * 16),
                 16, (int)(soff + (uint32_t)min(q, q1 - 1) * 16), 0, 0, 0);
+        asm volatile("" ::: "memory");  // the group's weights stay behind it: its last wait counts them
     };
     u32x4 w[kSlots][TNW];
     auto w_issue = [&](auto slot_c, int c) {
@@ -447,6 +448,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mx8_tiled(Mx8Gemm p, f32x4*
             // weights asked for in two buffers' steps, this one's included, and between
             // them the DMA of the buffer after it (before the first step too; a last group
             // asks for no weights behind it, and nothing is read after its T = 3).
+            // The wait of T = 3 also completes the next group's scales, which are read
+            // behind it: their DMA stands before the group's first step.  Behind it came
+            // four steps' weights and, between them, one buffer's DMA (kPer 2: just what this
+            // wait leaves under way) or three.
             constexpr int kSteps = kTail ? std::max(0, std::min(2 * kPer, 2 * kPer - (T + 1 - std::max(0, 4 - kAhead)))) : 2 * kPer;
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer * kStage + kSteps * TNW) : "memory");
             lds_barrier();
