@@ -470,9 +470,10 @@ typedef struct fp4_rms_norm_args {
     int32_t out_type;     /* 0 as x, 1 MX8 (out_stride is not used) */
 } fp4_rms_norm_args;
 
-/* All 16-bit arrays 16-byte aligned.  An array that is both read and written is
- * given with the same pointer and stride, or does not overlap (the same pointer with
- * another stride, or of two outputs: FP4_ERR_SHAPE).  rows == 0 is a no-op. */
+/* All 16-bit arrays 16-byte aligned.  What is written (out, out_scales, sum) lies apart
+ * from all other arrays, to the byte: views of one array side by side are apart.  An
+ * array that is both read and written is given with the same pointer and stride.  Else
+ * FP4_ERR_SHAPE.  rows == 0 is a no-op. */
 int fp4_rms_norm(const fp4_rms_norm_args* args, void* stream);
 
 /* Products of 8-bit activations with MXFP4 weights in the native packed layout

@@ -1,5 +1,6 @@
 // Root-mean-square norm with the residual's addition, in 16 or 8 bits, and the
 // 8-bit quantizer of activations (include/fp4gemm.h, section "8-bit activations").
+#include "apart.h"
 #include "mx8.h"
 
 namespace fp4 {
@@ -201,17 +202,24 @@ static int norm_impl(const fp4_rms_norm_args* p, void* stream) {
     if (mx8 ? !mx8_out_ok(p->out, p->out_scales)
             : !matrix_ok(p->out, p->out_stride) || !rows_apart(p->rows, 1, p->width, p->out_stride, p->width))
         return FP4_ERR_SHAPE;
-    // a row is read whole before it is written, so an output may lie where an input does,
-    // row on row; no two outputs may
-    auto apart_or_same = [&](const void* to, int64_t stride, const void* from, int64_t from_stride) {
-        return to != from || (p->rows == 1 || stride == from_stride);
-    };
-    const bool apart = mx8 ? p->out != p->x && p->out != p->residual
-                           : apart_or_same(p->out, p->out_stride, p->x, p->x_stride) &&
-                                 apart_or_same(p->out, p->out_stride, p->residual, p->residual_stride);
-    if (!apart || (p->sum && (p->sum == p->out || !apart_or_same(p->sum, p->sum_stride, p->x, p->x_stride) ||
-                              !apart_or_same(p->sum, p->sum_stride, p->residual, p->residual_stride))))
-        return FP4_ERR_SHAPE;
+    // a row is read whole before it is written, so a 16-bit output may be an input, row on row;
+    // else what is written lies apart from all other arrays
+    const int64_t kp = mx8_padded(p->width);
+    const Span x = span_of_rows(p->x, p->width, p->rows, p->x_stride);
+    const Span residual = span_of_rows(p->residual, p->width, p->rows, p->residual_stride);
+    const Span weight = span_of(p->weight, p->width * 2);
+    const Span sum = span_of_rows(p->sum, p->width, p->rows, p->sum_stride);
+    if (spans_meet(sum, weight) || !span_may_be(sum, x) || !span_may_be(sum, residual)) return FP4_ERR_SHAPE;
+    if (mx8) {
+        const Span codes = span_of(p->out, p->rows * kp), scales = span_of(p->out_scales, p->rows * kp / 32);
+        if (spans_meet(codes, scales)) return FP4_ERR_SHAPE;
+        for (const Span& from : {x, residual, weight, sum})
+            if (spans_meet(codes, from) || spans_meet(scales, from)) return FP4_ERR_SHAPE;
+    } else {
+        const Span out = span_of_rows(p->out, p->width, p->rows, p->out_stride);
+        if (spans_meet(out, weight) || spans_meet(out, sum) || !span_may_be(out, x) || !span_may_be(out, residual))
+            return FP4_ERR_SHAPE;
+    }
     int st = check_device();
     if (st != FP4_OK) return st;
     NormArgs a{};
@@ -226,7 +234,7 @@ static int norm_impl(const fp4_rms_norm_args* p, void* stream) {
     a.sum_stride = p->sum_stride;
     a.out_stride = p->out_stride;
     a.vecs = (int)(p->width / 8);
-    a.vecs_out = (int)((mx8 ? mx8_padded(p->width) : p->width) / 8);
+    a.vecs_out = (int)((mx8 ? kp : p->width) / 8);
     a.inv_width = 1.0 / (double)p->width;
     a.eps = p->eps;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -1,0 +1,98 @@
+"""Outputs that lie on other arrays of a call are refused, to the byte; views of one
+array side by side, and outputs in an input's place, are not.  Calls of the C entries
+with addresses that nothing stands behind: run only where no GPU could take them."""
+
+import ctypes
+
+import pytest
+
+from mixed_precision_bf16_amd import fp4gemm as F
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(autouse=True)
+def no_gpu():
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: for machines without a GPU")
+
+
+G = 1 << 30
+SHAPE, DEVICE, HIP = 2, 6, 7
+
+
+def _refused(status):
+    assert status in (SHAPE, DEVICE, HIP), status
+    return status == SHAPE
+
+
+# ------------------------------------------------------------------------ norm
+FAR = dict(x=1 * G, residual=2 * G, weight=3 * G, out=4 * G, out_scales=5 * G, sum=6 * G, rows=5, width=64, x_stride=64,
+           residual_stride=64, out_stride=64, sum_stride=64, eps=1e-6, act_type=0, out_type=0)
+ROW = 128                                                                  # bytes of a row
+
+
+def _norm(**over):
+    return _refused(F.lib().fp4_rms_norm(F._PACK_NORM.pack(*(FAR | over).values()), None))
+
+
+def test_norm_outputs_on_other_arrays():
+    assert not _norm()
+    for out in ("out", "sum"):
+        for other in ("x", "residual"):
+            assert not _norm(**{out: FAR[other]})                           # in its place
+            for by in (16, -16, ROW, -ROW, 4 * ROW, -4 * ROW, 4 * ROW + 112, -4 * ROW - 112):
+                assert _norm(**{out: FAR[other] + by}), (out, other, by)
+            for by in (5 * ROW, -5 * ROW):
+                assert not _norm(**{out: FAR[other] + by}), (out, other, by)
+        for by in (-4 * ROW - 112, -16, 0, 16, 112):
+            assert _norm(**{out: FAR["weight"] + by}), (out, by)
+        for by in (-5 * ROW, 128):
+            assert not _norm(**{out: FAR["weight"] + by}), (out, by)
+    for by in (0, 16, -4 * ROW, 4 * ROW):
+        assert _norm(sum=FAR["out"] + by)
+    assert not _norm(sum=FAR["out"] + 5 * ROW)
+
+
+def test_norm_views_of_one_array():
+    """x, residual, out and sum as columns of one array; the same columns shifted."""
+    side = dict(x=G, residual=G + 128, out=G + 256, sum=G + 384, x_stride=256, residual_stride=256, out_stride=256,
+                sum_stride=256)
+    assert not _norm(**side)
+    assert _norm(**(side | dict(out=G + 240))) and _norm(**(side | dict(sum=G + 400 - 32)))
+    assert _norm(**(side | dict(out=G + 128 + 512)))                        # the residual's columns, a row further
+    assert not _norm(**(side | dict(out=G + 256 + 512)))                    # its own columns, a row further
+    # rows of another stride inside one another: even rows of the array and all rows of its other half
+    assert not _norm(x=G, x_stride=256, out=G + 128, out_stride=128)
+    assert _norm(x=G, x_stride=256, out=G + 128, out_stride=64)
+    # a residual of one row for all, beside the output
+    assert not _norm(residual=7 * G, residual_stride=0, out=7 * G + ROW)
+    assert _norm(residual=7 * G + ROW, residual_stride=0, out=7 * G)
+    # one row: its stride means nothing
+    assert not _norm(rows=1, x=G, out=G, x_stride=72) and _norm(rows=1, x=G, out=G + 16)
+
+
+def test_norm_8_bit_outputs_on_other_arrays():
+    codes, scales = 5 * 128, 5 * 4                                          # bytes: rows of 64 are padded to 128
+    eight = dict(out_type=1, width=64)
+    assert not _norm(**eight)
+    for name, size in (("x", 5 * ROW), ("residual", 5 * ROW), ("sum", 5 * ROW), ("weight", ROW)):
+        for by in (-codes + 16, 0, 16, size - 16):
+            assert _norm(**eight, out=FAR[name] + by), (name, by)
+        for by in (-scales + 4, 0, 4, size - 4):
+            assert _norm(**eight, out_scales=FAR[name] + by), (name, by)
+        assert not _norm(**eight, out=FAR[name] - codes) and not _norm(**eight, out=FAR[name] + size)
+        assert not _norm(**eight, out_scales=FAR[name] - scales) and not _norm(**eight, out_scales=FAR[name] + size)
+    for by in (-scales + 4, 0, codes - 4):
+        assert _norm(**eight, out_scales=FAR["out"] + by)
+    assert not _norm(**eight, out_scales=FAR["out"] + codes)
+    # codes between the rows of a strided x
+    assert not _norm(**eight, rows=1, x_stride=1024, out=G + ROW) and not _norm(**eight, x_stride=1024, out=G + ROW)
+
+
+def test_norm_of_the_most_rows_is_checked_at_once():
+    """Strides and counts at their limits, unlike strides inside one another."""
+    most = dict(rows=1 << 24, width=1 << 20, x_stride=(1 << 40) - 8, out_stride=(1 << 40) - 16, residual=0, sum=0)
+    _norm(**most)
+    _norm(**(most | dict(x_stride=1 << 21, out_stride=(1 << 21) + 8, out=G + (1 << 21))))
+    assert _norm(**(most | dict(x_stride=1 << 20, out_stride=1 << 20, out=G + 16)))

@@ -1,0 +1,56 @@
+"""Overlapping outputs are refused before anything is written; views of one array side
+by side give the bits of separate arrays."""
+
+import pytest
+
+from mixed_precision_bf16_amd import fp4gemm as F
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gfx950():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    name = torch.cuda.get_device_properties(0).gcnArchName
+    if not name.startswith("gfx950"):
+        pytest.skip(f"needs gfx950, found {name}")
+    F.lib()
+    yield
+
+
+def _randn(*shape, seed=0):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(BF16)
+
+
+def _rejects(call, *unchanged):
+    before = [t.clone() for t in unchanged]
+    with pytest.raises(F.Fp4Error) as e:
+        call()
+    assert e.value.status == 2
+    torch.cuda.synchronize()
+    assert all(a.view(torch.uint8).equal(b.view(torch.uint8)) for a, b in zip(before, unchanged))
+
+
+@pytest.mark.parametrize("width", [512, 40960])
+def test_norm(width):
+    rows = 9
+    x, r, w = _randn(rows + 1, width), _randn(rows + 1, width, seed=1), _randn(width, seed=2)
+    _rejects(lambda: F.rms_norm(x[1:], w, out=x[:-1]), x)
+    _rejects(lambda: F.rms_norm(x[:-1], w, residual=r[:-1], sum_out=r[1:]), x, r)
+    _rejects(lambda: F.rms_norm(x[:-1], x[3], out=x[:-1]), x)
+    want, total = F.rms_norm(x[:-1], w, residual=r[:-1])
+    side = torch.zeros((rows, 4 * width), dtype=BF16, device="cuda")        # x, residual, out and sum, column by column
+    part = side.split(width, 1)
+    part[0].copy_(x[:-1])
+    part[1].copy_(r[:-1])
+    F.rms_norm(part[0], w, residual=part[1], out=part[2], sum_out=part[3])
+    assert part[2].equal(want) and part[3].equal(total) and part[0].equal(x[:-1]) and part[1].equal(r[:-1])
+    _rejects(lambda: F.rms_norm(part[0], w, residual=part[1], out=side[:, 2 * width - 8:3 * width - 8]), side)
+    eight = F.new_mx8(rows, width)
+    _rejects(lambda: F.rms_norm(eight.codes.view(BF16).view(-1)[:width].view(1, width).expand(rows, width), mx8=True, out=eight),
+             eight.codes)
