@@ -446,7 +446,8 @@ int fp4_mx8_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_by
 
 /* BF16 (act_type 0) or FP16 (1) rows to 8 bits on `stream`: element k of row i at
  * i * x_stride + k; x 16-byte aligned, x_stride >= 0, below 2^40 and a multiple
- * of 8; codes and scales do not overlap it.  rows == 0 is a no-op. */
+ * of 8; codes, scales and x lie apart, to the byte (else FP4_ERR_SHAPE).  rows == 0 is a
+ * no-op. */
 int fp4_quantize_mx8(const void* x, int64_t rows, int64_t K, int64_t x_stride, int act_type, void* codes,
                      void* scales, void* stream);
 

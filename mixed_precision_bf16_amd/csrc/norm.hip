@@ -265,7 +265,10 @@ static int quantize_mx8_impl(const void* x, int64_t rows, int64_t K, int64_t x_s
     if (rows < 0 || rows > (int64_t(1) << 24) || K < 32 || K > (int64_t(1) << 20) || K % 32) return FP4_ERR_SHAPE;
     if (rows == 0) return FP4_OK;
     if (!x || !codes || !scales) return FP4_ERR_NULL;
-    if (!matrix_ok(x, x_stride) || !mx8_out_ok(codes, scales) || codes == x) return FP4_ERR_SHAPE;
+    if (!matrix_ok(x, x_stride) || !mx8_out_ok(codes, scales)) return FP4_ERR_SHAPE;
+    const Span from = span_of_rows(x, K, rows, x_stride);
+    const Span to = span_of(codes, rows * mx8_padded(K)), powers = span_of(scales, rows * mx8_padded(K) / 32);
+    if (spans_meet(to, powers) || spans_meet(to, from) || spans_meet(powers, from)) return FP4_ERR_SHAPE;
     int st = check_device();
     if (st != FP4_OK) return st;
     NormArgs a{};

@@ -96,3 +96,25 @@ def test_norm_of_the_most_rows_is_checked_at_once():
     _norm(**most)
     _norm(**(most | dict(x_stride=1 << 21, out_stride=(1 << 21) + 8, out=G + (1 << 21))))
     assert _norm(**(most | dict(x_stride=1 << 20, out_stride=1 << 20, out=G + 16)))
+
+
+# ------------------------------------------------------------------- quantizer
+def _quantize(x=G, rows=5, K=64, stride=64, codes=2 * G, scales=3 * G):
+    return _refused(F.lib().fp4_quantize_mx8(x, rows, K, stride, 0, codes, scales, None))
+
+
+def test_quantizer_outputs_on_other_arrays():
+    n_codes, n_scales = 5 * 128, 5 * 4                                      # bytes: rows of 64 are padded to 128
+    assert not _quantize()
+    for by in (-n_codes + 16, 0, 16, 5 * ROW - 16):
+        assert _quantize(codes=G + by), by
+    for by in (-n_scales + 4, 0, 4, 5 * ROW - 4):
+        assert _quantize(scales=G + by), by
+    for by in (-n_scales + 4, 0, n_codes - 4):
+        assert _quantize(scales=2 * G + by), by
+    for by in (-n_codes, 5 * ROW):
+        assert not _quantize(codes=G + by), by
+    assert not _quantize(scales=2 * G + n_codes) and not _quantize(scales=G - n_scales)
+    # in the gaps between x's rows
+    assert not _quantize(stride=1024, codes=G + ROW) and not _quantize(stride=1024, scales=G + 4 * 2048 - 32)
+    assert _quantize(stride=320, codes=G + ROW) and _quantize(stride=1024, scales=G + 4 * 2048 - 16)

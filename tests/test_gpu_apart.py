@@ -54,3 +54,13 @@ def test_norm(width):
     eight = F.new_mx8(rows, width)
     _rejects(lambda: F.rms_norm(eight.codes.view(BF16).view(-1)[:width].view(1, width).expand(rows, width), mx8=True, out=eight),
              eight.codes)
+
+
+def test_quantizer():
+    x = _randn(6, 512)
+    codes = x.view(torch.uint8).view(-1)[512:512 + 4 * 512].view(4, 512).view(torch.float8_e4m3fn)
+    out = F.MX8(codes, torch.zeros((4, 16), dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu), 512)
+    _rejects(lambda: F.quantize_mx8(x[:4], out=out), x)
+    got, want = F.quantize_mx8(x[4:], out=F.MX8(codes[:2], out.scales[:2], 512)), F.quantize_mx8(x[4:].clone())
+    assert got.codes.view(torch.uint8).equal(want.codes.view(torch.uint8))
+    assert got.scales.view(torch.uint8).equal(want.scales.view(torch.uint8))
