@@ -540,9 +540,10 @@ typedef struct fp4_rope_args {
 
 /* out = x turned, on `stream`: element e of head h of token t at t *
  * token_stride + h * head_stride + e; BF16 (act_type 0) or FP16 (1).  out may be
- * x (same strides), else they do not overlap; its rows are apart.  head_dim a
- * multiple of 8, 8 .. 1024; heads <= 65536, tokens <= 2^24; alignment and strides
- * as fp4_kv_append.  tokens == 0 or heads == 0 is a no-op. */
+ * x (same strides), else they lie apart, to the byte (views of one array side by
+ * side do; else FP4_ERR_SHAPE), as out does from positions and frequencies; its rows are
+ * apart.  head_dim a multiple of 8, 8 .. 1024; heads <= 65536, tokens <= 2^24; alignment
+ * and strides as fp4_kv_append.  tokens == 0 or heads == 0 is a no-op. */
 int fp4_rope(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens, int64_t heads, int64_t head_dim,
              int64_t x_token_stride, int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride,
              int act_type, void* stream);

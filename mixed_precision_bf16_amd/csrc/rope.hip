@@ -1,5 +1,6 @@
 // Rotary positions (include/fp4gemm.h, section "Rotary positions"): alone, and
 // with the write of the rotated keys into the FP4 cache.
+#include "apart.h"
 #include "kv_layout.h"
 #include "mx8.h"
 
@@ -349,6 +350,13 @@ static void rope_t(int kind, const RopeArgs& r, const Rows& x, const RowsOut& y,
     else rope_kernel<ACT, kHalves, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
 }
 
+// Whether the turned rows `to`, which may be the rows `from`, lie apart from them, and from
+// the positions and frequencies.
+static bool turned_apart(const Span& to, const Span& from, const RopeArgs& r, int64_t tokens) {
+    return span_may_be(to, from) && !spans_meet(to, span_of(r.positions, tokens * 8)) &&
+           !spans_meet(to, span_of(r.frequencies, (int64_t)r.pairs * 4));
+}
+
 // Whether rows `to` begin elsewhere than rows `from`, or lie on them one by one.
 static bool apart_or_same(const void* to, int64_t to_ts, int64_t to_hs, const void* from, int64_t ts, int64_t hs,
                           int64_t tokens, int64_t heads) {
@@ -368,7 +376,8 @@ static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_
     st = rope_pointers(r);
     if (st != FP4_OK) return st;
     if (!rows_ok(x, x_ts, x_hs) || !rows_ok(out, out_ts, out_hs) || !rows_apart(tokens, heads, head_dim, out_ts, out_hs) ||
-        !apart_or_same(out, out_ts, out_hs, x, x_ts, x_hs, tokens, heads))
+        !turned_apart(span_of_rows(out, head_dim, tokens, out_ts, heads, out_hs),
+                      span_of_rows(x, head_dim, tokens, x_ts, heads, x_hs), r, tokens))
         return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;

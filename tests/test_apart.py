@@ -118,3 +118,31 @@ def test_quantizer_outputs_on_other_arrays():
     # in the gaps between x's rows
     assert not _quantize(stride=1024, codes=G + ROW) and not _quantize(stride=1024, scales=G + 4 * 2048 - 32)
     assert _quantize(stride=320, codes=G + ROW) and _quantize(stride=1024, scales=G + 4 * 2048 - 16)
+
+
+# -------------------------------------------------------------------- rotation
+def _rope(x=G, out=2 * G, tokens=3, heads=4, dim=64, xt=256, xh=64, ot=256, oh=64, positions=3 * G, frequencies=4 * G):
+    r = F._PACK_ROPE.pack(positions, frequencies, 64, 1.0, 0)
+    return _refused(F.lib().fp4_rope(r, x, out, tokens, heads, dim, xt, xh, ot, oh, 0, None))
+
+
+def test_rotated_rows_on_other_arrays():
+    token = 512                                                             # bytes of four heads
+    assert not _rope() and not _rope(out=G)
+    for by in (16, -16, 128, -128, token, -token, 3 * token - 16, 16 - 3 * token):
+        assert _rope(out=G + by), by
+    for by in (3 * token, -3 * token):
+        assert not _rope(out=G + by), by
+    # x and out side by side in one array of 12 heads; shifted by a head they meet
+    side = dict(xt=768, ot=768)
+    assert not _rope(out=G + token, **side) and not _rope(out=G + 1024, **side)
+    assert _rope(out=G + token - 128, **side) and _rope(out=G + 1536 - 128, **side) and _rope(out=G + 128, **side)
+    # head-major output of a token-major x: apart, inside it, and on its last element
+    assert not _rope(ot=64, oh=192) and _rope(out=G, ot=64, oh=192) and _rope(out=G + 3 * token - 16, ot=64, oh=192)
+    # one head, one token: their strides mean nothing
+    assert not _rope(out=G, heads=1, xh=64, oh=72) and not _rope(out=G, tokens=1, xt=256, ot=512)
+    # one row for all: outside it and on it
+    assert not _rope(x=G, xt=0, xh=0, out=G + 128) and _rope(x=G + 128, xt=0, xh=0, out=G)
+    for by in (-3 * token + 16, -16, 0, 16):
+        assert _rope(out=3 * G + by) and _rope(out=4 * G + by), by
+    assert _rope(out=4 * G + 112) and not _rope(out=4 * G + 128) and not _rope(out=3 * G + 32)

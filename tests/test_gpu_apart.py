@@ -64,3 +64,19 @@ def test_quantizer():
     got, want = F.quantize_mx8(x[4:], out=F.MX8(codes[:2], out.scales[:2], 512)), F.quantize_mx8(x[4:].clone())
     assert got.codes.view(torch.uint8).equal(want.codes.view(torch.uint8))
     assert got.scales.view(torch.uint8).equal(want.scales.view(torch.uint8))
+
+
+def test_rotation():
+    n, heads, dim = 37, 5, 64
+    both = _randn(n, 3 * heads, dim)
+    pos, (freq, _) = torch.arange(n, device="cuda"), F.rope_frequencies(dim)
+    x = both[:, :heads]
+    want = F.rope(x.clone(), pos, freq)
+    _rejects(lambda: F.rope(x, pos, freq, out=both[:, 1:heads + 1]), both)
+    _rejects(lambda: F.rope(x[1:], pos[1:], freq, out=x[:-1]), both)
+    _rejects(lambda: F.rope(both[:, heads - 1:2 * heads - 1], pos, freq, out=x), both)
+    rest = both[:, 2 * heads:].clone()
+    F.rope(x, pos, freq, out=both[:, heads:2 * heads])                      # beside it in the same array
+    assert both[:, heads:2 * heads].equal(want) and both[:, 2 * heads:].equal(rest)
+    F.rope(x, pos, freq, out=x)
+    assert x.equal(want)
