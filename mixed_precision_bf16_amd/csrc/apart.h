@@ -9,17 +9,23 @@ namespace fp4 {
 
 typedef __int128 wide_t;  // counts times strides pass 64 bits where the arguments make no sense
 
-// The bytes p + i * stride[0] + j * stride[1] + [0, width), i < count[0], j < count[1].
+// The bytes p + i * stride[0] + j * stride[1] + [0, width), i < count[0], j < count[1],
+// all of them below `end`.
 struct Span {
-    uintptr_t p;
+    uintptr_t p, end;
     int64_t width, count[2], stride[2];
 };
 
-inline Span span_of(const void* p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes, {1, 1}, {0, 0}}; }
+inline Span span_of(const void* p, int64_t width, int64_t n0 = 1, int64_t s0 = 0, int64_t n1 = 1, int64_t s1 = 0) {
+    Span s{reinterpret_cast<uintptr_t>(p), 0, width, {n0, n1}, {s0, s1}};
+    const wide_t end = (wide_t)s.p + (wide_t)(n0 - 1) * s0 + (wide_t)(n1 - 1) * s1 + width;
+    s.end = end > (wide_t)UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end;
+    return s;
+}
 
 // 16-bit rows: strides in elements.
 inline Span span_of_rows(const void* p, int64_t width, int64_t rows, int64_t stride, int64_t heads = 1, int64_t hs = 0) {
-    return {reinterpret_cast<uintptr_t>(p), width * 2, {rows, heads}, {stride * 2, hs * 2}};
+    return span_of(p, width * 2, rows, stride * 2, heads, hs * 2);
 }
 
 // The same elements under the same indices.
@@ -60,7 +66,7 @@ inline bool steps_reach(const SpanSteps* s, int n, wide_t from, wide_t to, int& 
 // Whether two spans share a byte.  A search of more than 2^16 counts (arrays of unlike
 // strides and many rows inside one another) ends as if they shared none.
 inline bool spans_meet(const Span& a, const Span& b) {
-    if (!a.p || !b.p) return false;
+    if (!a.p || !b.p || a.end <= b.p || b.end <= a.p) return false;
     SpanSteps s[4];
     int n = 0;
     wide_t width[2] = {a.width, b.width};
