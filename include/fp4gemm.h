@@ -549,10 +549,12 @@ int fp4_rope(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens
              int act_type, void* stream);
 
 /* fp4_rope of queries and keys and fp4_kv_append of the turned keys and the
- * values in one launch: the same bits as those calls one after another. */
+ * values in one launch: the same bits as those calls one after another.  What is
+ * written (q_out, the cache) lies apart from all other arrays, to the byte (queries,
+ * keys and values side by side in one array do; else FP4_ERR_SHAPE). */
 typedef struct fp4_append_rope_args {
     const void* q;        /* device [tokens][q_heads][head_dim]; NULL with q_heads == 0 */
-    void* q_out;          /* may be q, with q's strides; else overlaps none of q, k, v */
+    void* q_out;          /* may be q, with q's strides; else apart from it; apart from all else of the call */
     const void* k;        /* device [tokens][kv_heads][head_dim]; not written */
     const void* v;
     const int64_t* slots; /* device [tokens], none twice; outside the cache: key and value skipped, queries turned all the same */

@@ -350,19 +350,6 @@ static void rope_t(int kind, const RopeArgs& r, const Rows& x, const RowsOut& y,
     else rope_kernel<ACT, kHalves, false><<<grid, block, lds, s>>>(r, x, y, tokens, heads, head_dim);
 }
 
-// Whether the turned rows `to`, which may be the rows `from`, lie apart from them, and from
-// the positions and frequencies.
-static bool turned_apart(const Span& to, const Span& from, const RopeArgs& r, int64_t tokens) {
-    return span_may_be(to, from) && !spans_meet(to, span_of(r.positions, tokens * 8)) &&
-           !spans_meet(to, span_of(r.frequencies, (int64_t)r.pairs * 4));
-}
-
-// Whether rows `to` begin elsewhere than rows `from`, or lie on them one by one.
-static bool apart_or_same(const void* to, int64_t to_ts, int64_t to_hs, const void* from, int64_t ts, int64_t hs,
-                          int64_t tokens, int64_t heads) {
-    return to != from || ((tokens == 1 || to_ts == ts) && (heads == 1 || to_hs == hs));
-}
-
 static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_t tokens, int64_t heads,
                      int64_t head_dim, int64_t x_ts, int64_t x_hs, int64_t out_ts, int64_t out_hs, int act_type,
                      void* stream) {
@@ -375,9 +362,11 @@ static int rope_impl(const fp4_rope_args* rope, const void* x, void* out, int64_
     if (!x || !out) return FP4_ERR_NULL;
     st = rope_pointers(r);
     if (st != FP4_OK) return st;
-    if (!rows_ok(x, x_ts, x_hs) || !rows_ok(out, out_ts, out_hs) || !rows_apart(tokens, heads, head_dim, out_ts, out_hs) ||
-        !turned_apart(span_of_rows(out, head_dim, tokens, out_ts, heads, out_hs),
-                      span_of_rows(x, head_dim, tokens, x_ts, heads, x_hs), r, tokens))
+    if (!rows_ok(x, x_ts, x_hs) || !rows_ok(out, out_ts, out_hs) || !rows_apart(tokens, heads, head_dim, out_ts, out_hs))
+        return FP4_ERR_SHAPE;
+    const Span to = span_of_rows(out, head_dim, tokens, out_ts, heads, out_hs);
+    if (!span_may_be(to, span_of_rows(x, head_dim, tokens, x_ts, heads, x_hs)) ||
+        spans_meet(to, span_of(r.positions, tokens * 8)) || spans_meet(to, span_of(r.frequencies, (int64_t)r.pairs * 4)))
         return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;
@@ -444,11 +433,21 @@ static int append_rope_impl(const fp4_kv_cache* cache, const fp4_rope_args* rope
         return FP4_ERR_SHAPE;
     if (p->q_heads && (!rows_ok(p->q, p->q_token_stride, p->q_head_stride) ||
                        !rows_ok(p->q_out, p->q_out_token_stride, p->q_out_head_stride) ||
-                       !rows_apart(p->tokens, p->q_heads, cache->head_dim, p->q_out_token_stride, p->q_out_head_stride) ||
-                       p->q_out == p->k || p->q_out == p->v ||
-                       !apart_or_same(p->q_out, p->q_out_token_stride, p->q_out_head_stride, p->q, p->q_token_stride,
-                                      p->q_head_stride, p->tokens, p->q_heads)))
+                       !rows_apart(p->tokens, p->q_heads, cache->head_dim, p->q_out_token_stride, p->q_out_head_stride)))
         return FP4_ERR_SHAPE;
+    // what is written (queries, cache) lies apart from all else of the call
+    auto span = [&](const void* x, int64_t ts, int64_t heads, int64_t hs) {
+        return span_of_rows(x, cache->head_dim, p->tokens, ts, heads, hs);
+    };
+    const Span q = span(p->q, p->q_token_stride, p->q_heads, p->q_head_stride);
+    const Span qo = span(p->q_out, p->q_out_token_stride, p->q_heads, p->q_out_head_stride);
+    const Span held = span_of(a.c.data, (int64_t)a.c.pages * a.c.tiles_per_page * a.c.kv_heads *
+                                            kv_tile_bytes(cache->format, cache->head_dim));
+    if (!span_may_be(qo, q) || spans_meet(qo, held) || spans_meet(held, q)) return FP4_ERR_SHAPE;
+    for (const Span& from : {span(p->k, p->k_token_stride, a.c.kv_heads, p->k_head_stride),
+                             span(p->v, p->v_token_stride, a.c.kv_heads, p->v_head_stride), span_of(p->slots, p->tokens * 8),
+                             span_of(a.r.positions, p->tokens * 8), span_of(a.r.frequencies, (int64_t)a.r.pairs * 4)})
+        if (spans_meet(qo, from) || spans_meet(held, from)) return FP4_ERR_SHAPE;
     st = check_device();
     if (st != FP4_OK) return st;
     a.q_heads = (int)p->q_heads;

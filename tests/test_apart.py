@@ -146,3 +146,36 @@ def test_rotated_rows_on_other_arrays():
     for by in (-3 * token + 16, -16, 0, 16):
         assert _rope(out=3 * G + by) and _rope(out=4 * G + by), by
     assert _rope(out=4 * G + 112) and not _rope(out=4 * G + 128) and not _rope(out=3 * G + 32)
+
+
+def _append(data=G, **over):
+    c = F._KVCacheDesc(data=data, pages=2, page_size=32, kv_heads=2, head_dim=64, format=0, k_alpha=1.0, v_alpha=1.0)
+    f = dict(q=2 * G, q_out=3 * G, k=4 * G, v=5 * G, slots=6 * G, tokens=3, q_heads=4, qt=256, qh=64, ot=256, oh=64,
+             kt=128, kh=64, vt=128, vh=64, act=0, positions=7 * G, frequencies=8 * G) | over
+    r = F._PACK_ROPE.pack(f.pop("positions"), f.pop("frequencies"), 64, 1.0, 0)
+    return _refused(F.lib().fp4_kv_append_rope(ctypes.byref(c), r, F._PACK_APPEND_ROPE.pack(*f.values()), None))
+
+
+def test_rotated_queries_and_the_cache_on_other_arrays():
+    n_q, n_k = 3 * 512, 3 * 256                                             # bytes of the queries, of the keys
+    size = F.kv_cache_size(2, 32, 2, 64, 0)
+    assert not _append() and not _append(q_out=2 * G) and not _append(q=0, q_out=0, q_heads=0)
+    for by in (16, -16, 512, n_q - 16, 16 - n_q):
+        assert _append(q_out=2 * G + by), by
+    assert not _append(q_out=2 * G + n_q) and not _append(q_out=2 * G - n_q)
+    for other, last in ((4 * G, n_k), (5 * G, n_k), (G, size), (6 * G, 16), (7 * G, 16), (8 * G, 128)):
+        for by in (16 - n_q, 0, last - 16):
+            assert _append(q_out=other + by), (other // G, by)
+        assert not _append(q_out=other - n_q) and not _append(q_out=other + (last + 31) // 16 * 16)
+    for other, last in ((2 * G, n_q), (4 * G, n_k), (5 * G, n_k), (6 * G, 16), (7 * G, 16), (8 * G, 112)):
+        for by in (16 - size, 0, last - 16):
+            assert _append(data=other + by), (other // G, by)
+        assert not _append(data=other - size) and not _append(data=other + n_q)
+    # queries, keys and values side by side in the rows of one projection; in place; shifted by a head
+    rows = dict(q=2 * G, k=2 * G + 512, v=2 * G + 768, qt=512, kt=512, vt=512)
+    assert not _append(**rows) and not _append(**rows, q_out=2 * G, ot=512)
+    for by in (128, -128, 1024 + 128):
+        assert _append(**rows, q_out=2 * G + by, ot=512), by
+    assert not _append(**rows, q_out=2 * G + 3 * 1024)
+    # head-major keys that begin behind the queries
+    assert not _append(k=2 * G + n_q, kt=64, kh=192, q_out=2 * G) and _append(k=2 * G + n_q - 128, kt=64, kh=192, q_out=2 * G)

@@ -80,3 +80,21 @@ def test_rotation():
     assert both[:, heads:2 * heads].equal(want) and both[:, 2 * heads:].equal(rest)
     F.rope(x, pos, freq, out=x)
     assert x.equal(want)
+
+
+def test_rotation_with_the_cache():
+    n, qh, h, dim, page = 37, 4, 2, 64, 32
+    qkv = _randn(n + 1, qh + 2 * h, dim)
+    pos, (freq, _) = torch.arange(n, device="cuda"), F.rope_frequencies(dim)
+    slots = torch.randperm(5 * page, generator=torch.Generator().manual_seed(1))[:n].cuda()
+    cache, other = F.new_kv_cache(5, page, h, dim, 0), F.new_kv_cache(5, page, h, dim, 0)
+    cache.data.zero_(), other.data.zero_()
+    q, k, v = qkv[:n].split([qh, h, h], 1)
+    want = F.kv_append_rope(other, q.clone(), k.clone(), v.clone(), slots, pos, freq)
+    for out in (qkv[:n, 1:qh + 1], qkv[:n, qh:], qkv[1:, :qh]):
+        _rejects(lambda: F.kv_append_rope(cache, q, k, v, slots, pos, freq, q_out=out), qkv, cache.data)
+    room = cache.data[:n * qh * dim * 2].view(BF16).view(n, qh, dim)
+    _rejects(lambda: F.kv_append_rope(cache, q, k, v, slots, pos, freq, q_out=room), qkv, cache.data)
+    _rejects(lambda: F.kv_append_rope(cache, room, k, v, slots, pos, freq), qkv, cache.data)
+    F.kv_append_rope(cache, q, k, v, slots, pos, freq, q_out=q)
+    assert q.equal(want) and cache.data.equal(other.data)
