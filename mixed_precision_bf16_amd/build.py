@@ -24,7 +24,7 @@ SOURCES = ["repack.cpp", "fp4gemm.hip", "decode_bf16.hip", "decode_f16.hip", "pr
            "moe_bf16.hip", "kv_cache.hip", "attention.hip", "attention_nv_bf16.hip", "attention_nv_f16.hip",
            "attention_mx_bf16.hip", "attention_mx_f16.hip", "norm.hip", "rope.hip", "gemm_mx8.hip"]
 HEADERS = ["layout.h", "kernels.h", "dispatch.h", "decode_inst.inc", "prefill_inst.inc", "kv_layout.h",
-           "attention.h", "attention_inst.inc", "apart.h", "mx8.h", "gemm_mx8.h",
+           "attention.h", "attention_inst.inc", "apart.h", "mx8.h", "mx8_plan.h", "gemm_mx8.h",
            os.path.join("..", "..", "include", "fp4gemm.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

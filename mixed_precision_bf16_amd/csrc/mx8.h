@@ -5,12 +5,9 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "mx8_plan.h"
 
 namespace fp4 {
-
-constexpr int64_t kMx8PadK = 128;  // rows are padded to whole matrix-core steps
-
-inline int64_t mx8_padded(int64_t K) { return (K + kMx8PadK - 1) / kMx8PadK * kMx8PadK; }
 
 // Scale byte of a block whose largest finite magnitude is amax (FP32 bits): the
 // least power of two with amax / 2^(byte - 127) <= 448 = 1.75 * 2^8.
