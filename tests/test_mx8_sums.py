@@ -68,3 +68,13 @@ def test_size_of_the_cut():
     size = np.sqrt((y * y).mean())
     assert 3e-6 < np.sqrt((off * off).mean()) / size < 6e-6
     assert 4e-8 < (np.abs(off) / total).mean() < 9e-8
+
+
+def test_the_largest_elements_are_rounded_to_two_to_128():
+    """E4M3 has steps of 16 in 128 .. 256: from 248 scales on, 256 scales."""
+    x = np.zeros((2, 32))
+    x[0, 3], x[1, 3] = 248.0 * 2.0 ** 120, 247.0 * 2.0 ** 120
+    v = oracle.mx8_value(*oracle.mx8_quantize_reference(x), 32)
+    assert v[0, 3] == 2.0 ** 128 and v[1, 3] == 240.0 * 2.0 ** 120
+    largest = np.array([[np.finfo(np.float32).max] + [0.0] * 31])
+    assert oracle.mx8_value(*oracle.mx8_quantize_reference(largest), 32)[0, 0] == 2.0 ** 128
