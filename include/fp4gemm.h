@@ -456,7 +456,9 @@ int fp4_quantize_mx8(const void* x, int64_t rows, int64_t K, int64_t x_stride, i
  *   out = h / sqrt(mean(h^2) + eps) * weight
  * The norm is taken of the unrounded h.  The squares are summed in FP64; the
  * root, its product with h and that with the weight are each rounded to FP32,
- * then the result to its type: the same bits whatever the kernel. */
+ * then the result to its type: the same bits whatever the kernel, but where the root
+ * lies so close to a border between FP32 values that the order of the sum decides
+ * (about one row in 2^28). */
 typedef struct fp4_rms_norm_args {
     const void* x;        /* device, BF16 or FP16 [rows][width], strided */
     const void* residual; /* the same, or NULL: h = x */

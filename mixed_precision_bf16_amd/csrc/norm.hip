@@ -52,10 +52,11 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // y = h * root * weight with h = x + residual (FP32), root = 1 / sqrt(mean(h^2) +
-// eps).  The squares are summed in FP64, so that neither their order nor their
-// size matters (BF16 values reach 1e38), and root, h * root and its product with
-// the weight are each rounded to FP32 once: every result is the same on any
-// split of the row.
+// eps).  The squares, exact in FP64, are summed there, so that their size does not
+// matter (BF16 values reach 1e38) and their order hardly does, and root, h * root and its
+// product with the weight are each rounded to FP32 once: a result is the same on any
+// split of the row unless the root lies within some 2^-52 of a border between FP32 values,
+// about once in 2^28 rows.
 // A team of T threads holds a row of up to 8 T V elements in registers and
 // reads it once.  Bound by the bytes: 4095 x 8192 (BF16, a residual, 8-bit output;
 // 236 MB) takes 42.5 us, 5.5 TB/s, with 512 threads a row and the nontemporal hint on
