@@ -234,8 +234,11 @@ __device__ __forceinline__ void turned_block(const uint16_t* x, int d0, const Ro
 
 // A workgroup takes kRopeTile tokens and the heads of its share (blockIdx.y).  Bound by
 // the bytes where tokens are many: 64 heads of 128 of 8191 tokens take 51.5 us, 5.2 TB/s;
-// by the table in FP64 and one round of workgroups where they are few (1001 tokens of 72
-// heads of 64 in FP16: 8.2 us).
+// where they are few by what one workgroup does in turn: positions and frequencies from
+// memory, the table in FP64, a barrier, and only then the first rows (1001 tokens of 36
+// heads of 128 in FP16, 64 elements of each turned in pairs: 8.2 us, bytes for 3.5).
+// Halves at any distance move single elements: 8191 tokens of 40 heads of 80 take 84 us
+// with 20 elements turned, 29 with 32.
 template <int ACT, int KIND, bool kFar>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs r, Rows x, RowsOut y, int tokens, int heads,
                                                    int head_dim) {
@@ -249,7 +252,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs r, Rows x, RowsOut y
 }
 
 // The bytes again, and the scattered stores of the values' codes: 8191 tokens of 64 + 8
-// heads of 128 take 65 us, 1 token 6.6.
+// heads of 128 take 65 us; 1 token takes 6.5, the latencies of rope_kernel in turn and
+// the slot's behind the table.
 // Shares of blockIdx.y: first the KV heads' (kv_parts; their scattered stores take
 // longest), then the query heads'.  The 4 GP threads of four tokens and one head lie
 // together (kv_append_kernel).

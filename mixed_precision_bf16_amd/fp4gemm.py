@@ -823,7 +823,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
     multiple of 8 (with mx8: 32).  Returns y, of x's type or (mx8) an MX8; with a
     residual (y, h), h rounded to x's type: the next layer's residual.  out and
     sum_out are filled if given; sum_out may be x or residual, and out (16-bit)
-    the other one."""
+    the other one; else they share no byte with another array of the call."""
     import torch
     dtype, dev = x.dtype, x.device
     act = _act_type(dtype, "x")
@@ -896,7 +896,8 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
     "silu" or "gelu": act(G) * U of the products G and U with the first and the
     second half of the weight's rows, N / 2 columns.  Returns (or fills) a
     tensor [m][columns] of `dtype` (bfloat16 by default, or float16) or, with
-    mx8, an MX8."""
+    mx8, an MX8.  Up to 16 rows the sums are FP32's; with more the matrix cores cut
+    the low bits of small products off first (include/fp4gemm.h)."""
     import torch
     g = _GATES.get(gate)
     if g is None or not isinstance(a, MX8):
@@ -959,7 +960,10 @@ def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str | None = N
       bands   by the turns n = original f / 2 pi that a pair makes in the original
               context: n > high kept, n < low as linear, between them blended by n
       yarn    the same blend by pair number, between the pairs that make `fast`
-              and `slow` turns; amplitude 1 + 0.1 ln factor"""
+              and `slow` turns; amplitude 1 + 0.1 ln factor.  The rounding of the
+              pair numbers, their bounds and the least spread of 1e-3 are those of the
+              published scaling (Peng et al., "YaRN: Efficient Context Window Extension
+              of Large Language Models", 2023), which checkpoints rely on"""
     import math
 
     import torch
@@ -1005,7 +1009,8 @@ def rope(x, positions, frequencies, interleaved: bool = False, amplitude: float 
     and head strides that are multiples of 8) turned by its positions (int64
     CUDA [tokens]).  frequencies: float32 CUDA [rotary / 2] (rope_frequencies);
     the first `rotary` elements of a head are turned, in halves or, interleaved,
-    in neighbouring pairs.  Returns (or fills) out, which may be x."""
+    in neighbouring pairs.  Returns (or fills) out, which may be x, else shares
+    no byte with another array of the call."""
     import torch
     act = _act_type(x.dtype, "x")
     if x.dim() != 3 or not x.is_cuda:
@@ -1038,7 +1043,8 @@ def kv_append_rope(cache: KVCache, q, k, v, slots, positions, frequencies, inter
     the values, in one launch.  q: [tokens][q_heads][head_dim]; k, v:
     [tokens][kv_heads][head_dim] (not written); slots, positions: int64 CUDA
     [tokens], no slot twice.  Returns (or fills) q_out, which may be q.  A token
-    whose slot is outside the cache is turned but not written."""
+    whose slot is outside the cache is turned but not written.  q_out and the cache
+    share no byte with another array of the call."""
     import torch
     act = _act_type(k.dtype, "k")
     dev, dim = cache._data.device, cache._head_dim
