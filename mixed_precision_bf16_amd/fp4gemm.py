@@ -784,6 +784,11 @@ def _mx8_out(out, rows: int, K: int, device):
     return out
 
 
+def _refuse_mx8(out):
+    if isinstance(out, MX8):
+        raise ValueError("an MX8 out goes with mx8=True")
+
+
 def _pack(packer, what: str, *fields) -> bytes:
     try:
         return packer.pack(*fields)
@@ -854,6 +859,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, mx8: bool = False
             if out is None:
                 made.append(out := torch.empty(rows, width, dtype=dtype, device=dev))
             else:
+                _refuse_mx8(out)
                 os = _matrix(out, "out", rows, width, dtype, dev)
             to = out.data_ptr()
         if residual is not None:
@@ -907,6 +913,7 @@ def gemm_mx8(a: MX8, wq, sq, N: int, gate: str | None = None, alpha: float = 1.0
             raise ValueError("dtype does not go with mx8")
         kind = 2
     else:
+        _refuse_mx8(out)
         if dtype is None:
             dtype = out.dtype if out is not None else torch.bfloat16
         kind = _act_type(dtype, "dtype")

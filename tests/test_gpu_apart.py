@@ -1,4 +1,4 @@
-"""Overlapping outputs are refused before anything is written; views of one array side
+"""Overlapping outputs, and outputs of the other kind, are refused before anything is written; views of one array side
 by side give the bits of separate arrays."""
 
 import pytest
@@ -98,3 +98,13 @@ def test_rotation_with_the_cache():
     _rejects(lambda: F.kv_append_rope(cache, room, k, v, slots, pos, freq), qkv, cache.data)
     F.kv_append_rope(cache, q, k, v, slots, pos, freq, q_out=q)
     assert q.equal(want) and cache.data.equal(other.data)
+
+
+def test_8_bit_rows_as_16_bit_outputs():
+    x = _randn(3, 64)
+    a = F.quantize_mx8(x)
+    W = [torch.zeros(k, dtype=torch.uint8, device="cuda") for k in F.native_repack_size(64, 64)]
+    for call in (lambda: F.rms_norm(x, out=F.new_mx8(3, 64)), lambda: F.gemm_mx8(a, *W, 64, out=F.new_mx8(3, 64)),
+                 lambda: F.gemm_mx8(a, *W, 64, dtype=BF16, out=F.new_mx8(3, 64))):
+        with pytest.raises(ValueError, match="mx8"):
+            call()
