@@ -486,10 +486,11 @@ int fp4_rms_norm(const fp4_rms_norm_args* args, void* stream);
  * 2^128 in 8 bits); for more rows on the scaled 8-bit matrix cores, which cut products off
  * before they add them: of each eight k (8 i .. 8 i + 7) a product loses, toward zero, what
  * lies below 2^(e - 13), e being the largest sum of its two codes' exponents that a
- * nonzero product of the eight has.  A sum loses less than 2^-10 of sum |a w|; Gaussian rows of 8192 lose 4e-6 of the result's
- * size (root mean square; 3 of 1000 BF16 results then round to the neighbour), 1.2e-5 with
- * channels ten times as strong among them.  So a row's bits may differ from one batch to
- * another; who needs FP32 sums of all products gives at most 16 rows a call:
+ * nonzero product of the eight has.  A sum loses less than 2^-10 of sum |a w|; Gaussian
+ * rows of 8192 lose 4e-6 of the result's size (root mean square; 3 of 1000 BF16 results
+ * then round to the neighbour), 1.2e-5 with channels ten times as strong among them.  So a
+ * row's bits may differ from one batch to another; who needs FP32 sums of all products
+ * gives at most 16 rows a call:
  *   gate 0:  Y = alpha * (A . dequant(W)^T), N columns
  *   gate 1:  Y = silu(alpha * G) * (alpha * U), gate 2: gelu(alpha * G) * (alpha * U)
  *            (tanh form), with G and U the products with rows 0 .. N/2 - 1 and
